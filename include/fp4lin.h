@@ -329,6 +329,115 @@ fp4_status fp4_linear_backward(const void *dY, int32_t dy_dtype, int64_t M, int6
                                const float *sW, void *dA, int32_t da_dtype, void *dW,
                                int32_t dw_dtype, void *workspace, size_t ws_bytes, void *stream);
 
+/* ---------------------------------------------------------------------------------------------
+ * FP8 (E4M3) linear layer with a scale per block of 128, beside the FP4 layer: for layers where one
+ * scale per row is too coarse.  Scales are powers of two: e is the smallest integer >= -127 with
+ * max|x| <= 448 * 2^e over the block (-127 for a block of zeros), held as the byte e + 127 (E8M0); codes are the
+ * nearest E4M3 values of x * 2^-e, ties to even, sign kept.  A block that holds a NaN or an infinity
+ * has byte 255 and NaN codes: whatever it touches in a product is NaN.
+ *   FP4_BLOCK_VECTOR: blocks of 1 x 128 along the contraction (activations, gradients)
+ *   FP4_BLOCK_SQUARE: blocks of 128 x 128 (weights; the same values in both operand orders)
+ * An operand is contraction-contiguous.  For a matrix of `rows` rows and contraction length L:
+ *   codes   rows x Lp bytes, Lp = L rounded up to 128, the pad zero
+ *   scales  dwords [(L/128 rounded up) / 4 rounded up][srows], byte kb % 4 of dword
+ *           (kb / 4) * srows + r for block kb of scale row r; srows = rows (VECTOR) or rows / 128
+ *           rounded up (SQUARE, r = row / 128)
+ * Sizes: any from 1 up to 2^23 - 128 a side and 2^34 elements a matrix; row strides (ld, in elements,
+ * >= columns) and input pointers at any element alignment; codes and scales 16-byte aligned; Y, dX and dW dense. */
+enum { FP4_BLOCK_VECTOR = 0, FP4_BLOCK_SQUARE = 1 };
+
+/* Host-only: bytes of an operand's codes and scales (0 if the arguments are invalid). */
+size_t fp4_block8_codes_bytes(int64_t rows, int64_t L);
+size_t fp4_block8_scales_bytes(int64_t rows, int64_t L, int32_t mode);
+
+/* Quantize X (R x C, rows ld apart, fp32 or bf16) to either or both operands:
+ *   row_codes, row_scales: X itself (rows R, contraction C), or both NULL
+ *   col_codes, col_scales: X transposed (rows C, contraction R), or both NULL
+ * For FP4_BLOCK_VECTOR the two have blocks along their own contraction, so different values.
+ * Returns FP4_OK or FP4_ERR_{NULL,SHAPE,DTYPE,ALIGN,DEVICE,HIP}. */
+fp4_status fp4_block8_quantize(const void *X, int32_t x_dtype, int64_t R, int64_t C, int64_t ld, int32_t mode,
+                               uint8_t *row_codes, uint8_t *row_scales, uint8_t *col_codes, uint8_t *col_scales,
+                               void *stream);
+
+/* The values of an operand (rows x L, dense) in y_dtype; exact in both types but for fp32 or bf16
+ * subnormals and blocks whose values pass the type's range. */
+fp4_status fp4_block8_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t rows, int64_t L, int32_t mode,
+                                 void *Y, int32_t y_dtype, void *stream);
+
+/* The product of two operands: Y (M x N, y_dtype) = A . B^T with A of M rows, B of N rows, both of
+ * contraction length K; summed in fp32, rounded once. */
+fp4_status fp4_block8_gemm(const uint8_t *a_codes, const uint8_t *a_scales, int32_t a_mode, const uint8_t *b_codes,
+                           const uint8_t *b_scales, int32_t b_mode, int64_t M, int64_t N, int64_t K, void *Y,
+                           int32_t y_dtype, void *stream);
+
+/* The layer's forward: Y = X . W with X (M x K, rows ldx apart) quantized in vector blocks along K and W
+ * given as the operand of N rows and contraction K (w_mode).
+ *   xt_codes, xt_scales: NULL, or the operand X transposed (rows K, contraction M, vector blocks)
+ *            that the backward needs, made in the same pass over X
+ *   workspace: at least fp4_block8_linear_workspace_bytes(M, K, N) bytes.
+ * Returns FP4_OK or FP4_ERR_{NULL,SHAPE,DTYPE,WORKSPACE,ALIGN,DEVICE,HIP}. */
+size_t fp4_block8_linear_workspace_bytes(int64_t M, int64_t K, int64_t N);
+fp4_status fp4_block8_linear(const void *X, int32_t x_dtype, int64_t M, int64_t K, int64_t ldx, const uint8_t *w_codes,
+                             const uint8_t *w_scales, int32_t w_mode, int64_t N, void *Y, int32_t y_dtype,
+                             uint8_t *xt_codes, uint8_t *xt_scales, void *workspace, size_t ws_bytes, void *stream);
+
+/* The layer's backward, the quantizers' derivative taken as one (as in fp4_linear_backward):
+ *      dX = Q(dY) . W^T   (dY in vector blocks along N; W as the operand of K rows, contraction N)
+ *      dW = X^T . Q(dY)   (both in vector blocks along M; X^T as fp4_block8_linear's xt)
+ * dX (M x K) or dW (K x N) may be NULL (not wanted), and then its operand too.
+ *   workspace: at least fp4_block8_backward_workspace_bytes(M, N) bytes. */
+size_t fp4_block8_backward_workspace_bytes(int64_t M, int64_t N);
+fp4_status fp4_block8_backward(const void *dY, int32_t dy_dtype, int64_t M, int64_t K, int64_t N, int64_t lddy,
+                               const uint8_t *w_codes, const uint8_t *w_scales, int32_t w_mode,
+                               const uint8_t *xt_codes, const uint8_t *xt_scales, void *dX, int32_t dx_dtype, void *dW,
+                               int32_t dw_dtype, void *workspace, size_t ws_bytes, void *stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * 4-bit key/value cache.  `pages` pages of `page` tokens (a power of two, 16 to 1024), hkv heads of
+ * size d (64 or 128).  Each group of 32 values along d is held as E2M1 codes (nearest of x * 2^-e, ties to
+ * even, saturating at 6) and the byte e + 127, e the smallest integer >= -127 with max|x| <= 7 * 2^e.
+ * A token whose key or value holds a NaN or infinity in a head reads back as NaN in that head, and
+ * so do the attention rows that see it.  The caller zeroes the memory once, before the first use.
+ * A slot is a token's place: page index * page + offset in the page. */
+
+/* Host-only: the cache's bytes (0 if the arguments are invalid). */
+size_t fp4_kv4_cache_bytes(int64_t pages, int32_t page, int32_t hkv, int32_t d);
+
+/* Write n tokens: K and V (n x hkv x d, dtype fp32 or bf16, d contiguous, token and head strides in elements,
+ * any element alignment) to slots[i] (slot_bytes 4: int32, 8: int64).  Slots outside the cache are skipped;
+ * of two equal slots in one call, either token may stay. */
+fp4_status fp4_kv4_write(uint8_t *cache, int64_t pages, int32_t page, int32_t hkv, int32_t d, const void *K,
+                         const void *V, int32_t dtype, int64_t n, int64_t k_token_stride, int64_t k_head_stride,
+                         int64_t v_token_stride, int64_t v_head_stride, const void *slots, int32_t slot_bytes,
+                         void *stream);
+
+/* Read n tokens back: K and V dense n x hkv x d; slots outside the cache give zeros. */
+fp4_status fp4_kv4_read(const uint8_t *cache, int64_t pages, int32_t page, int32_t hkv, int32_t d, const void *slots,
+                        int32_t slot_bytes, int64_t n, void *K, void *V, int32_t dtype, void *stream);
+
+/* Causal attention of packed queries over the cache.
+ *   q        nq x hq x d bf16 (d contiguous, strides in elements), hq a multiple of hkv: query head i reads
+ *            key/value head i / (hq / hkv)
+ *   q_start  device int32[b + 1]: queries q_start[i] .. q_start[i+1] - 1 belong to sequence i (at most max_q of
+ *            them); or NULL: query i belongs to sequence i (nq = b, max_q = 1)
+ *   lens     device int32[b]: tokens of each sequence in the cache, its queries' own among them: query j of
+ *            qlen stands at position len - qlen + j
+ *   table    device int32, b rows of `width` page indices, rows table_stride apart; entries outside the cache
+ *            are as if their tokens were masked
+ *   window   0, or the number of tokens a query sees, its own included
+ *   scale    of the scores (1 / sqrt(d) usually)
+ *   o        nq x hq x d bf16 dense; lse  NULL or fp32 nq x hq: natural log of the sum of exp(score)
+ * A query that sees no token gets zeros and lse = -infinity.  Softmax statistics and sums are fp32.
+ * Two calls on overlapping workspaces must be ordered.  Limits: max_q * (hq / hkv) < 2^24.
+ * Return FP4_OK or FP4_ERR_{NULL,SHAPE,DTYPE,WORKSPACE,ALIGN,DEVICE,HIP}. */
+size_t fp4_kv4_attention_workspace_bytes(int32_t b, int32_t max_q, int32_t hq, int32_t hkv, int32_t d, int32_t page,
+                                         int32_t width);
+fp4_status fp4_kv4_attention(const void *q, int64_t q_token_stride, int64_t q_head_stride, int64_t nq, int32_t hq,
+                             const int32_t *q_start, const int32_t *lens, int32_t b, int32_t max_q,
+                             const int32_t *table, int64_t table_stride, int32_t width, const uint8_t *cache,
+                             int64_t pages, int32_t page, int32_t hkv, int32_t d, int32_t window, float scale, void *o,
+                             float *lse, void *workspace, size_t ws_bytes, void *stream);
+
 /* Host-only: the kernel selection, the same rule the launches use, so a caller (a profiler
  * summary, a benchmark) can name what runs.  fp4_gemm_kernel_name: the FP4 GEMM kernel that
  * fp4_gemm and fp4_linear_forward launch for an M x N x K product on a device with num_cus

@@ -25,6 +25,7 @@ FP4_F32, FP4_BF16 = 0, 1
 FP4_Q16 = 2  # fp4_gemm output only: int16 4*acc with fp32 escapes in the workspace
 FP4_PER_ROW, FP4_PER_COL = 0, 1
 FP4_STAGE_A, FP4_STAGE_W = 1, 2
+FP4_BLOCK_VECTOR, FP4_BLOCK_SQUARE = 0, 1
 
 EXPORTS = (
     "fp4_quantize", "fp4_outlier_capacity", "fp4_outlier_workspace_bytes", "fp4_outlier_clamp",
@@ -33,6 +34,10 @@ EXPORTS = (
     "fp4_linear_forward_wq", "fp4_forward_quantize", "fp4_forward_product", "fp4_gemm_fp8emu_workspace_bytes", "fp4_gemm_fp8emu",
     "fp4_fp8_workspace_bytes", "fp4_fp8_quantize", "fp4_fp8_dequantize",
     "fp4_backward_layout", "fp4_backward_workspace_bytes", "fp4_linear_backward",
+    "fp4_block8_codes_bytes", "fp4_block8_scales_bytes", "fp4_block8_quantize", "fp4_block8_dequantize",
+    "fp4_block8_gemm", "fp4_block8_linear_workspace_bytes", "fp4_block8_linear",
+    "fp4_block8_backward_workspace_bytes", "fp4_block8_backward",
+    "fp4_kv4_cache_bytes", "fp4_kv4_write", "fp4_kv4_read", "fp4_kv4_attention_workspace_bytes", "fp4_kv4_attention",
     "fp4_gemm_kernel_name", "fp4_comp_kernel_name", "fp4_status_string",
 )
 
@@ -84,6 +89,21 @@ def lib():
         "fp4_backward_layout": (i32, [i64, i64, i64, C.POINTER(BwdLayout)]),
         "fp4_backward_workspace_bytes": (sz, [i64, i64, i64]),
         "fp4_linear_backward": (i32, [vp, i32, i64, i64, i64, vp, vp, vp, vp, vp, i32, vp, i32, vp, sz, vp]),
+        "fp4_block8_codes_bytes": (sz, [i64, i64]),
+        "fp4_block8_scales_bytes": (sz, [i64, i64, i32]),
+        "fp4_block8_quantize": (i32, [vp, i32, i64, i64, i64, i32, vp, vp, vp, vp, vp]),
+        "fp4_block8_dequantize": (i32, [vp, vp, i64, i64, i32, vp, i32, vp]),
+        "fp4_block8_gemm": (i32, [vp, vp, i32, vp, vp, i32, i64, i64, i64, vp, i32, vp]),
+        "fp4_block8_linear_workspace_bytes": (sz, [i64, i64, i64]),
+        "fp4_block8_linear": (i32, [vp, i32, i64, i64, i64, vp, vp, i32, i64, vp, i32, vp, vp, vp, sz, vp]),
+        "fp4_block8_backward_workspace_bytes": (sz, [i64, i64]),
+        "fp4_block8_backward": (i32, [vp, i32, i64, i64, i64, i64, vp, vp, i32, vp, vp, vp, i32, vp, i32, vp, sz, vp]),
+        "fp4_kv4_cache_bytes": (sz, [i64, i32, i32, i32]),
+        "fp4_kv4_write": (i32, [vp, i64, i32, i32, i32, vp, vp, i32, i64, i64, i64, i64, i64, vp, i32, vp]),
+        "fp4_kv4_read": (i32, [vp, i64, i32, i32, i32, vp, i32, i64, vp, vp, i32, vp]),
+        "fp4_kv4_attention_workspace_bytes": (sz, [i32, i32, i32, i32, i32, i32, i32]),
+        "fp4_kv4_attention": (i32, [vp, i64, i64, i64, i32, vp, vp, i32, i32, vp, i64, i32, vp, i64, i32, i32, i32,
+                                    i32, C.c_float, vp, vp, vp, sz, vp]),
         "fp4_gemm_kernel_name": (C.c_char_p, [i64, i64, i64, i32]),
         "fp4_comp_kernel_name": (C.c_char_p, [i64, i64]),
         "fp4_status_string": (C.c_char_p, [i32]),
@@ -407,3 +427,228 @@ def backward_intermediates(ws: torch.Tensor, M: int, K: int, N: int) -> dict:
                 Hq=view(lay.Hq, N * (M // 2), torch.uint8, (N, M // 2)), sH=view(lay.sH, 4 * N, torch.float32, (N,)),
                 WqT=view(lay.WqT, K * (N // 2), torch.uint8, (K, N // 2)),
                 AqT=view(lay.AqT, K * (M // 2), torch.uint8, (K, M // 2)))
+
+
+# --------------------------------------------------------------------------- FP8 linear layer, blocks of 128
+class Block8:
+    """An E4M3 operand: `rows` rows of contraction length `length`, one power-of-two scale per
+    block of 128 along the contraction (FP4_BLOCK_VECTOR) or per 128 x 128 block (FP4_BLOCK_SQUARE).
+    codes: u8 (rows, length rounded up to 128); scales: u8, laid out as the C header says."""
+    __slots__ = ("codes", "scales", "rows", "length", "mode")
+
+    def __init__(self, rows: int, length: int, mode: int, device):
+        n = lib().fp4_block8_scales_bytes(rows, length, mode)
+        if n == 0:
+            raise Fp4Error(f"no block-128 operand of {rows} rows, contraction {length}, mode {mode}")
+        self.rows, self.length, self.mode = rows, length, mode
+        self.codes = torch.empty((rows, (length + 127) // 128 * 128), dtype=torch.uint8, device=device)
+        self.scales = torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def _need_rows(*ts):
+    """Matrices on a HIP device whose rows are contiguous (any row stride, any alignment)."""
+    for t in ts:
+        if not t.is_cuda or t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1) or \
+                (t.shape[0] > 1 and t.stride(0) < t.shape[1]):
+            raise ValueError("expected a matrix on a HIP device with contiguous rows")
+
+
+def _ld(t: torch.Tensor) -> int:
+    return max(t.stride(0), t.shape[1])
+
+
+def _same_device(ref: torch.Tensor, *ts):
+    for t in ts:
+        if t is not None and t.device != ref.device:
+            raise ValueError("tensors must be on one device")
+
+
+def _block8_scratch(ws: torch.Tensor | None, nbytes: int, device) -> torch.Tensor:
+    if ws is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    _need_cuda(ws)
+    return ws
+
+
+def block8_quantize(X: torch.Tensor, mode: int = FP4_BLOCK_VECTOR, rows: bool = True, cols: bool = False):
+    """(operand of X, operand of X transposed), each None when not asked for.  For a weight W (K x N)
+    in FP4_BLOCK_SQUARE, cols is the forward's operand and rows the one dX contracts with."""
+    _need_rows(X)
+    R, Cn = X.shape
+    r = Block8(R, Cn, mode, X.device) if rows else None
+    c = Block8(Cn, R, mode, X.device) if cols else None
+    _check(lib().fp4_block8_quantize(_ptr(X), _dt(X), R, Cn, _ld(X), mode, _ptr(r.codes) if r else None,
+                                     _ptr(r.scales) if r else None, _ptr(c.codes) if c else None,
+                                     _ptr(c.scales) if c else None, _stream(X)))
+    return r, c
+
+
+def block8_dequantize(op: Block8, out_dtype: torch.dtype = torch.float32) -> torch.Tensor:
+    """The values that an operand stands for (rows x length)."""
+    Y = torch.empty((op.rows, op.length), dtype=out_dtype, device=op.codes.device)
+    _check(lib().fp4_block8_dequantize(_ptr(op.codes), _ptr(op.scales), op.rows, op.length, op.mode, _ptr(Y),
+                                       _out_dtype_code(out_dtype), _stream(Y)))
+    return Y
+
+
+def block8_gemm(a: Block8, b: Block8, out_dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
+    """a . b^T of two operands with one contraction length."""
+    if a.length != b.length:
+        raise ValueError(f"contraction lengths differ: {a.length} and {b.length}")
+    _same_device(a.codes, b.codes)
+    Y = torch.empty((a.rows, b.rows), dtype=out_dtype, device=a.codes.device)
+    _check(lib().fp4_block8_gemm(_ptr(a.codes), _ptr(a.scales), a.mode, _ptr(b.codes), _ptr(b.scales), b.mode, a.rows,
+                                 b.rows, a.length, _ptr(Y), _out_dtype_code(out_dtype), _stream(Y)))
+    return Y
+
+
+def block8_linear_forward(x: torch.Tensor, w: Block8, out_dtype: torch.dtype | None = None, for_backward: bool = False,
+                          ws: torch.Tensor | None = None):
+    """y = x . W with x (M x K, fp32 or bf16) quantized in blocks of 128 along K and W given by
+    block8_quantize(W, FP4_BLOCK_SQUARE, cols=True)[1].  for_backward: (y, operand of x transposed)."""
+    _need_rows(x)
+    M, K = x.shape
+    if K != w.length:
+        raise ValueError(f"x has {K} columns, the weight a contraction of {w.length}")
+    _same_device(x, w.codes)
+    Y = torch.empty((M, w.rows), dtype=out_dtype or x.dtype, device=x.device)
+    if M == 0:
+        if for_backward:
+            raise ValueError("no rows to contract in the backward")
+        return Y
+    L = lib()
+    xt = Block8(K, M, FP4_BLOCK_VECTOR, x.device) if for_backward else None
+    ws = _block8_scratch(ws, L.fp4_block8_linear_workspace_bytes(M, K, w.rows), x.device)
+    _check(L.fp4_block8_linear(_ptr(x), _dt(x), M, K, _ld(x), _ptr(w.codes), _ptr(w.scales), w.mode, w.rows, _ptr(Y),
+                               _dt(Y), _ptr(xt.codes) if xt else None, _ptr(xt.scales) if xt else None, _ptr(ws),
+                               ws.numel(), _stream(x)))
+    return (Y, xt) if for_backward else Y
+
+
+def block8_linear_backward(dy: torch.Tensor, w: Block8 | None, xt: Block8 | None, out_dtype: torch.dtype | None = None,
+                           ws: torch.Tensor | None = None):
+    """(dx, dw) from dy (M x N), W's operand of K rows (block8_quantize's rows) and the operand of x
+    transposed (block8_linear_forward's); w or xt None: that gradient is not wanted (None)."""
+    _need_rows(dy)
+    if w is None and xt is None:
+        raise ValueError("no gradient asked for")
+    M, N = dy.shape
+    K = w.rows if w is not None else xt.rows
+    if (w is not None and w.length != N) or (xt is not None and (xt.length != M or xt.rows != K)):
+        raise ValueError("operands do not fit dy")
+    if xt is not None and xt.mode != FP4_BLOCK_VECTOR:
+        raise ValueError("the activation's operand has vector blocks")
+    _same_device(dy, w.codes if w is not None else None, xt.codes if xt is not None else None)
+    out_dtype = out_dtype or dy.dtype
+    dx = torch.empty((M, K), dtype=out_dtype, device=dy.device) if w is not None else None
+    dw = torch.empty((K, N), dtype=out_dtype, device=dy.device) if xt is not None else None
+    L = lib()
+    ws = _block8_scratch(ws, L.fp4_block8_backward_workspace_bytes(M, N), dy.device)
+    od = _out_dtype_code(out_dtype)
+    _check(L.fp4_block8_backward(_ptr(dy), _dt(dy), M, K, N, _ld(dy), _ptr(w.codes) if w is not None else None,
+                                 _ptr(w.scales) if w is not None else None, w.mode if w is not None else 0,
+                                 _ptr(xt.codes) if xt is not None else None, _ptr(xt.scales) if xt is not None else None,
+                                 _ptr(dx), od, _ptr(dw), od, _ptr(ws), ws.numel(), _stream(dy)))
+    return dx, dw
+
+
+# --------------------------------------------------------------------------- 4-bit key/value cache
+class KV4Cache:
+    """A paged cache of keys and values in 4 bits (data: u8, laid out as the C header's library
+    does; pages x page tokens x heads x d)."""
+    __slots__ = ("data", "pages", "page", "heads", "d")
+
+    def __init__(self, data, pages, page, heads, d):
+        self.data, self.pages, self.page, self.heads, self.d = data, pages, page, heads, d
+
+
+def kv4_cache(pages: int, page: int, heads: int, d: int, device="cuda") -> KV4Cache:
+    """An empty cache: page (tokens) a power of two from 16 to 1024, d 64 or 128."""
+    n = lib().fp4_kv4_cache_bytes(pages, page, heads, d)
+    if n == 0:
+        raise Fp4Error(f"no 4-bit cache of {pages} pages of {page} tokens, {heads} heads of {d}")
+    return KV4Cache(torch.zeros(n, dtype=torch.uint8, device=device), pages, page, heads, d)
+
+
+def _slot_bytes(t: torch.Tensor, n: int) -> int:
+    if t.dtype not in (torch.int32, torch.int64):
+        raise TypeError(f"expected int32 or int64 indices, got {t.dtype}")
+    if not t.is_cuda or not t.is_contiguous() or t.numel() != n:
+        raise ValueError(f"expected {n} contiguous indices on a HIP device")
+    return t.element_size()
+
+
+def kv4_write(cache: KV4Cache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor) -> None:
+    """Quantize k and v (n x heads x d, fp32 or bf16, d contiguous) into the cache at slots (page index *
+    page + offset; those outside the cache are skipped)."""
+    n = k.shape[0]
+    for t in (k, v):
+        if not t.is_cuda or t.shape != (n, cache.heads, cache.d) or t.stride(2) != 1:
+            raise ValueError(f"expected (n, {cache.heads}, {cache.d}) on a HIP device, the last dimension contiguous")
+    if k.dtype != v.dtype:
+        raise TypeError("k and v must share a dtype")
+    sb = _slot_bytes(slots, n)
+    _same_device(cache.data, k, v, slots)
+    if n == 0:
+        return
+    _check(lib().fp4_kv4_write(_ptr(cache.data), cache.pages, cache.page, cache.heads, cache.d, _ptr(k), _ptr(v), _dt(k),
+                               n, k.stride(0), k.stride(1), v.stride(0), v.stride(1), _ptr(slots), sb, _stream(k)))
+
+
+def kv4_read(cache: KV4Cache, slots: torch.Tensor, d: int | None = None, out_dtype: torch.dtype = torch.bfloat16):
+    """(k, v), n x heads x d, of the tokens at slots; d, if given, must be the cache's."""
+    if d is not None and d != cache.d:
+        raise ValueError(f"the cache holds heads of {cache.d}")
+    n = slots.numel()
+    sb = _slot_bytes(slots, n)
+    _same_device(cache.data, slots)
+    k = torch.empty((n, cache.heads, cache.d), dtype=out_dtype, device=slots.device)
+    v = torch.empty_like(k)
+    if n:
+        _check(lib().fp4_kv4_read(_ptr(cache.data), cache.pages, cache.page, cache.heads, cache.d, _ptr(slots), sb, n,
+                                  _ptr(k), _ptr(v), _out_dtype_code(out_dtype), _stream(slots)))
+    return k, v
+
+
+def kv4_attention_workspace(q: torch.Tensor, cache: KV4Cache, pages: torch.Tensor, max_q: int = 1) -> torch.Tensor:
+    """A workspace for kv4_attention with these sizes and any window."""
+    n = lib().fp4_kv4_attention_workspace_bytes(pages.shape[0], max_q, q.shape[1], cache.heads, cache.d, cache.page,
+                                                pages.shape[1])
+    return torch.empty(max(n, 16), dtype=torch.uint8, device=q.device)
+
+
+def kv4_attention(q: torch.Tensor, cache: KV4Cache, pages: torch.Tensor, lens: torch.Tensor,
+                  q_start: torch.Tensor | None = None, max_q: int = 1, window: int = 0, scale: float | None = None,
+                  return_lse: bool = False, ws: torch.Tensor | None = None):
+    """Causal attention of packed bf16 queries q (nq x hq x d) over the cache.  pages: int32 page table
+    (b x width); lens: int32 tokens of each sequence in the cache, its queries' own among them; q_start: int32
+    b + 1 offsets of the sequences' queries (at most max_q each), or None for one query a sequence;
+    window: tokens a query sees (0: all).  A query that sees nothing gets 0 and lse -inf."""
+    if q.dtype != torch.bfloat16:
+        raise TypeError(f"expected bfloat16 queries, got {q.dtype}")
+    if not q.is_cuda or q.dim() != 3 or q.shape[2] != cache.d or q.stride(2) != 1:
+        raise ValueError(f"expected queries (nq, hq, {cache.d}) on a HIP device, the last dimension contiguous")
+    nq, hq, d = q.shape
+    if hq == 0 or hq % cache.heads:
+        raise ValueError(f"{hq} query heads over {cache.heads} key/value heads")
+    b = pages.shape[0]
+    for t, shape in ((lens, (b,)), (q_start, (b + 1,))):
+        if t is not None and (t.dtype != torch.int32 or not t.is_cuda or tuple(t.shape) != shape or not t.is_contiguous()):
+            raise ValueError(f"expected int32 {shape} on a HIP device")
+    if pages.dtype != torch.int32 or not pages.is_cuda or pages.dim() != 2 or pages.stride(1) != 1 or \
+            (b > 1 and pages.stride(0) < pages.shape[1]):
+        raise ValueError("expected an int32 page table (b, width) on a HIP device, rows contiguous")
+    if q_start is None and nq != b:
+        raise ValueError(f"{nq} queries for {b} sequences without q_start")
+    _same_device(q, cache.data, pages, lens, q_start, ws)
+    o = torch.empty((nq, hq, d), dtype=q.dtype, device=q.device)
+    lse = torch.empty((nq, hq), dtype=torch.float32, device=q.device) if return_lse else None
+    if nq and b:
+        if ws is None:
+            ws = kv4_attention_workspace(q, cache, pages, max_q)
+        _check(lib().fp4_kv4_attention(_ptr(q), q.stride(0), q.stride(1), nq, hq, _ptr(q_start), _ptr(lens), b, max_q,
+                                       _ptr(pages), max(pages.stride(0), pages.shape[1]), pages.shape[1],
+                                       _ptr(cache.data), cache.pages, cache.page, cache.heads, d, window,
+                                       d ** -0.5 if scale is None else float(scale), _ptr(o), _ptr(lse), _ptr(ws),
+                                       ws.numel(), _stream(q)))
+    return (o, lse) if return_lse else o
