@@ -395,7 +395,8 @@ fp4_status fp4_block8_backward(const void *dY, int32_t dy_dtype, int64_t M, int6
 /* ---------------------------------------------------------------------------------------------
  * 4-bit key/value cache.  `pages` pages of `page` tokens (a power of two, 16 to 1024), hkv heads of
  * size d (64 or 128).  Each group of 32 values along d is held as E2M1 codes (nearest of x * 2^-e, ties to
- * even, saturating at 6) and the byte e + 127, e the smallest integer >= -127 with max|x| <= 7 * 2^e.
+ * even, saturating at 6, and at 3 where e = 126, as 4 * 2^126 is no fp32 number) and the byte e + 127, e the
+ * smallest integer >= -127 with max|x| <= 7 * 2^e.
  * A token whose key or value holds a NaN or infinity in a head reads back as NaN in that head, and
  * so do the attention rows that see it.  The caller zeroes the memory once, before the first use.
  * A slot is a token's place: page index * page + offset in the page. */

@@ -47,6 +47,16 @@ __global__ __launch_bounds__(256) void k_kv4_write(uint8_t *__restrict__ cache, 
             k[i] *= fk;
             v[i] *= fv;
         }
+        // 4 * 2^126 is no fp32 number: there 3 is the largest code, so that whatever is held stays
+        // finite where its token is masked (0 * inf would be NaN)
+        if (ek == 253u) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) k[i] = fminf(fmaxf(k[i], -3.0f), 3.0f);
+        }
+        if (ev == 253u) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = fminf(fmaxf(v[i], -3.0f), 3.0f);
+        }
         ck = e2m1_pack8(k);
         cv = e2m1_pack8(v);
     } else {

@@ -26,6 +26,7 @@
 namespace fp4 {
 
 typedef float v4f __attribute__((ext_vector_type(4)));
+typedef float v16f __attribute__((ext_vector_type(16)));
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
 typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
@@ -34,14 +35,19 @@ namespace {
 
 constexpr int NW = 4;        // waves of a decode workgroup
 constexpr int TT = 32;       // tokens a wave takes at once
+constexpr int CR = 128;      // rows of a workgroup of the many-rows kernel: 32 a wave
+constexpr int CT = 64;       // tokens it takes at once
+constexpr int FEW = 32;      // rows a (sequence, head) up to which the decode kernel takes them
 constexpr float LN2 = 0.69314718055994530942f;
 constexpr float LOG2E = 1.44269504088896340736f;
 
 struct DecArgs {
     Kv4Attn a;
-    int g, rt;        // heads a group; row tiles of 16 a (sequence, head)
+    int g, rt;        // heads a group; row tiles a (sequence, head)
+    int tr;           // rows of a tile (16 or CR)
+    int pr;           // rows a partial result holds: min(tr, max_q * g)
     int splits;       // workgroups along the tokens
-    int chunk;        // tokens each takes (a multiple of NW * TT)
+    int chunk;        // tokens each takes (a multiple of the unit, NW * TT or CT)
     float c;          // scale * log2(e)
 };
 
@@ -58,7 +64,7 @@ __device__ __forceinline__ Span span_of(const Kv4Attn &a, int g, int seq, int ro
     s.len = a.lens[seq];
     s.qbeg = a.q_start ? max(a.q_start[seq], 0) : seq;
     s.qlen = a.q_start ? min(a.q_start[seq + 1], a.nq) - s.qbeg : 1;
-    s.rows = max(s.qlen, 0) * g;
+    s.rows = min(max(s.qlen, 0), a.max_q) * g;
     const int cap = min(s.len, a.width << a.geo.page_log2);
     if (row0 >= s.rows) {
         s.lo = s.hi = s.full_lo = s.full_hi = 0;
@@ -113,13 +119,23 @@ __device__ __forceinline__ void unpack_cols(const uint32_t (&w)[8], const float 
     c1 = __builtin_bit_cast(v8bf, u32x4{hi[0], hi[1], hi[2], hi[3]});
 }
 
+// Largest over the four lanes n, n + 16, n + 32, n + 48, in each of them.
+__device__ __forceinline__ float half_max(float x) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float quarter_max(float x) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return half_max(fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1])));
+}
+
 }  // namespace
 
 // Few rows (single tokens, drafts): 16 rows of one (sequence, key/value head) a workgroup, its four
 // waves taking tiles of 32 tokens in turn and joining in LDS; `splits` workgroups share the tokens.
 // Bound by the cache's bytes.
 template <int D>
-__global__ __launch_bounds__(64 * NW) void k_kv4_decode(DecArgs p) {
+__global__ __launch_bounds__(64 * NW, 3) void k_kv4_decode(DecArgs p) {
     constexpr int J = D / 16;   // columns a lane owns in the O^T tiles: J n + j
     constexpr int KS = D / 32;  // contraction steps of the scores
     const Kv4Attn &a = p.a;
@@ -151,7 +167,7 @@ __global__ __launch_bounds__(64 * NW) void k_kv4_decode(DecArgs p) {
         qf[i] = __builtin_bit_cast(v8bf, x);
     }
 
-    const int P = 1 << a.geo.page_log2;
+    const int lg = a.geo.page_log2, P = 1 << lg;
     const int64_t region = a.geo.region();
     const int32_t *table = a.pages + (int64_t)seq * a.page_rs;
     v4f acc[J];
@@ -159,90 +175,109 @@ __global__ __launch_bounds__(64 * NW) void k_kv4_decode(DecArgs p) {
     for (int j = 0; j < J; ++j) acc[j] = v4f{0, 0, 0, 0};
     float m = -INFINITY, l = 0.0f;
 
-    for (int t0 = beg + wave * TT; t0 < end; t0 += NW * TT) {
-        // tokens of the scores' row n in half s: 8 (n / 4) + 4 s + n % 4; of V's step: 8 h + 0..7.
-        // A page that the table does not hold (outside the cache) is as if its tokens were masked.
-        const int tk = t0 + 8 * (n >> 2), tv = t0 + 8 * h;
-        const int pk = tk < end ? table[tk >> a.geo.page_log2] : -1;
-        const int pv = tv < end ? table[tv >> a.geo.page_log2] : -1;
-        const bool okk = (uint32_t)pk < (uint64_t)a.geo.pages, okv = (uint32_t)pv < (uint64_t)a.geo.pages;
-        uint32_t kw[2][KS], ks[2];
+    // A lane's part of a tile of 32 tokens.  Tokens of the scores' row n in half s: 8 (n / 4) + 4 s +
+    // n % 4; of V's step: 8 h + 0..7.  Nothing is masked here: the page index is clamped into the
+    // table's row and into the cache, whose bytes are finite numbers wherever a score is masked away.
+    struct Tile {
+        uint32_t kw[2][KS], vw[8];
+        uint32_t ks[2];
+        uint2 vs;
+        bool okk;  // the page is one of the cache's (K's lane; V's tokens are the same pages)
+    };
+    auto page_at = [&](int t) { return table[min(t, end - 1) >> lg]; };
+    auto fetch = [&](int t0, int pk, int pv, Tile &x) {
+        x.okk = (uint32_t)pk < (uint64_t)a.geo.pages;
+        const bool okv = (uint32_t)pv < (uint64_t)a.geo.pages;
+        const uint8_t *kb = a.cache + ((int64_t)(x.okk ? pk : 0) * a.geo.hkv + head) * region;
+        const uint8_t *vb = a.cache + ((int64_t)(okv ? pv : 0) * a.geo.hkv + head) * region;
+        const int tk = ((t0 + 8 * (n >> 2)) & (P - 1)) + (n & 3), tv = (t0 + 8 * h) & (P - 1);
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-            ks[s] = 0;
+            const int tok = tk + 4 * s;
+            if constexpr (D == 128) {
+                const u32x4 w = *reinterpret_cast<const u32x4 *>(kb + tok * (D / 2) + h * (D / 8));
 #pragma unroll
-            for (int i = 0; i < KS; ++i) kw[s][i] = 0;
-            if (okk) {
-                const int tok = (tk & (P - 1)) + 4 * s + (n & 3);
-                const uint8_t *base = a.cache + ((int64_t)pk * a.geo.hkv + head) * region;
-                const uint32_t *src = reinterpret_cast<const uint32_t *>(base + tok * (D / 2) + h * (D / 8));
-#pragma unroll
-                for (int i = 0; i < KS; ++i) kw[s][i] = src[i];
-                ks[s] = base[a.geo.ks_off() + (h * D / 128) * P + tok];
+                for (int i = 0; i < 4; ++i) x.kw[s][i] = w[i];
+            } else {
+                const uint2 w = *reinterpret_cast<const uint2 *>(kb + tok * (D / 2) + h * (D / 8));
+                x.kw[s][0] = w.x;
+                x.kw[s][1] = w.y;
             }
+            x.ks[s] = kb[a.geo.ks_off() + (h * D / 128) * P + tok];
         }
-        uint32_t vw[8];
-        uint2 vs = make_uint2(0, 0);
+        const int dw = D == 128 ? n : n >> 1;
+        const u32x4 *src = reinterpret_cast<const u32x4 *>(vb + a.geo.v_off() + ((tv >> 3) * (D / 8) + dw) * 32);
+        const u32x4 y0 = src[0], y1 = src[1];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) vw[i] = 0;
-        if (okv) {
-            const int tok = tv & (P - 1);
-            const uint8_t *base = a.cache + ((int64_t)pv * a.geo.hkv + head) * region;
-            const int dw = D == 128 ? n : n >> 1;
-            const u32x4 *src = reinterpret_cast<const u32x4 *>(base + a.geo.v_off() + ((tok >> 3) * (D / 8) + dw) * 32);
-            const u32x4 x = src[0], y = src[1];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                vw[i] = x[i];
-                vw[4 + i] = y[i];
-            }
-            vs = *reinterpret_cast<const uint2 *>(base + a.geo.vs_off() + (n * J / 32) * P + tok);
+        for (int i = 0; i < 4; ++i) {
+            x.vw[i] = y0[i];
+            x.vw[4 + i] = y1[i];
         }
+        x.vs = *reinterpret_cast<const uint2 *>(vb + a.geo.vs_off() + (n * J / 32) * P + tv);
+    };
+
+    // two tiles of loads in flight: the next tile's bytes and the page indices of the one after it
+    const int first = beg + wave * TT;
+    Tile cur;
+    int pk = 0, pv = 0;
+    if (first < end) {
+        fetch(first, page_at(first + 8 * (n >> 2)), page_at(first + 8 * h), cur);
+        pk = page_at(first + NW * TT + 8 * (n >> 2));
+        pv = page_at(first + NW * TT + 8 * h);
+    }
+    for (int t0 = first; t0 < end; t0 += NW * TT) {
+        Tile nxt;
+        fetch(t0 + NW * TT, pk, pv, nxt);
+        pk = page_at(t0 + 2 * NW * TT + 8 * (n >> 2));
+        pv = page_at(t0 + 2 * NW * TT + 8 * h);
         if constexpr (D == 64) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) vw[i] >>= 16 * (n & 1);
+            for (int i = 0; i < 8; ++i) cur.vw[i] >>= 16 * (n & 1);
         }
-
         // scores: element r of half s is token t0 + 8 h + 4 s + r, row n
         float x[8];
-        const bool okp = __shfl((int)okk, 4 * h, 64) != 0;  // of the lane's score tokens' page
+        const uint64_t okm = __builtin_amdgcn_ballot_w64(cur.okk);
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
             v4f d = v4f{0, 0, 0, 0};
             v8bf kf[KS];
-            unpack_row<KS>(kw[s], ks[s], kf);
+            unpack_row<KS>(cur.kw[s], cur.ks[s], kf);
 #pragma unroll
             for (int i = 0; i < KS; ++i) d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf[i], qf[i], d, 0, 0, 0);
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int tok = t0 + 8 * h + 4 * s + r;
-                x[4 * s + r] = okp && tok < min(vhi, end) && tok >= vlo ? d[r] * p.c : -INFINITY;
+            for (int r = 0; r < 4; ++r) x[4 * s + r] = d[r] * p.c;
+        }
+        if (okm != ~0ull || t0 < sp.full_lo || t0 + TT > min(sp.full_hi, end)) {  // some token is masked
+            const bool okp = ((okm >> (4 * h)) & 1) != 0;  // of the lane's score tokens' page
+            const int hi = okp ? min(vhi, end) : 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int tok = t0 + 8 * h + i;
+                x[i] = tok < hi && tok >= vlo ? x[i] : -INFINITY;
             }
         }
-        float mx = m;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) mx = fmaxf(mx, x[i]);
-        mx = fmaxf(mx, __shfl_xor(mx, 16, 64));
-        mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
+        float mx = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
+        mx = fmaxf(m, quarter_max(mx));
         const float mu = mx == -INFINITY ? 0.0f : mx;
-        const float alpha = __builtin_amdgcn_exp2f(m - mu);
-        m = mx;
-        l *= alpha;
+        if (__builtin_amdgcn_ballot_w64(mx != m) != 0) {  // rarely, after a row's first tiles
+            const float alpha = __builtin_amdgcn_exp2f(m - mu);
+            m = mx;
+            l *= alpha;
 #pragma unroll
-        for (int j = 0; j < J; ++j) acc[j] *= alpha;
+            for (int j = 0; j < J; ++j) acc[j] *= alpha;
+        }
         float e[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            e[i] = __builtin_amdgcn_exp2f(x[i] - mu);
-            l += e[i];
-        }
+        for (int i = 0; i < 8; ++i) e[i] = __builtin_amdgcn_exp2f(x[i] - mu);
+        l += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
         const v8bf pb = __builtin_bit_cast(v8bf, u32x4{bf16_pack2(e[0], e[1]), bf16_pack2(e[2], e[3]),
                                                        bf16_pack2(e[4], e[5]), bf16_pack2(e[6], e[7])});
+        const uint2 vs = cur.vs;
         const float sc[8] = {scale_of<0>(vs.x), scale_of<1>(vs.x), scale_of<2>(vs.x), scale_of<3>(vs.x),
                              scale_of<0>(vs.y), scale_of<1>(vs.y), scale_of<2>(vs.y), scale_of<3>(vs.y)};
         v8bf c0, c1;
 #define PV(B)                                                                                 \
-    unpack_cols<B>(vw, sc, c0, c1);                                                           \
+    unpack_cols<B>(cur.vw, sc, c0, c1);                                                       \
     acc[2 * B] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(c0, pb, acc[2 * B], 0, 0, 0);        \
     acc[2 * B + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(c1, pb, acc[2 * B + 1], 0, 0, 0);
         PV(0)
@@ -252,6 +287,7 @@ __global__ __launch_bounds__(64 * NW) void k_kv4_decode(DecArgs p) {
             PV(3)
         }
 #undef PV
+        cur = nxt;
     }
 
     // the waves join: maxima, then sums and outputs over the common maximum, in wave order
@@ -298,7 +334,7 @@ __global__ __launch_bounds__(64 * NW) void k_kv4_decode(DecArgs p) {
         } else {
             // partial row: D sums, then the maximum and the sum of the split
             float *w = reinterpret_cast<float *>(a.ws) +
-                       ((((int64_t)seq * p.rt + rt) * a.geo.hkv + head) * p.splits + split) * 16 * (D + 4) + r * (D + 4);
+                       (((((int64_t)seq * p.rt + rt) * a.geo.hkv + head) * p.splits + split) * p.pr + r) * (D + 4);
             *reinterpret_cast<float4 *>(w + col) = make_float4(o[0], o[1], o[2], o[3]);
             if (col == 0) {
                 w[D] = M;
@@ -308,84 +344,365 @@ __global__ __launch_bounds__(64 * NW) void k_kv4_decode(DecArgs p) {
     }
 }
 
-// Joins the splits of a (sequence, head): one wave a row, splits in ascending order.
+// Many rows (chunks of prompts): 128 rows of one (sequence, key/value head) a workgroup, 32 a wave.
+// Every tile of 64 tokens is unpacked to bf16 once by the whole workgroup into one of two LDS
+// buffers, while the waves multiply the other: with 16 rows a wave, as above, unpacking in registers
+// would take more time than the products.  Tokens are rows of K's operand with bits 2 and 3 of their
+// index exchanged, so that a lane's eight scores of one V step are eight consecutive tokens.
+// Two workgroups a CU (64 KiB of LDS each), so one's softmax runs beside the other's products.
+template <int D>
+__global__ __launch_bounds__(256, 2) void k_kv4_chunk(DecArgs p) {
+    constexpr int KC = D / 8;     // 16-byte pieces of a token's K row
+    constexpr int KS = D / 16;    // contraction steps of the scores
+    constexpr int DT = D / 32;    // tiles of 32 columns; dwords of K and tokens of V a thread unpacks
+    __shared__ __attribute__((aligned(16))) uint8_t sk[2][CT * D * 2];
+    __shared__ __attribute__((aligned(16))) uint8_t sv[2][D * CT * 2];
+    const Kv4Attn &a = p.a;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, n = lane & 31, h = lane >> 5;
+    int id = blockIdx.x;
+    const int split = id % p.splits; id /= p.splits;
+    const int head = id % a.geo.hkv; id /= a.geo.hkv;
+    const int rt = p.rt - 1 - id % p.rt, seq = id / p.rt;  // the longest first
+    const int row0 = rt * CR;
+    const Span sp = span_of(a, p.g, seq, row0, CR);
+    if (row0 >= sp.rows) return;
+    const int beg = sp.lo + split * p.chunk, end = min(sp.hi, beg + p.chunk);
+    if (p.splits > 1 && beg >= end) return;  // the joining kernel counts the splits the same way
+
+    // this lane's row, and what the wave's rows see
+    const int row = row0 + wave * 32 + n;
+    const bool live = row < sp.rows;
+    const int qi = live ? row / p.g : 0, qh = live ? head * p.g + row % p.g : 0;
+    const int pos = sp.len - sp.qlen + qi;
+    const int vhi = live ? min(pos + 1, end) : 0, vlo = a.window ? pos - a.window + 1 : 0;
+    const Span sw = span_of(a, p.g, seq, row0 + wave * 32, 32);
+    const bool neg = p.c < 0.0f;  // the maximum is taken before the scale: a negative one goes to q
+    const float c = neg ? -p.c : p.c;
+    v8bf qf[KS];
+#pragma unroll
+    for (int i = 0; i < KS; ++i) {
+        u32x4 x = {0, 0, 0, 0};
+        if (live)
+            x = *reinterpret_cast<const ua_u32x4 *>(a.q + (int64_t)(sp.qbeg + qi) * a.q_ts + (int64_t)qh * a.q_hs +
+                                                    16 * i + 8 * h);
+        if (neg) x ^= 0x80008000u;
+        qf[i] = __builtin_bit_cast(v8bf, x);
+    }
+
+    // What a thread unpacks: DT dwords of one token's K (of one group of 32), and eight columns of DT
+    // consecutive tokens' V.
+    const int lg = a.geo.page_log2, P = 1 << lg;
+    const int64_t region = a.geo.region();
+    const int32_t *table = a.pages + (int64_t)seq * a.page_rs;
+    const int kt = tid >> 2, kq = tid & 3;
+    constexpr int VP = 8 / DT;
+    const int vp = tid % VP, vn = tid / VP % (D / 8), vt = tid / VP / (D / 8);
+    const int vtok = vt * 8 + vp * DT;
+    uint32_t kw[DT], vw[DT], ks, vs;
+    auto page_at = [&](int t) {
+        const int pg = table[min(t, end - 1) >> lg];
+        return (uint32_t)pg < (uint64_t)a.geo.pages ? pg : -1;
+    };
+    // pages outside the cache: their tokens' bytes are any page's, and their scores are masked
+    bool okk;
+    auto fetch = [&](int t0) {
+        const int pk = page_at(t0 + kt), pv = page_at(t0 + vtok);
+        okk = pk >= 0;
+        const uint8_t *kb = a.cache + ((int64_t)max(pk, 0) * a.geo.hkv + head) * region;
+        const uint8_t *vb = a.cache + ((int64_t)max(pv, 0) * a.geo.hkv + head) * region;
+        const int tk = (t0 + kt) & (P - 1), tv = (t0 + vtok) & (P - 1);
+        const uint8_t *ka = kb + tk * (D / 2) + kq * (D / 8);
+        const uint8_t *va = vb + a.geo.v_off() + ((tv >> 3) * (D / 8) + vn) * 32 + (tv & 7) * 4;
+        if constexpr (D == 128) {
+            const u32x4 x = *reinterpret_cast<const u32x4 *>(ka), y = *reinterpret_cast<const u32x4 *>(va);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                kw[i] = x[i];
+                vw[i] = y[i];
+            }
+            vs = *reinterpret_cast<const uint32_t *>(vb + a.geo.vs_off() + (vn >> 2) * P + tv);
+        } else {
+            const uint2 x = *reinterpret_cast<const uint2 *>(ka), y = *reinterpret_cast<const uint2 *>(va);
+            kw[0] = x.x;
+            kw[1] = x.y;
+            vw[0] = y.x;
+            vw[1] = y.y;
+            vs = *reinterpret_cast<const uint16_t *>(vb + a.geo.vs_off() + (vn >> 2) * P + tv);
+        }
+        ks = kb[a.geo.ks_off() + (kq * D / 128) * P + tk];
+    };
+    // K rows: KC pieces, turned so that 16 rows of one piece lie on 16 places; V rows (columns): 8
+    // pieces of eight tokens, turned for the reads (32 consecutive columns) and the writes (every eighth)
+    auto kpiece = [](int r, int ch) { return D == 128 ? r * 16 + (ch ^ (r & 15)) : r * 8 + (ch ^ ((r >> 1) & 7)); };
+    auto vpiece = [](int col, int ch) { return col * 8 + (ch ^ (((col >> 1) ^ (col >> 4)) & 7)); };
+    const int krow = (kt & ~12) | ((kt & 4) << 1) | ((kt & 8) >> 1);
+    auto unpack = [&](int b) {
+        v8bf kf[DT];
+        unpack_row<DT>(kw, okk ? ks : 0u, kf);
+#pragma unroll
+        for (int i = 0; i < DT; ++i) *reinterpret_cast<v8bf *>(&sk[b][kpiece(krow, kq * DT + i) * 16]) = kf[i];
+        const float sc[4] = {scale_of<0>(vs), scale_of<1>(vs), scale_of<2>(vs), scale_of<3>(vs)};
+        uint32_t x[DT][4];
+#pragma unroll
+        for (int t = 0; t < DT; ++t) {
+            x[t][0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(vw[t], sc[t], 0));
+            x[t][1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(vw[t], sc[t], 1));
+            x[t][2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(vw[t], sc[t], 2));
+            x[t][3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(vw[t], sc[t], 3));
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const uint32_t sel = j & 1 ? 0x07060302u : 0x05040100u;
+            uint8_t *d = &sv[b][vpiece(vn * 8 + j, vt) * 16 + vp * DT * 2];
+            if constexpr (D == 128)
+                *reinterpret_cast<uint2 *>(d) = make_uint2(__builtin_amdgcn_perm(x[1][j >> 1], x[0][j >> 1], sel),
+                                                           __builtin_amdgcn_perm(x[3][j >> 1], x[2][j >> 1], sel));
+            else
+                *reinterpret_cast<uint32_t *>(d) = __builtin_amdgcn_perm(x[1][j >> 1], x[0][j >> 1], sel);
+        }
+    };
+
+    v16f acc[DT];
+#pragma unroll
+    for (int j = 0; j < DT; ++j)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[j][r] = 0.0f;
+    float m = -INFINITY, l = 0.0f;  // m: of the unscaled scores
+
+    // whether some page of a tile lies outside the cache, from the waves that unpacked it
+    __shared__ uint64_t bad[2][4];
+    if (beg < end) {
+        fetch(beg);
+        const uint64_t bm = ~__builtin_amdgcn_ballot_w64(okk);
+        if (lane == 0) bad[0][wave] = bm;
+        unpack(0);
+        fetch(beg + CT);
+    }
+    int b = 0;
+    for (int t0 = beg; t0 < end; t0 += CT, b ^= 1) {
+        __syncthreads();  // tile t0 is in buffer b, and nobody reads the other any more
+        if (t0 + CT < end) {
+            const uint64_t bm = ~__builtin_amdgcn_ballot_w64(okk);
+            if (lane == 0) bad[b ^ 1][wave] = bm;
+            unpack(b ^ 1);
+            fetch(t0 + 2 * CT);
+        }
+        if (t0 >= sw.hi || t0 + CT <= sw.lo) continue;  // the wave's rows see nothing of it
+        v16f s[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) s[u][r] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < KS; ++i)
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const v8bf kf = *reinterpret_cast<const v8bf *>(&sk[b][kpiece(u * 32 + n, 2 * i + h) * 16]);
+                s[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[i], s[u], 0, 0, 0);
+            }
+        // element r of block u: token t0 + 32 u + 16 (r / 8) + 8 h + r % 8 of row n
+        const uint64_t anybad = bad[b][0] | bad[b][1] | bad[b][2] | bad[b][3];
+        if (anybad != 0 || t0 < sw.full_lo || t0 + CT > min(sw.full_hi, end)) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    const int q = 32 * u + 16 * (r >> 3) + 8 * h + (r & 7), tok = t0 + q;
+                    // token q was unpacked by threads 4 q .. 4 q + 3: bit 4 (q % 16) of wave q / 16
+                    const bool ok = ((bad[b][q >> 4] >> (4 * (q & 15))) & 1) == 0;
+                    s[u][r] = ok && tok < vhi && tok >= vlo ? s[u][r] : -INFINITY;
+                }
+        }
+        float mx = m;
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int r = 0; r < 16; r += 2) mx = fmaxf(mx, fmaxf(s[u][r], s[u][r + 1]));
+        mx = half_max(mx);
+        const float mu = mx == -INFINITY ? 0.0f : mx * c;
+        if (__builtin_amdgcn_ballot_w64(mx != m) != 0) {
+            const float alpha = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m * c - mu);
+            m = mx;
+            l *= alpha;
+#pragma unroll
+            for (int j = 0; j < DT; ++j) acc[j] *= alpha;
+        }
+        v8bf pb[4];
+        float ls[4];
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                float e[8];
+#pragma unroll
+                for (int r = 0; r < 8; ++r) e[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[u][8 * k + r], c, -mu));
+                ls[2 * u + k] = ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
+                pb[2 * u + k] = __builtin_bit_cast(v8bf, u32x4{bf16_pack2(e[0], e[1]), bf16_pack2(e[2], e[3]),
+                                                               bf16_pack2(e[4], e[5]), bf16_pack2(e[6], e[7])});
+            }
+        l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int j = 0; j < DT; ++j) {
+                const v8bf vf = *reinterpret_cast<const v8bf *>(&sv[b][vpiece(j * 32 + n, 2 * k + h) * 16]);
+                acc[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf, pb[k], acc[j], 0, 0, 0);
+            }
+    }
+    l += __shfl_xor(l, 32, 64);
+    if (!live) return;
+    // element r of tile j: column 32 j + 8 (r / 4) + 4 h + r % 4 of row n
+    if (p.splits == 1) {
+        const int64_t out = (int64_t)(sp.qbeg + qi) * a.hq + qh;
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll
+        for (int j = 0; j < DT; ++j)
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                *reinterpret_cast<uint2 *>(a.o + out * D + 32 * j + 8 * q + 4 * h) =
+                    make_uint2(bf16_pack2(acc[j][4 * q] * inv, acc[j][4 * q + 1] * inv),
+                               bf16_pack2(acc[j][4 * q + 2] * inv, acc[j][4 * q + 3] * inv));
+        if (a.lse && h == 0) a.lse[out] = l == 0.0f ? -INFINITY : (m * c + __builtin_amdgcn_logf(l)) * LN2;
+    } else {
+        float *w = reinterpret_cast<float *>(a.ws) +
+                   (((((int64_t)seq * p.rt + rt) * a.geo.hkv + head) * p.splits + split) * p.pr + wave * 32 + n) * (D + 4);
+#pragma unroll
+        for (int j = 0; j < DT; ++j)
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                *reinterpret_cast<float4 *>(w + 32 * j + 8 * q + 4 * h) =
+                    make_float4(acc[j][4 * q], acc[j][4 * q + 1], acc[j][4 * q + 2], acc[j][4 * q + 3]);
+        if (h == 0) {
+            w[D] = m == -INFINITY ? m : m * c;
+            w[D + 1] = l;
+        }
+    }
+}
+
+// Joins the splits of a row: a workgroup a row, D / 4 lanes to a split's columns, so 8 (D = 128) or
+// 16 splits are read at once.  Each lane group sums its splits in ascending order, then the groups
+// are summed in order.
 template <int D>
 __global__ __launch_bounds__(256) void k_kv4_join(DecArgs p) {
+    constexpr int L = D / 4, G = 256 / L;
     const Kv4Attn &a = p.a;
-    const int lane = threadIdx.x & 63;
-    int64_t id = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-    const int r = (int)(id % 16); id /= 16;
+    const int lane = threadIdx.x % L, grp = threadIdx.x / L;
+    int64_t id = blockIdx.x;
+    const int r = (int)(id % p.pr); id /= p.pr;
     const int head = (int)(id % a.geo.hkv); id /= a.geo.hkv;
     const int rt = (int)(id % p.rt);
     const int seq = (int)(id / p.rt);
-    if (seq >= a.b) return;
-    const Span sp = span_of(a, p.g, seq, rt * 16, 16);
-    const int row = rt * 16 + r;
+    const Span sp = span_of(a, p.g, seq, rt * p.tr, p.tr);
+    const int row = rt * p.tr + r;
     if (row >= sp.rows) return;
     const int ns = sp.hi > sp.lo ? (sp.hi - sp.lo + p.chunk - 1) / p.chunk : 0;
+    const int64_t SS = (int64_t)p.pr * (D + 4);
     const float *w = reinterpret_cast<const float *>(a.ws) +
-                     (((int64_t)seq * p.rt + rt) * a.geo.hkv + head) * p.splits * 16 * (D + 4) + r * (D + 4);
-    constexpr int SS = 16 * (D + 4);
-    float M = -INFINITY;
-    for (int s = lane; s < ns; s += 64) M = fmaxf(M, w[(int64_t)s * SS + D]);
-#pragma unroll
-    for (int off = 32; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor(M, off, 64));
-    const float mu = M == -INFINITY ? 0.0f : M;
-    constexpr int E = D / 64;
-    float o[E] = {}, L = 0.0f;
-    for (int s = 0; s < ns; ++s) {
-        const float *x = w + (int64_t)s * SS;
-        const float f = __builtin_amdgcn_exp2f(x[D] - mu);
-        L += x[D + 1] * f;
-#pragma unroll
-        for (int i = 0; i < E; ++i) o[i] += x[lane * E + i] * f;
+                     ((((int64_t)seq * p.rt + rt) * a.geo.hkv + head) * p.splits * p.pr + r) * (D + 4);
+    float M = -INFINITY, Lsum = 0.0f, o[4] = {0, 0, 0, 0};
+#pragma unroll 4
+    for (int s = grp; s < ns; s += G) {
+        const float4 v = *reinterpret_cast<const float4 *>(w + s * SS + lane * 4);
+        const float2 ml = *reinterpret_cast<const float2 *>(w + s * SS + D);
+        const float nm = fmaxf(M, ml.x), mu = nm == -INFINITY ? 0.0f : nm;
+        const float f0 = __builtin_amdgcn_exp2f(M - mu), f1 = __builtin_amdgcn_exp2f(ml.x - mu);
+        M = nm;
+        Lsum = Lsum * f0 + ml.y * f1;
+        o[0] = o[0] * f0 + v.x * f1;
+        o[1] = o[1] * f0 + v.y * f1;
+        o[2] = o[2] * f0 + v.z * f1;
+        o[3] = o[3] * f0 + v.w * f1;
     }
-    const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+    __shared__ __attribute__((aligned(16))) float so[G][D + 4];
+    *reinterpret_cast<float4 *>(&so[grp][lane * 4]) = make_float4(o[0], o[1], o[2], o[3]);
+    if (lane == 0) {
+        so[grp][D] = M;
+        so[grp][D + 1] = Lsum;
+    }
+    __syncthreads();
+    if (grp != 0) return;
+#pragma unroll
+    for (int i = 1; i < G; ++i) M = fmaxf(M, so[i][D]);
+    const float mu = M == -INFINITY ? 0.0f : M;
+    Lsum = 0.0f;
+    o[0] = o[1] = o[2] = o[3] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < G; ++i) {
+        const float f = __builtin_amdgcn_exp2f(so[i][D] - mu);
+        const float4 v = *reinterpret_cast<const float4 *>(&so[i][lane * 4]);
+        Lsum += so[i][D + 1] * f;
+        o[0] += v.x * f;
+        o[1] += v.y * f;
+        o[2] += v.z * f;
+        o[3] += v.w * f;
+    }
+    const float inv = Lsum == 0.0f ? 0.0f : 1.0f / Lsum;
     const int64_t out = (int64_t)(sp.qbeg + row / p.g) * a.hq + head * p.g + row % p.g;
-    if constexpr (E == 2)
-        *reinterpret_cast<uint32_t *>(a.o + out * D + lane * 2) = bf16_pack2(o[0] * inv, o[1] * inv);
-    else
-        a.o[out * D + lane] = (uint16_t)bf16_pack2(o[0] * inv, 0.0f);
-    if (a.lse && lane == 0) a.lse[out] = L == 0.0f ? -INFINITY : (M + __builtin_amdgcn_logf(L)) * LN2;
+    *reinterpret_cast<uint2 *>(a.o + out * D + lane * 4) =
+        make_uint2(bf16_pack2(o[0] * inv, o[1] * inv), bf16_pack2(o[2] * inv, o[3] * inv));
+    if (a.lse && lane == 0) a.lse[out] = Lsum == 0.0f ? -INFINITY : (M + __builtin_amdgcn_logf(Lsum)) * LN2;
 }
 
 namespace {
+
 constexpr int64_t WANT = 1024;  // workgroups of a call, where its tokens allow: four a CU
-// The split of a call along the tokens: WANT workgroups in all, each with at least one round of its
-// waves' tiles.
-void plan(int b, int max_q, int hq, const Kv4Geom &g, int width, int window, DecArgs &p) {
-    p.g = hq / g.hkv;
-    p.rt = (int)(((int64_t)max_q * p.g + 15) / 16);
-    const int64_t groups = (int64_t)b * g.hkv * p.rt, unit = NW * TT;
-    int64_t span = (int64_t)width << g.page_log2;
-    if (window) span = std::min<int64_t>(span, (int64_t)window + 16 / p.g + 1 + TT);  // + the start's rounding down
-    int64_t splits = (WANT + groups - 1) / groups;
-    splits = std::max<int64_t>(1, std::min(splits, (span + unit - 1) / unit));
+constexpr int64_t FAR = 1024;   // tokens after which a workgroup's share is split all the same ...
+constexpr int64_t FAR_SPLITS = 64;  // ... into at most this many: sequences of unlike lengths balance
+
+// Rows and tiles of a call: up to FEW rows a (sequence, head) go to the decode kernel.
+void tiles_of(int max_q, int g, DecArgs &p) {
+    const int64_t rows = (int64_t)max_q * g;
+    p.g = g;
+    p.tr = rows > FEW ? CR : 16;
+    p.pr = (int)std::min<int64_t>(rows, p.tr);
+    p.rt = (int)((rows + p.tr - 1) / p.tr);
+}
+// The split of a call along `span` tokens, at most (it does not fall as the span grows).
+int64_t splits_of(const DecArgs &p, int64_t groups, int64_t span) {
+    const int64_t unit = p.tr == CR ? CT : NW * TT, want = p.tr == CR ? WANT / 2 : WANT;
+    int64_t splits = (want + groups - 1) / groups;
+    if (p.tr != CR) splits = std::max(splits, std::min((span + FAR - 1) / FAR, FAR_SPLITS));
+    return std::max<int64_t>(1, std::min(splits, (span + unit - 1) / unit));
+}
+void plan(const Kv4Attn &a, DecArgs &p) {
+    tiles_of(a.max_q, a.hq / a.geo.hkv, p);
+    const int64_t groups = (int64_t)a.b * a.geo.hkv * p.rt, unit = p.tr == CR ? CT : NW * TT;
+    int64_t span = (int64_t)a.width << a.geo.page_log2;
+    // a window's span: that of the tile's first to its last query, and the start's rounding down
+    if (a.window) span = std::min<int64_t>(span, (int64_t)a.window + p.tr / p.g + 1 + CT);
+    const int64_t splits = splits_of(p, groups, span);
     const int64_t chunk = ((span + splits - 1) / splits + unit - 1) / unit * unit;
     p.chunk = (int)chunk;
     p.splits = (int)((span + chunk - 1) / chunk);
 }
+
 }  // namespace
 
 // Enough for every window: a window only shortens the span, so the bound on the splits falls.
 size_t kv4_attn_ws_bytes(int b, int max_q, int hq, const Kv4Geom &g, int width) {
-    const int64_t rt = ((int64_t)max_q * (hq / g.hkv) + 15) / 16, groups = (int64_t)b * g.hkv * rt, unit = NW * TT;
-    const int64_t splits = std::min((WANT + groups - 1) / groups, (((int64_t)width << g.page_log2) + unit - 1) / unit);
-    return splits <= 1 ? 0 : (size_t)(groups * splits) * 16 * (g.d + 4) * 4;
+    DecArgs p;
+    tiles_of(max_q, hq / g.hkv, p);
+    const int64_t groups = (int64_t)b * g.hkv * p.rt, splits = splits_of(p, groups, (int64_t)width << g.page_log2);
+    return splits <= 1 ? 0 : (size_t)(groups * splits) * p.pr * (g.d + 4) * 4;
 }
 
 hipError_t launch_kv4_attn(const Kv4Attn &a, hipStream_t s) {
     DecArgs p;
     p.a = a;
     p.c = a.scale * LOG2E;
-    plan(a.b, a.max_q, a.hq, a.geo, a.width, a.window, p);
+    plan(a, p);
     const int64_t tiles = (int64_t)a.b * p.rt * a.geo.hkv;
     const dim3 grid((unsigned)(tiles * p.splits));
-    if (a.geo.d == 128) hipLaunchKernelGGL(k_kv4_decode<128>, grid, dim3(64 * NW), 0, s, p);
-    else hipLaunchKernelGGL(k_kv4_decode<64>, grid, dim3(64 * NW), 0, s, p);
+    if (p.tr == CR) {
+        if (a.geo.d == 128) hipLaunchKernelGGL(k_kv4_chunk<128>, grid, dim3(256), 0, s, p);
+        else hipLaunchKernelGGL(k_kv4_chunk<64>, grid, dim3(256), 0, s, p);
+    } else {
+        if (a.geo.d == 128) hipLaunchKernelGGL(k_kv4_decode<128>, grid, dim3(64 * NW), 0, s, p);
+        else hipLaunchKernelGGL(k_kv4_decode<64>, grid, dim3(64 * NW), 0, s, p);
+    }
     hipError_t e = hipGetLastError();
     if (e == hipSuccess && p.splits > 1) {
-        const dim3 jg((unsigned)(tiles * 4));
+        const dim3 jg((unsigned)(tiles * p.pr));
         if (a.geo.d == 128) hipLaunchKernelGGL(k_kv4_join<128>, jg, dim3(256), 0, s, p);
         else hipLaunchKernelGGL(k_kv4_join<64>, jg, dim3(256), 0, s, p);
         e = hipGetLastError();

@@ -217,6 +217,46 @@ def test_bad_pages_are_masked():
                 assert np.abs(f64(lse)[row] - wl[0]).max() <= 1e-3
 
 
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+def test_largest_finite_values(dt):
+    """Values next to the type's largest read back finite, and as tokens that a row does not see they
+    leave it as it was."""
+    big = torch.finfo(DT[dt]).max
+    for qlens in ([3], [50]):
+        c = Case([90], qlens, 4, 2, 128, 32, width=4)
+        base = c.run(window=40)
+        x = torch.full((2, 2, 128), big, dtype=DT[dt])
+        x[1] = -x[1]
+        slots = torch.tensor([int(c.table[0, 2]) * 32 + 27, int(c.table[0, 0]) * 32], device=DEV)  # tokens 91 and 0
+        fp4.kv4_write(c.cache, x.to(DEV), x.to(DEV), slots)
+        for t in fp4.kv4_read(c.cache, slots, out_dtype=torch.float32):
+            assert np.array_equal(f64(t), np.copysign(3 * 2.0 ** 126, f64(x)))
+        o, lse = c.run(window=40)
+        rows = slice(1, None) if qlens == [50] else slice(0, None)  # of 50, the first query's window ends at token 1
+        assert torch.equal(o[rows], base[0][rows]) and torch.equal(lse[rows], base[1][rows])
+
+
+@pytest.mark.parametrize("qlens", [[2, 1], [30, 41]])
+@pytest.mark.parametrize("d", [64, 128])
+def test_negative_scale(qlens, d):
+    Case([150, 333], qlens, 6, 2, d, 16).check(scale=-0.07)
+
+
+def test_more_queries_than_stated():
+    """A sequence with more queries than max_q: the first max_q are computed, nothing else is written."""
+    for qlens, mq in (([9, 2], 3), ([80, 40], 40)):
+        c = Case([200, 120], qlens, 4, 2, 64, 16)
+        want = c.run()
+        ws = torch.zeros(fp4.kv4_attention_workspace(c.q.to(DEV), c.cache, c.table.to(DEV), mq).numel() + 65536,
+                         dtype=torch.uint8, device=DEV)
+        n = ws.numel() - 65536
+        o, lse = c.run(max_q=mq, ws=ws[:n])
+        rows = torch.cat([torch.arange(mq), torch.arange(c.starts[1], c.starts[1] + min(mq, qlens[1]))])
+        assert torch.allclose(o[rows].float(), want[0][rows].float(), atol=2.0 ** -5, rtol=2.0 ** -6)
+        assert torch.allclose(lse[rows], want[1][rows], atol=1e-4)
+        assert int(ws[n:].max()) == 0
+
+
 def test_q_strides_and_defaults():
     """Queries inside the fused projection's rows; no q_start; a wider table; no lse."""
     c = Case([100, 3, 64], [1, 1, 1], 8, 2, 64, 16)
