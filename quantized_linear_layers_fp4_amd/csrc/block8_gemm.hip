@@ -9,13 +9,13 @@
 // register and the instruction selects the byte.
 //
 // Workgroup: 4 waves as 2 x 2, each W x W tiles of 32 x 32 (V_MFMA_SCALE_F32_32X32X64_F8F6F4), so
-// 64 W rows and columns.  K advances in slices of 64 (one step of the instruction), which travel
-// straight to one of four LDS buffers, three slices ahead; the fragments of a slice are read under the
-// matrix work of the one before it, so one barrier a slice is all that the waves wait for.  W = 4 is
-// persistent (one workgroup a CU): the next tile's first slices are on their way while a tile's results
-// are stored, and its stores drain under the next tile's products.  The product is formed
-// transposed, so a lane holds four consecutive columns of one row; the tiles are turned to row order
-// through LDS and stored 16 bytes a lane.
+// 64 W rows and columns.  A stage is one block of 128 along K (a whole cache line a row) of both
+// operands, loaded straight to LDS; the fragments of a step of 64 are read under the matrix work of the
+// one before it, and a stage's buffer is refilled as soon as its second step's fragments are read, so a
+// stage has one barrier.  W = 4 is persistent (one workgroup a CU): the next tile's first stages are on
+// their way while a tile's results are stored, and its stores drain under the next tile's products.
+// The product is formed transposed, so a lane holds four consecutive columns of one row; the tiles are
+// turned to row order through LDS and stored 16 bytes a lane.
 #include <type_traits>
 
 #include "block8.h"
@@ -83,12 +83,12 @@ __device__ __forceinline__ void mma_exact(v16f (&acc)[WI][WJ], const v8i (&a)[WI
     }
 }
 
-// One wave's share of a slice of an operand: W loads of 1 KiB, straight to LDS.
-template <int W>
+// One wave's share of a stage of an operand: L loads of 1 KiB, straight to LDS.
+template <int L>
 __device__ __forceinline__ void rows_to_lds(const uint8_t *base, int bytes, uint8_t *buf, const int *off, int koff) {
     const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(base), 0, bytes, BUF_FLAGS);
 #pragma unroll
-    for (int j = 0; j < W; ++j)
+    for (int j = 0; j < L; ++j)
         __builtin_amdgcn_raw_ptr_buffer_load_lds(r, LDS_PTR(buf + j * 1024), 16, off[j], koff, 0, 0);
 }
 
@@ -112,15 +112,17 @@ __device__ __forceinline__ void mma(v16f (&acc)[WI][WJ], const v8i (&a)[WI], con
 }  // namespace
 
 template <int YDT, int W>
-__global__ __launch_bounds__(256, W == 4 ? 1 : W == 2 ? 2 : 4) void k_block8_gemm(Args8 p) {
-    constexpr int T = 64 * W, OP = T * 64, SLICE = 2 * OP;
-    constexpr bool WALK = W == 4;       // persistent
-    constexpr int D = 2 * W;            // loads to LDS a wave issues a slice, and scale loads a pair of blocks
+__global__ __launch_bounds__(256, W == 4 ? 1 : 2) void k_block8_gemm(Args8 p) {
+    constexpr int T = 64 * W, OP = T * 128, STAGE = 2 * OP;
+    constexpr bool WALK = W == 4;             // persistent
+    constexpr int NST = W == 1 ? 4 : 2;       // stage buffers
+    constexpr int D = 4 * W, S = 2 * W;       // a wave's loads to LDS a stage, and its scale loads a pair of blocks
     constexpr int PATCH = 32 * 144;
-    __shared__ __attribute__((aligned(1024))) uint8_t sb0[SLICE < 4 * PATCH && !WALK ? 4 * PATCH : SLICE];
-    __shared__ __attribute__((aligned(1024))) uint8_t sb1[SLICE];
-    __shared__ __attribute__((aligned(1024))) uint8_t sb2[SLICE];
-    __shared__ __attribute__((aligned(1024))) uint8_t sb3[SLICE];
+    // arrays of their own: the compiler would make a read wait for every load on its way into the same one
+    __shared__ __attribute__((aligned(1024))) uint8_t sm0[STAGE < 4 * PATCH && !WALK ? 4 * PATCH : STAGE];
+    __shared__ __attribute__((aligned(1024))) uint8_t sm1[STAGE];
+    __shared__ __attribute__((aligned(1024))) uint8_t sm2[NST > 2 ? STAGE : 16];
+    __shared__ __attribute__((aligned(1024))) uint8_t sm3[NST > 2 ? STAGE : 16];
     __shared__ __attribute__((aligned(16))) uint8_t own_patch[WALK ? 4 * PATCH : 16];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -142,15 +144,15 @@ __global__ __launch_bounds__(256, W == 4 ? 1 : W == 2 ? 2 : 4) void k_block8_gem
     origin(lg, m0, n0);
 
     // Descriptors start at a tile's first row: offsets stay small whatever the operand's size, and rows
-    // past the matrix read zeros.  A slice past the contraction's end (or past the last tile) has an
-    // empty descriptor and reads zeros.  1 KiB (16 rows of 64 bytes) a load: lane l fills 16-byte place l of
-    // it, row l / 4 at place l % 4, whose chunk is turned by the row's bits 2 and 3, so that 16
+    // past the matrix read zeros.  A stage past the contraction's end (or past the last tile) has an
+    // empty descriptor and reads zeros.  1 KiB (8 rows of 128 bytes) a load: lane l fills 16-byte place l of
+    // it, row l / 8 at place l % 8, whose chunk is turned by the row's bits 1 to 3, so that 16
     // consecutive rows of one chunk lie on 16 distinct places modulo 16.
     const int ldA = (int)p.A.ld, ldB = (int)p.B.ld;
-    int offA[W], offB[W];
+    int offA[2 * W], offB[2 * W];
 #pragma unroll
-    for (int j = 0; j < W; ++j) {
-        const int row = (wave * W + j) * 16 + (lane >> 2), ch = ((lane & 3) ^ ((lane >> 4) & 3)) * 16;
+    for (int j = 0; j < 2 * W; ++j) {
+        const int row = (wave * 2 * W + j) * 8 + (lane >> 3), ch = ((lane & 7) ^ ((row >> 1) & 7)) * 16;
         offA[j] = row * ldA + ch;
         offB[j] = row * ldB + ch;
     }
@@ -163,22 +165,22 @@ __global__ __launch_bounds__(256, W == 4 ? 1 : W == 2 ? 2 : 4) void k_block8_gem
                    (int)min((int64_t)T, p.N - n) * ldB};
     };
     auto dma = [&](uint8_t *buf, Src s, int koff, bool in) {
-        rows_to_lds<W>(s.a, in ? s.na : 0, buf + wave * W * 1024, offA, koff);
-        rows_to_lds<W>(s.b, in ? s.nb : 0, buf + OP + wave * W * 1024, offB, koff);
+        rows_to_lds<2 * W>(s.a, in ? s.na : 0, buf + wave * W * 2048, offA, koff);
+        rows_to_lds<2 * W>(s.b, in ? s.nb : 0, buf + OP + wave * W * 2048, offB, koff);
     };
-    // lane l: row l % 32 of a tile, 32 consecutive values from 32 (l / 32)
-    const int at0 = (lane & 31) * 64 + (((2 * (lane >> 5)) ^ ((lane >> 2) & 3)) << 4), at1 = at0 ^ 16;
-    auto frags = [&](const uint8_t *buf, v8i (&a)[W], v8i (&b)[W]) {
+    // step h of a stage; lane l: row l % 32 of a tile, 32 consecutive values from 64 h + 32 (l / 32)
+    const int at = (lane & 31) * 128 + (((2 * (lane >> 5)) ^ ((lane >> 1) & 7)) << 4);
+    auto frags = [&](const uint8_t *buf, int h, v8i (&a)[W], v8i (&b)[W]) {
+        const uint8_t *sa_ = buf + wm * W * 4096, *sb_ = buf + OP + wn * W * 4096;
+        const int x0 = at ^ (h * 64), x1 = x0 ^ 16;
 #pragma unroll
         for (int i = 0; i < W; ++i) {
-            const uint8_t *t = buf + (wm * W + i) * 2048;
-            const u32x4 x = *reinterpret_cast<const u32x4 *>(t + at0), y = *reinterpret_cast<const u32x4 *>(t + at1);
+            const u32x4 x = *reinterpret_cast<const u32x4 *>(sa_ + i * 4096 + x0), y = *reinterpret_cast<const u32x4 *>(sa_ + i * 4096 + x1);
             a[i] = v8i{(int)x.x, (int)x.y, (int)x.z, (int)x.w, (int)y.x, (int)y.y, (int)y.z, (int)y.w};
         }
 #pragma unroll
         for (int j = 0; j < W; ++j) {
-            const uint8_t *t = buf + OP + (wn * W + j) * 2048;
-            const u32x4 x = *reinterpret_cast<const u32x4 *>(t + at0), y = *reinterpret_cast<const u32x4 *>(t + at1);
+            const u32x4 x = *reinterpret_cast<const u32x4 *>(sb_ + j * 4096 + x0), y = *reinterpret_cast<const u32x4 *>(sb_ + j * 4096 + x1);
             b[j] = v8i{(int)x.x, (int)x.y, (int)x.z, (int)x.w, (int)y.x, (int)y.y, (int)y.z, (int)y.w};
         }
     };
@@ -202,75 +204,82 @@ __global__ __launch_bounds__(256, W == 4 ? 1 : W == 2 ? 2 : 4) void k_block8_gem
     v8i a0[W], b0[W], a1[W], b1[W];
     uint32_t sa[W], sb[W], ta[W], tb[W];
     Src cur = source(m0, n0);
-    // slices 0..3 of the first tile, and its first scales, in the order of the loop
-    dma(sb0, cur, 0, true);
-    dma(sb1, cur, 64, true);
+    // the first stages and scales, in the order of the loop
+    dma(sm0, cur, 0, true);
     __builtin_amdgcn_sched_barrier(0);
     scales(m0, n0, 0, ta, tb);
     __builtin_amdgcn_sched_barrier(0);
-    dma(sb2, cur, 128, 1 < p.KB);
-    dma(sb3, cur, 192, 1 < p.KB);
+    dma(sm1, cur, 128, 1 < p.KB);
+    if constexpr (NST > 2) {
+        dma(sm2, cur, 256, 2 < p.KB);
+        dma(sm3, cur, 384, 3 < p.KB);
+    }
     __builtin_amdgcn_sched_barrier(0);
-    wait_vm<4 * D>();  // slice 0 has landed: slices 1..3 and the scales came after it
+    wait_vm<(NST - 1) * D + S>();  // stage 0 has landed: the others and the scales came after it
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
-    frags(sb0, a0, b0);
+    frags(sm0, 0, a0, b0);
 
-    // One slice: (a, b) hold its fragments.  The wait leaves NW loads in flight, those issued after
-    // the next slice's; then everyone's part of the next slice has landed and everyone holds its
-    // fragments of this one, whose buffer takes the slice four further on.
-    auto slice = [&](auto nw, auto kk, uint8_t *buf, const uint8_t *nbuf, const v8i (&a)[W], const v8i (&b)[W],
-                     v8i (&na)[W], v8i (&nb)[W], Src src, int koff, bool in, auto &&before) {
+    // One block: (a0, b0) hold its first step's fragments.  At the barrier everyone holds the second step's,
+    // so the buffer takes the stage NST further on, and the wait, which leaves NW loads in flight (those
+    // issued after the next stage's), has made everyone's part of the next stage land.
+    auto block = [&](auto nw, auto kk, uint8_t *buf, const uint8_t *nbuf, Src src, int koff, bool in, auto &&before) {
+        constexpr int KK = decltype(kk)::value;
+        __builtin_amdgcn_sched_barrier(0);
+        before();
+        frags(buf, 1, a1, b1);
+        if constexpr (YDT == DT_F32) mma_exact<KK, W, W>(acc, a0, b0, sa, sb);
+        else mma<KK, W, W>(acc, a0, b0, sa, sb);
+        if constexpr (W == 4 && YDT == DT_BF16) {
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // matrix instruction
+                __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);  // LDS read
+            }
+            __builtin_amdgcn_sched_group_barrier(0x008, 8, 0);
+        }
         __builtin_amdgcn_sched_barrier(0);
         wait_vm<decltype(nw)::value>();
         __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
         __builtin_amdgcn_s_barrier();
         __builtin_amdgcn_sched_barrier(0);
-        before();
         dma(buf, src, koff, in);
-        frags(nbuf, na, nb);
-        constexpr int KK = decltype(kk)::value;
-        if constexpr (YDT == DT_F32) {
-            mma_exact<KK, W, W>(acc, a, b, sa, sb);
-        } else {
-            mma<KK, W, W>(acc, a, b, sa, sb);
-            if constexpr (W == 4) {
+        frags(nbuf, 0, a0, b0);
+        if constexpr (YDT == DT_F32) mma_exact<KK, W, W>(acc, a1, b1, sa, sb);
+        else mma<KK, W, W>(acc, a1, b1, sa, sb);
+        if constexpr (W == 4 && YDT == DT_BF16) {
 #pragma unroll
-                for (int q = 0; q < 8; ++q) {
-                    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // matrix instruction
-                    __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);  // LDS read
-                    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-                    __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);  // load to LDS
-                }
+            for (int q = 0; q < 16; ++q) {
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                if (q < 8) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+                __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);  // load to LDS
             }
         }
         __builtin_amdgcn_sched_barrier(0);
     };
-    // Two blocks: four slices.  The scales of the next pair (tile (sm, sn), pair sit) are fetched between
-    // slice 1's loads and slice 2's, so a wait sees, of the loads issued after those it is for, two
-    // slices' and, in slices 3 and 0, the scales' too.  FRESH: the STORES stores of the tile before lie
-    // behind slice 3's loads, and the first three waits leave them in flight.
+    // Two blocks.  The scales of the next pair (tile (sm, sn), pair sit) are fetched at the second's start.
+    // What was issued after the next block's stage: NST - 2 stages, and the scales of the pairs begun
+    // since; in a workgroup's first pair (FIRST) not even those.  FRESH: the STORES stores of the tile
+    // before lie behind its last loads.
     constexpr int STORES = W == 4 ? 32 : 0;
-    using I0 = std::integral_constant<int, 0>;
-    using I1 = std::integral_constant<int, 1>;
-    auto pair = [&](auto fresh, int it, Src src, int koff, bool in, bool in2, int64_t sm, int64_t sn, int sit) {
-        constexpr int E = decltype(fresh)::value ? STORES : 0;
+    constexpr int NORMAL = 0, FIRST = 1, FRESH = 2;
+    auto pair = [&](auto mode, uint8_t *u0, uint8_t *u1, const uint8_t *u2, int it, Src src, int koff, bool in, bool in2, int64_t sm_, int64_t sn, int sit) {
+        constexpr int MODE = decltype(mode)::value;
+        constexpr int W0 = (NST - 2) * D + (MODE == FIRST ? 0 : (NST - 2) / 2 * S) + (MODE == FRESH ? STORES : 0);
+        constexpr int W1 = (NST - 2) * D + (MODE == FIRST && NST > 2 ? 0 : NST / 2 * S);
         // a block past the end gets 2^0: its codes are zeros, but its scale byte is not written
-        const bool whole = 2 * it + 1 < p.KB;
-        const uint32_t keep = whole ? 0xFFFFu : 0xFFu, fill = whole ? 0u : 0x7F00u;
+        const bool both = 2 * it + 1 < p.KB;
+        const uint32_t keep = both ? 0xFFFFu : 0xFFu, fill = both ? 0u : 0x7F00u;
 #pragma unroll
         for (int i = 0; i < W; ++i) {
             sa[i] = (ta[i] & keep) | fill;
             sb[i] = (tb[i] & keep) | fill;
         }
-        auto none = [] {};
-        slice(std::integral_constant<int, 3 * D + E>{}, I0{}, sb0, sb1, a0, b0, a1, b1, src, koff, in, none);
-        slice(std::integral_constant<int, 2 * D + E>{}, I0{}, sb1, sb2, a1, b1, a0, b0, src, koff + 64, in, none);
-        slice(std::integral_constant<int, 2 * D + E>{}, I1{}, sb2, sb3, a0, b0, a1, b1, src, koff + 128, in2, [&] {
-            scales(sm, sn, sit, ta, tb);
+        block(std::integral_constant<int, W0>{}, std::integral_constant<int, 0>{}, u0, u1, src, koff, in, [] {});
+        block(std::integral_constant<int, W1>{}, std::integral_constant<int, 1>{}, u1, u2, src, koff + 128, in2, [&] {
+            scales(sm_, sn, sit, ta, tb);
             __builtin_amdgcn_sched_barrier(0);
         });
-        slice(std::integral_constant<int, 3 * D>{}, I1{}, sb3, sb0, a1, b1, a0, b0, src, koff + 192, in2, none);
     };
 
     bool fresh = false;
@@ -286,23 +295,30 @@ __global__ __launch_bounds__(256, W == 4 ? 1 : W == 2 ? 2 : 4) void k_block8_gem
             for (int j = 0; j < W; ++j)
 #pragma unroll
                 for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
-        // pair `it` is multiplied while pair it + 1, or the next tile's first, is fetched
-        auto run = [&](auto f, int it) {
-            const bool end = it + 1 == iters;
-            const int kb = end ? 0 : 2 * it + 2;  // first block fetched
-            const Src src{pick(end, nxt.a, cur.a), pick(end, nxt.b, cur.b), pick(end, nxt.na, cur.na), pick(end, nxt.nb, cur.nb)};
-            pair(f, it, src, kb * 128, !end || more, end ? more && p.KB > 1 : kb + 1 < p.KB, pick(end, nm0, m0),
+        // pair `it` is multiplied while the stages NST blocks on, or the next tile's first, are fetched
+        auto run = [&](auto mode, uint8_t *u0, uint8_t *u1, const uint8_t *u2, int it) {
+            const bool end = it + 1 == iters, far = 2 * it + NST >= 2 * iters;  // far: past this tile
+            const int kb = far ? 2 * it + NST - 2 * iters : 2 * it + NST;       // first block fetched
+            const Src src{pick(far, nxt.a, cur.a), pick(far, nxt.b, cur.b), pick(far, nxt.na, cur.na), pick(far, nxt.nb, cur.nb)};
+            pair(mode, u0, u1, u2, it, src, kb * 128, (!far || more) && kb < p.KB, (!far || more) && kb + 1 < p.KB, pick(end, nm0, m0),
                  pick(end, nn0, n0), end ? 0 : it + 1);
         };
+        using Normal = std::integral_constant<int, NORMAL>;
         int it = 0;
-        if constexpr (WALK) {
-            if (fresh) {
-                run(std::true_type{}, 0);
+        if constexpr (NST > 2) {
+            run(std::integral_constant<int, FIRST>{}, sm0, sm1, sm2, 0);
+            for (it = 1; it < iters; it += 2) {
+                run(Normal{}, sm2, sm3, sm0, it);
+                if (it + 1 < iters) run(Normal{}, sm0, sm1, sm2, it + 1);
+            }
+        } else {
+            if (WALK && fresh) {
+                run(std::integral_constant<int, FRESH>{}, sm0, sm1, sm0, 0);
                 it = 1;
             }
+            for (; it < iters; ++it) run(Normal{}, sm0, sm1, sm0, it);
         }
-        for (; it < iters; ++it) run(std::false_type{}, it);
-        if constexpr (!WALK) {  // the patches lie in slice buffers: nothing may land there any more
+        if constexpr (!WALK) {  // the patches lie in stage buffers: nothing may land there any more
             wait_vm<0>();
             __builtin_amdgcn_s_waitcnt(0xC07F);
             __builtin_amdgcn_s_barrier();
@@ -335,7 +351,7 @@ __global__ __launch_bounds__(256, W == 4 ? 1 : W == 2 ? 2 : 4) void k_block8_gem
                         for (int q = 0; q < 4; ++q) {
                             const v16f &x = acc[i][j0 + t];
                             const int at = wave * PATCH + (lane & 31) * 144 + (t * 32 + 8 * q + 4 * (lane >> 5)) * ES;
-                            uint8_t *d = (WALK ? own_patch : sb0) + at;
+                            uint8_t *d = (WALK ? own_patch : sm0) + at;
                             if constexpr (YDT == DT_BF16)
                                 *reinterpret_cast<u32x2 *>(d) =
                                     u32x2{bf16_pack2(x[4 * q], x[4 * q + 1]), bf16_pack2(x[4 * q + 2], x[4 * q + 3])};
@@ -350,7 +366,7 @@ __global__ __launch_bounds__(256, W == 4 ? 1 : W == 2 ? 2 : 4) void k_block8_gem
                     uint8_t *base = static_cast<uint8_t *>(p.Y) + (row * p.N + col) * ES;
 #pragma unroll
                     for (int k = 0; k < 32 / RK; ++k) {
-                        const u32x4 o = *reinterpret_cast<const u32x4 *>((WALK ? own_patch : sb0) + wave * PATCH +
+                        const u32x4 o = *reinterpret_cast<const u32x4 *>((WALK ? own_patch : sm0) + wave * PATCH +
                                                                          (k * RK + lane / CHUNKS) * 144 + lane % CHUNKS * 16);
                         uint8_t *y = base + k * RK * p.N * ES + loff;
                         const int rows = (int)min(p.M - row - k * RK, (int64_t)RK);  // may be <= 0, as cols
