@@ -25,7 +25,7 @@ HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 
 SOURCES = ["abi.cpp", "quant.hip", "gemm.hip", "comp.hip", "escape.hip", "emu.hip", "fp8codec.hip", "bwd.hip", "noalloc.hip",
-           "block_abi.cpp", "block8.hip", "block8_gemm.hip", "kv4.hip", "kv4_attn.hip"]
+           "block_abi.cpp", "block8.hip", "block8_gemm.hip", "block8_few.hip", "kv4.hip", "kv4_attn.hip"]
 
 FLAGS = [
     f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC",

@@ -28,6 +28,30 @@ hipError_t launch_block8_dequant(const uint8_t *codes, const uint8_t *scales, in
 hipError_t launch_block8_gemm(const Op8 &A, const Op8 &B, int64_t M, int64_t N, int64_t K, void *Y, int y_dt, int cus,
                               hipStream_t s);
 
+// The same for few rows of A, and with A (X, rows ldx apart) quantized on the way.
+// Where: measured on a bf16 layer with the weight out of the caches, few rows' kernel | tiles of 64 x 64,
+// us, at (K, N) = (4096, 22016): 24.3 | 25.8 for 16 rows, 31.3 | 26.7 for 32; (4096, 12288): 14.1 | 14.6 for
+// 16, 20.3 | 14.7 for 32; (2048, 6144): 9.9 | 9.3 for 32, 13.5 | 9.7 for 64; (4096, 4096): 12.9 | 13.8 for 64;
+// (11008, 4096): 12.0 | 27.6 for one, 21.8 | 29.3 for 64.  Its work grows with the rows, in steps of 16;
+// the tiles' is a chain of K / 128 loads until they fill the device.
+inline bool block8_few(int64_t M, int64_t N) {
+    return M <= 64 && (N + 15) / 16 * (M <= 16 ? 1 : M <= 32 ? 2 : 4) <= 1024;
+}
+// Quantizing in every workgroup instead of once: 20.4 | 26.9 us for one row at (4096, 22016), where four
+// rows are 27.0 | 26.8; with a workgroup or two a CU it is the shorter way up to 128 blocks (8.8 | 9.5 for four
+// rows at (4096, 4096)), which is also what fits beside the patches.
+inline bool block8_few_direct(int64_t M, int64_t N, int64_t K) {
+    return M * ((K + 127) / 128) <= 128 && M <= ((N + 15) / 16 <= 512 ? 16 : 2);
+}
+hipError_t launch_block8_few(const Op8 &A, const Op8 &B, int64_t M, int64_t N, int64_t K, void *Y, int y_dt, hipStream_t s);
+hipError_t launch_block8_few_direct(const void *X, int x_dt, int64_t ldx, const Op8 &B, int64_t M, int64_t N, int64_t K,
+                                    void *Y, int y_dt, hipStream_t s);
+
+typedef int v8i __attribute__((ext_vector_type(8)));
+typedef float v4f __attribute__((ext_vector_type(4)));
+typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
+typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+
 // Loads and stores at the element's own alignment (global memory takes any on gfx950).
 typedef unsigned int ua_u32x4 __attribute__((ext_vector_type(4), aligned(2)));
 
@@ -103,4 +127,22 @@ __device__ __forceinline__ uint32_t amax8(const float v[8]) {
     return m;
 }
 
+// Operands of a product with fp32 output, on the bf16 instruction at half the rate.  The scaled E4M3
+// instruction aligns its products in groups of eight to the largest and drops what lies 14 or more
+// binary places below (measured: 1.4e-5 of the result on normal data, 5e-5 with outlier channels),
+// which a bf16 output (2^-9) does not see and an fp32 one does.  E4M3 values times their power of two
+// are exact in bf16, and the conversion applies the scale.
+template <int KK>
+__device__ __forceinline__ void to_bf16(const v8i &x, uint32_t s, v8bf (&f)[4]) {
+    const float sc = __uint_as_float(((s >> (8 * KK)) & 255u) << 23);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        u32x4 w;
+        w[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x[2 * q], sc, false));
+        w[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x[2 * q], sc, true));
+        w[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x[2 * q + 1], sc, false));
+        w[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x[2 * q + 1], sc, true));
+        f[q] = __builtin_bit_cast(v8bf, w);
+    }
+}
 }  // namespace fp4

@@ -22,11 +22,8 @@
 
 namespace fp4 {
 
-typedef int v8i __attribute__((ext_vector_type(8)));
 typedef float v16f __attribute__((ext_vector_type(16)));
-typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
-typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 #define LDS_PTR(p) ((__attribute__((address_space(3))) void *)(p))
 
 namespace {
@@ -47,24 +44,7 @@ __device__ __forceinline__ void wait_vm() {
     __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | 0x0F70);
 }
 
-// fp32 outputs: the same product on the bf16 instruction, at half the rate.  The scaled E4M3
-// instruction aligns its products in groups of eight to the largest and drops what lies 14 or more
-// binary places below (measured: 1.4e-5 of the result on normal data, 5e-5 with outlier channels),
-// which a bf16 output (2^-9) does not see and an fp32 one does.  E4M3 values times their power of two
-// are exact in bf16, and the conversion applies the scale.
-template <int KK>
-__device__ __forceinline__ void to_bf16(const v8i &x, uint32_t s, v8bf (&f)[4]) {
-    const float sc = __uint_as_float(((s >> (8 * KK)) & 255u) << 23);
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        u32x4 w;
-        w[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x[2 * q], sc, false));
-        w[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x[2 * q], sc, true));
-        w[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x[2 * q + 1], sc, false));
-        w[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x[2 * q + 1], sc, true));
-        f[q] = __builtin_bit_cast(v8bf, w);
-    }
-}
+// fp32 outputs: the product on the bf16 instruction (to_bf16).
 template <int KK, int WI, int WJ>
 __device__ __forceinline__ void mma_exact(v16f (&acc)[WI][WJ], const v8i (&a)[WI], const v8i (&b)[WJ],
                                           const uint32_t (&sa)[WI], const uint32_t (&sb)[WJ]) {
@@ -421,6 +401,7 @@ hipError_t launch_block8_gemm(const Op8 &A, const Op8 &B, int64_t M, int64_t N, 
     p.KB = (int)((K + 127) / 128);
     p.Y = Y;
     p.tilesM = p.tilesN = p.group = 0;
+    if (block8_few(M, N)) return launch_block8_few(A, B, M, N, K, Y, y_dt, s);
     // the largest tile that still gives every CU a workgroup
     auto count = [&](int64_t t) { return ((M + t - 1) / t) * ((N + t - 1) / t); };
     const int w = count(256) >= cus ? 4 : (count(128) >= cus ? 2 : 1);

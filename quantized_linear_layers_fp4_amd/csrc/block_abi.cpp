@@ -113,6 +113,9 @@ fp4_status fp4_block8_linear(const void *X, int32_t x_dtype, int64_t M, int64_t 
     int cus;
     const fp4_status st = device_check(&cus);
     if (st != FP4_OK) return st;
+    if (!xt_codes && block8_few_direct(M, N, K))
+        return hip_status(launch_block8_few_direct(X, dt_in(x_dtype), ldx, op8(w_codes, w_scales, N, K, w_mode), M, N, K, Y,
+                                                   dt_in(y_dtype), hs(stream)));
     uint8_t *xc = static_cast<uint8_t *>(workspace), *xs = xc + up256(fp4_block8_codes_bytes(M, K));
     hipError_t e = launch_block8_quant(X, dt_in(x_dtype), M, K, ldx, false, xc, xs, xt_codes, xt_scales, hs(stream));
     if (e == hipSuccess)

@@ -221,3 +221,48 @@ def test_refusals():
     with pytest.raises(fp4.Fp4Error):
         fp4.block8_linear_forward(x, w, ws=torch.empty(16, dtype=torch.uint8, device=DEV))
     assert fp4.block8_linear_forward(x[:0], w).shape == (0, 8)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+@pytest.mark.parametrize("M", [1, 3, 16, 17, 32, 33, 64, 65])
+@pytest.mark.parametrize("K,N", [(1, 1), (130, 17), (777, 48), (2176, 100), (1000, 1290)])
+def test_few_rows(M, K, N, dt):
+    """A decode batch: few rows, from strided rows at an odd element, with and without the transposed operand."""
+    x, w = data(M, K, DT[dt], M + K), data(K, N, DT[dt], N, 0.02)
+    wide = torch.zeros(M, K + 3, dtype=DT[dt])
+    wide[:, 1:1 + K] = x
+    xs = wide.to(DEV)[:, 1:1 + K]
+    _, wq = fp4.block8_quantize(w.to(DEV), fp4.FP4_BLOCK_SQUARE, rows=False, cols=True)
+    a, b = ref.blocks(f64(x), 1, 128), ref.blocks(f64(w), 128, 128).T
+    for out in (torch.bfloat16, torch.float32):
+        y = fp4.block8_linear_forward(xs, wq, out_dtype=out)
+        check_product(y, a, b, out, K)
+        z, _ = fp4.block8_linear_forward(xs, wq, out_dtype=out, for_backward=True)
+        check_product(z, a, b, out, K)
+        q = fp4.block8_gemm(fp4.block8_quantize(xs)[0], wq, out)
+        assert torch.equal(q, z)
+
+
+def test_few_rows_nonfinite():
+    """A block with a NaN or an infinity makes its row NaN, and no other."""
+    for M in (5, 40):
+        x, w = data(M, 500, torch.bfloat16, 3), data(500, 40, torch.bfloat16, 4, 0.02)
+        x[1, 130], x[3, 499] = float("nan"), float("inf")
+        _, wq = fp4.block8_quantize(w.to(DEV), fp4.FP4_BLOCK_SQUARE, rows=False, cols=True)
+        y = f64(fp4.block8_linear_forward(x.to(DEV), wq))
+        bad = np.zeros(M, bool)
+        bad[[1, 3]] = True
+        assert np.isnan(y[bad]).all() and np.isfinite(y[~bad]).all()
+
+
+@pytest.mark.parametrize("M,N,K", [(4097, 4100, 300), (4200, 4352, 129), (8200, 2100, 640)])
+def test_large_tiles(M, N, K):
+    """More than one 256 x 256 tile a workgroup: ragged edges, an odd number of blocks, both output types."""
+    x, w = data(M, K, torch.bfloat16, 1), data(N, K, torch.bfloat16, 2)
+    a, b = fp4.block8_quantize(x.to(DEV))[0], fp4.block8_quantize(w.to(DEV))[0]
+    va, vb = ref.blocks(f64(x), 1, 128), ref.blocks(f64(w), 1, 128)
+    for out in (torch.bfloat16, torch.float32):
+        y = fp4.block8_gemm(a, b, out)
+        check_product(y, va, vb, out, K)
+        for _ in range(3):
+            assert torch.equal(fp4.block8_gemm(a, b, out), y)
