@@ -19,6 +19,7 @@
 // bf16; P is rounded to bf16 (2^-9 of each term, as the output itself is), the sum of P is taken
 // before that rounding.
 #include <algorithm>
+#include <type_traits>
 
 #include "block8.h"
 #include "kv4.h"
@@ -30,7 +31,6 @@ typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
 
 namespace {
 
-constexpr int NW = 4;        // waves of a decode workgroup
 constexpr int TT = 32;       // tokens a wave takes at once
 constexpr int CR = 128;      // rows of a workgroup of the many-rows kernel: 32 a wave
 constexpr int CT = 64;       // tokens it takes at once
@@ -41,10 +41,11 @@ constexpr float LOG2E = 1.44269504088896340736f;
 struct DecArgs {
     Kv4Attn a;
     int g, rt;        // heads a group; row tiles a (sequence, head)
-    int tr;           // rows of a tile (16 or CR)
+    int tr;           // rows of a tile: 16 or CR
     int pr;           // rows a partial result holds: min(tr, max_q * g)
+    int nw;           // waves of a workgroup
     int splits;       // workgroups along the tokens
-    int chunk;        // tokens each takes (a multiple of the unit, NW * TT or CT)
+    int chunk;        // tokens each takes (a multiple of the unit, nw * TT or CT)
     float c;          // scale * log2(e)
 };
 
@@ -116,6 +117,11 @@ __device__ __forceinline__ void unpack_cols(const uint32_t (&w)[8], const float 
     c1 = __builtin_bit_cast(v8bf, u32x4{hi[0], hi[1], hi[2], hi[3]});
 }
 
+// The largest of three, NaN if one is: one instruction, where fmaxf would first quiet each operand.  A NaN
+// score that a row sees makes the row NaN in any case.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    return __builtin_elementwise_maximum(__builtin_elementwise_maximum(a, b), c);
+}
 // Largest over the four lanes n, n + 16, n + 32, n + 48, in each of them.
 __device__ __forceinline__ float half_max(float x) {
     const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
@@ -128,11 +134,11 @@ __device__ __forceinline__ float quarter_max(float x) {
 
 }  // namespace
 
-// Few rows (single tokens, drafts): 16 rows of one (sequence, key/value head) a workgroup, its four
+// Few rows (single tokens, drafts): 16 rows of one (sequence, key/value head) a workgroup, its NW
 // waves taking tiles of 32 tokens in turn and joining in LDS; `splits` workgroups share the tokens.
 // Bound by the cache's bytes.
-template <int D>
-__global__ __launch_bounds__(64 * NW, 3) void k_kv4_decode(DecArgs p) {
+template <int D, int NW>
+__global__ __launch_bounds__(64 * NW, NW == 4 ? 3 : 1) void k_kv4_decode(DecArgs p) {
     constexpr int J = D / 16;   // columns a lane owns in the O^T tiles: J n + j
     constexpr int KS = D / 32;  // contraction steps of the scores
     const Kv4Attn &a = p.a;
@@ -253,16 +259,17 @@ __global__ __launch_bounds__(64 * NW, 3) void k_kv4_decode(DecArgs p) {
                 x[i] = tok < hi && tok >= vlo ? x[i] : -INFINITY;
             }
         }
-        float mx = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
-        mx = fmaxf(m, quarter_max(mx));
-        const float mu = mx == -INFINITY ? 0.0f : mx;
-        if (__builtin_amdgcn_ballot_w64(mx != m) != 0) {  // rarely, after a row's first tiles
-            const float alpha = __builtin_amdgcn_exp2f(m - mu);
+        const float mx = fmaxf(m, quarter_max(max3(max3(x[0], x[1], x[2]), max3(x[3], x[4], x[5]), fmaxf(x[6], x[7]))));
+        // the maximum moves only when it would rise by more than 2^8: until then the factors stay below 2^8,
+        // which neither fp32 sums nor a bf16 factor's relative error mind, and nothing is rescaled
+        if (__builtin_amdgcn_ballot_w64(m == -INFINITY ? mx != -INFINITY : mx - m > 8.0f) != 0) {
+            const float alpha = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m - mx);
             m = mx;
             l *= alpha;
 #pragma unroll
             for (int j = 0; j < J; ++j) acc[j] *= alpha;
         }
+        const float mu = m == -INFINITY ? 0.0f : m;
         float e[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) e[i] = __builtin_amdgcn_exp2f(x[i] - mu);
@@ -352,10 +359,10 @@ __global__ __launch_bounds__(256, 2) void k_kv4_chunk(DecArgs p) {
     constexpr int KC = D / 8;     // 16-byte pieces of a token's K row
     constexpr int KS = D / 16;    // contraction steps of the scores
     constexpr int DT = D / 32;    // tiles of 32 columns; dwords of K and tokens of V a thread unpacks
-    __shared__ __attribute__((aligned(16))) uint8_t sk[2][CT * D * 2];
-    __shared__ __attribute__((aligned(16))) uint8_t sv[2][D * CT * 2];
+    __shared__ __attribute__((aligned(16))) uint8_t sk0[CT * D * 2], sv0[D * CT * 2], sk1[CT * D * 2], sv1[D * CT * 2];
     const Kv4Attn &a = p.a;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, n = lane & 31, h = lane >> 5;
+    const int tid = threadIdx.x, lane = tid & 63, n = lane & 31, h = lane >> 5;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     int id = blockIdx.x;
     const int split = id % p.splits; id /= p.splits;
     const int head = id % a.geo.hkv; id /= a.geo.hkv;
@@ -396,17 +403,15 @@ __global__ __launch_bounds__(256, 2) void k_kv4_chunk(DecArgs p) {
     const int vp = tid % VP, vn = tid / VP % (D / 8), vt = tid / VP / (D / 8);
     const int vtok = vt * 8 + vp * DT;
     uint32_t kw[DT], vw[DT], ks, vs;
-    auto page_at = [&](int t) {
-        const int pg = table[min(t, end - 1) >> lg];
-        return (uint32_t)pg < (uint64_t)a.geo.pages ? pg : -1;
-    };
+    const uint8_t *const headp = a.cache + (int64_t)head * region;
+    const int64_t pstride = (int64_t)a.geo.hkv * region;
+    auto page_at = [&](int t) { return table[min(t, end - 1) >> lg]; };
     // pages outside the cache: their tokens' bytes are any page's, and their scores are masked
     bool okk;
-    auto fetch = [&](int t0) {
-        const int pk = page_at(t0 + kt), pv = page_at(t0 + vtok);
-        okk = pk >= 0;
-        const uint8_t *kb = a.cache + ((int64_t)max(pk, 0) * a.geo.hkv + head) * region;
-        const uint8_t *vb = a.cache + ((int64_t)max(pv, 0) * a.geo.hkv + head) * region;
+    auto fetch = [&](int t0, int pk, int pv) {
+        okk = (uint32_t)pk < (uint64_t)a.geo.pages;
+        const bool okv = (uint32_t)pv < (uint64_t)a.geo.pages;
+        const uint8_t *kb = headp + (okk ? pk : 0) * pstride, *vb = headp + (okv ? pv : 0) * pstride;
         const int tk = (t0 + kt) & (P - 1), tv = (t0 + vtok) & (P - 1);
         const uint8_t *ka = kb + tk * (D / 2) + kq * (D / 8);
         const uint8_t *va = vb + a.geo.v_off() + ((tv >> 3) * (D / 8) + vn) * 32 + (tv & 7) * 4;
@@ -432,12 +437,24 @@ __global__ __launch_bounds__(256, 2) void k_kv4_chunk(DecArgs p) {
     // pieces of eight tokens, turned for the reads (32 consecutive columns) and the writes (every eighth)
     auto kpiece = [](int r, int ch) { return D == 128 ? r * 16 + (ch ^ (r & 15)) : r * 8 + (ch ^ ((r >> 1) & 7)); };
     auto vpiece = [](int col, int ch) { return col * 8 + (ch ^ (((col >> 1) ^ (col >> 4)) & 7)); };
+    // the reads' places: row n (+ 32 u: a constant further on) at piece 2 i + h, and column n + 32 j at
+    // piece 2 k + h, where j turns the piece by 2 j
+    int ka[KS], va[4];
+#pragma unroll
+    for (int i = 0; i < KS; ++i) ka[i] = kpiece(n, 2 * i + h) * 16;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) va[i] = vpiece(n, 2 * i + h) * 16;
     const int krow = (kt & ~12) | ((kt & 4) << 1) | ((kt & 8) >> 1);
-    auto unpack = [&](int b) {
+    int kst[DT], vst[8];
+#pragma unroll
+    for (int i = 0; i < DT; ++i) kst[i] = kpiece(krow, kq * DT + i) * 16;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) vst[j] = vpiece(vn * 8 + j, vt) * 16 + vp * DT * 2;
+    auto unpack = [&](uint8_t *dk, uint8_t *dv) {
         v8bf kf[DT];
         unpack_row<DT>(kw, okk ? ks : 0u, kf);
 #pragma unroll
-        for (int i = 0; i < DT; ++i) *reinterpret_cast<v8bf *>(&sk[b][kpiece(krow, kq * DT + i) * 16]) = kf[i];
+        for (int i = 0; i < DT; ++i) *reinterpret_cast<v8bf *>(dk + kst[i]) = kf[i];
         const float sc[4] = {scale_of<0>(vs), scale_of<1>(vs), scale_of<2>(vs), scale_of<3>(vs)};
         uint32_t x[DT][4];
 #pragma unroll
@@ -450,7 +467,7 @@ __global__ __launch_bounds__(256, 2) void k_kv4_chunk(DecArgs p) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const uint32_t sel = j & 1 ? 0x07060302u : 0x05040100u;
-            uint8_t *d = &sv[b][vpiece(vn * 8 + j, vt) * 16 + vp * DT * 2];
+            uint8_t *d = dv + vst[j];
             if constexpr (D == 128)
                 *reinterpret_cast<uint2 *>(d) = make_uint2(__builtin_amdgcn_perm(x[1][j >> 1], x[0][j >> 1], sel),
                                                            __builtin_amdgcn_perm(x[3][j >> 1], x[2][j >> 1], sel));
@@ -468,38 +485,58 @@ __global__ __launch_bounds__(256, 2) void k_kv4_chunk(DecArgs p) {
 
     // whether some page of a tile lies outside the cache, from the waves that unpacked it
     __shared__ uint64_t bad[2][4];
+    // tile t0 is multiplied while t0 + CT is unpacked, t0 + 2 CT's bytes are on their way and the page indices
+    // of t0 + 3 CT
+    int pk = 0, pv = 0;
+    auto pages_of = [&](int t0) {
+        pk = page_at(t0 + kt);
+        pv = page_at(t0 + vtok);
+    };
     if (beg < end) {
-        fetch(beg);
+        pages_of(beg);
+        fetch(beg, pk, pv);
+        pages_of(beg + CT);
         const uint64_t bm = ~__builtin_amdgcn_ballot_w64(okk);
         if (lane == 0) bad[0][wave] = bm;
-        unpack(0);
-        fetch(beg + CT);
+        unpack(sk0, sv0);
+        fetch(beg + CT, pk, pv);
+        pages_of(beg + 2 * CT);
     }
-    int b = 0;
-    for (int t0 = beg; t0 < end; t0 += CT, b ^= 1) {
+    auto tile = [&](auto buf, int t0, const uint8_t *ck, const uint8_t *cv, uint8_t *nk, uint8_t *nv) {
+        constexpr int b = decltype(buf)::value;
         __syncthreads();  // tile t0 is in buffer b, and nobody reads the other any more
-        if (t0 + CT < end) {
+        // the next tile is unpacked whether there is one or not (the fetched bytes are always some page's), so
+        // that it lies beside the products, which are matrix instructions
+        auto next = [&] {
             const uint64_t bm = ~__builtin_amdgcn_ballot_w64(okk);
             if (lane == 0) bad[b ^ 1][wave] = bm;
-            unpack(b ^ 1);
-            fetch(t0 + 2 * CT);
+            unpack(nk, nv);
+            fetch(t0 + 2 * CT, pk, pv);
+            pages_of(t0 + 3 * CT);
+        };
+        if (t0 >= sw.hi || t0 + CT <= sw.lo) {  // the wave's rows see nothing of it
+            next();
+            return;
         }
-        if (t0 >= sw.hi || t0 + CT <= sw.lo) continue;  // the wave's rows see nothing of it
         v16f s[2];
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
             for (int r = 0; r < 16; ++r) s[u][r] = 0.0f;
+        __builtin_amdgcn_sched_barrier(0);
+        next();
 #pragma unroll
         for (int i = 0; i < KS; ++i)
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-                const v8bf kf = *reinterpret_cast<const v8bf *>(&sk[b][kpiece(u * 32 + n, 2 * i + h) * 16]);
+                const v8bf kf = *reinterpret_cast<const v8bf *>(ck + ka[i] + u * (64 * D));
                 s[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[i], s[u], 0, 0, 0);
             }
+        __builtin_amdgcn_sched_barrier(0);
         // element r of block u: token t0 + 32 u + 16 (r / 8) + 8 h + r % 8 of row n
-        const uint64_t anybad = bad[b][0] | bad[b][1] | bad[b][2] | bad[b][3];
-        if (anybad != 0 || t0 < sw.full_lo || t0 + CT > min(sw.full_hi, end)) {
+        const uint64_t any = bad[b][0] | bad[b][1] | bad[b][2] | bad[b][3];
+        const bool anybad = __builtin_amdgcn_readfirstlane((int)any | (int)(any >> 32)) != 0;
+        if (anybad || t0 < sw.full_lo || t0 + CT > min(sw.full_hi, end)) {
 #pragma unroll
             for (int u = 0; u < 2; ++u)
 #pragma unroll
@@ -510,41 +547,41 @@ __global__ __launch_bounds__(256, 2) void k_kv4_chunk(DecArgs p) {
                     s[u][r] = ok && tok < vhi && tok >= vlo ? s[u][r] : -INFINITY;
                 }
         }
+        // The maximum moves only when it would rise by more than 2^8: until then the factors stay below 2^8,
+        // which neither fp32 sums nor a bf16 factor's relative error mind, and nothing is rescaled.
         float mx = m;
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
-            for (int r = 0; r < 16; r += 2) mx = fmaxf(mx, fmaxf(s[u][r], s[u][r + 1]));
+            for (int r = 0; r < 16; r += 2) mx = max3(mx, s[u][r], s[u][r + 1]);
         mx = half_max(mx);
-        const float mu = mx == -INFINITY ? 0.0f : mx * c;
-        if (__builtin_amdgcn_ballot_w64(mx != m) != 0) {
-            const float alpha = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m * c - mu);
+        if (__builtin_amdgcn_ballot_w64(m == -INFINITY ? mx != -INFINITY : (mx - m) * c > 8.0f) != 0) {
+            const float alpha = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((m - mx) * c);
             m = mx;
             l *= alpha;
 #pragma unroll
             for (int j = 0; j < DT; ++j) acc[j] *= alpha;
         }
-        v8bf pb[4];
-        float ls[4];
+        const float mu = m == -INFINITY ? 0.0f : m * c;
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+        for (int k = 0; k < 4; ++k) {
+            float e[8];
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                float e[8];
-#pragma unroll
-                for (int r = 0; r < 8; ++r) e[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[u][8 * k + r], c, -mu));
-                ls[2 * u + k] = ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
-                pb[2 * u + k] = __builtin_bit_cast(v8bf, u32x4{bf16_pack2(e[0], e[1]), bf16_pack2(e[2], e[3]),
-                                                               bf16_pack2(e[4], e[5]), bf16_pack2(e[6], e[7])});
-            }
-        l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
+            for (int r = 0; r < 8; ++r) e[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[k >> 1][8 * (k & 1) + r], c, -mu));
+            l += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
+            const v8bf pb = __builtin_bit_cast(v8bf, u32x4{bf16_pack2(e[0], e[1]), bf16_pack2(e[2], e[3]),
+                                                           bf16_pack2(e[4], e[5]), bf16_pack2(e[6], e[7])});
 #pragma unroll
             for (int j = 0; j < DT; ++j) {
-                const v8bf vf = *reinterpret_cast<const v8bf *>(&sv[b][vpiece(j * 32 + n, 2 * k + h) * 16]);
-                acc[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf, pb[k], acc[j], 0, 0, 0);
+                const v8bf vf = *reinterpret_cast<const v8bf *>(cv + va[k ^ j] + j * 4096);
+                acc[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf, pb, acc[j], 0, 0, 0);
             }
+        }
+    };
+    for (int t0 = beg; t0 < end; t0 += 2 * CT) {
+        tile(std::integral_constant<int, 0>{}, t0, sk0, sv0, sk1, sv1);
+        if (t0 + CT < end) tile(std::integral_constant<int, 1>{}, t0 + CT, sk1, sv1, sk0, sv0);
     }
     l += __shfl_xor(l, 32, 64);
     if (!live) return;
@@ -576,19 +613,20 @@ __global__ __launch_bounds__(256, 2) void k_kv4_chunk(DecArgs p) {
     }
 }
 
-// Joins the splits of a row: a workgroup a row, D / 4 lanes to a split's columns, so 8 (D = 128) or
-// 16 splits are read at once.  Each lane group sums its splits in ascending order, then the groups
-// are summed in order.
-template <int D>
+// Joins the splits of a row: D / 4 lanes to a split's columns, so a workgroup has 8 (D = 128) or 16 lane
+// groups; G of them read a row's splits at once (all, or one where there are few splits and many rows).
+// Each group sums its splits in ascending order, then the groups are summed in order.
+template <int D, int G>
 __global__ __launch_bounds__(256) void k_kv4_join(DecArgs p) {
-    constexpr int L = D / 4, G = 256 / L;
+    constexpr int L = D / 4, RW = 256 / L / G;  // RW rows a workgroup
     const Kv4Attn &a = p.a;
-    const int lane = threadIdx.x % L, grp = threadIdx.x / L;
-    int64_t id = blockIdx.x;
+    const int lane = threadIdx.x % L, grp = threadIdx.x / L % G;
+    int64_t id = (int64_t)blockIdx.x * RW + threadIdx.x / L / G;
     const int r = (int)(id % p.pr); id /= p.pr;
     const int head = (int)(id % a.geo.hkv); id /= a.geo.hkv;
     const int rt = (int)(id % p.rt);
     const int seq = (int)(id / p.rt);
+    if (seq >= a.b) return;  // (of a workgroup that joins one row, all or none)
     const Span sp = span_of(a, p.g, seq, rt * p.tr, p.tr);
     const int row = rt * p.tr + r;
     if (row >= sp.rows) return;
@@ -610,28 +648,30 @@ __global__ __launch_bounds__(256) void k_kv4_join(DecArgs p) {
         o[2] = o[2] * f0 + v.z * f1;
         o[3] = o[3] * f0 + v.w * f1;
     }
-    __shared__ __attribute__((aligned(16))) float so[G][D + 4];
-    *reinterpret_cast<float4 *>(&so[grp][lane * 4]) = make_float4(o[0], o[1], o[2], o[3]);
-    if (lane == 0) {
-        so[grp][D] = M;
-        so[grp][D + 1] = Lsum;
-    }
-    __syncthreads();
-    if (grp != 0) return;
+    if constexpr (G > 1) {
+        __shared__ __attribute__((aligned(16))) float so[G][D + 4];
+        *reinterpret_cast<float4 *>(&so[grp][lane * 4]) = make_float4(o[0], o[1], o[2], o[3]);
+        if (lane == 0) {
+            so[grp][D] = M;
+            so[grp][D + 1] = Lsum;
+        }
+        __syncthreads();
+        if (grp != 0) return;
 #pragma unroll
-    for (int i = 1; i < G; ++i) M = fmaxf(M, so[i][D]);
-    const float mu = M == -INFINITY ? 0.0f : M;
-    Lsum = 0.0f;
-    o[0] = o[1] = o[2] = o[3] = 0.0f;
+        for (int i = 1; i < G; ++i) M = fmaxf(M, so[i][D]);
+        const float mu = M == -INFINITY ? 0.0f : M;
+        Lsum = 0.0f;
+        o[0] = o[1] = o[2] = o[3] = 0.0f;
 #pragma unroll
-    for (int i = 0; i < G; ++i) {
-        const float f = __builtin_amdgcn_exp2f(so[i][D] - mu);
-        const float4 v = *reinterpret_cast<const float4 *>(&so[i][lane * 4]);
-        Lsum += so[i][D + 1] * f;
-        o[0] += v.x * f;
-        o[1] += v.y * f;
-        o[2] += v.z * f;
-        o[3] += v.w * f;
+        for (int i = 0; i < G; ++i) {
+            const float f = __builtin_amdgcn_exp2f(so[i][D] - mu);
+            const float4 v = *reinterpret_cast<const float4 *>(&so[i][lane * 4]);
+            Lsum += so[i][D + 1] * f;
+            o[0] += v.x * f;
+            o[1] += v.y * f;
+            o[2] += v.z * f;
+            o[3] += v.w * f;
+        }
     }
     const float inv = Lsum == 0.0f ? 0.0f : 1.0f / Lsum;
     const int64_t out = (int64_t)(sp.qbeg + row / p.g) * a.hq + head * p.g + row % p.g;
@@ -646,28 +686,38 @@ constexpr int64_t WANT = 1024;  // workgroups of a call, where its tokens allow:
 constexpr int64_t FAR = 1024;   // tokens after which a workgroup's share is split all the same ...
 constexpr int64_t FAR_SPLITS = 64;  // ... into at most this many: sequences of unlike lengths balance
 
+// A call of few (sequence, head, tile)s over few tokens goes to workgroups of WIDE waves instead of several
+// of four: they join in LDS, which saves the second launch (about 4 us of the host's time).  On the
+// device, split | wide, us, d 128: 8 groups 7.3 | 7.1 at 512 tokens, 7.5 | 9.2 at 1024, 7.8 | 13.2 at 2048;
+// 64 groups 9.2 | 9.4 at 1024, 12.6 | 13.5 at 2048; 256 groups 13.1 | 8.5 at 512, 15.6 | 11.4 at 1024, 33.0 | 29.7 at 4096, 58.5 | 53.2 at 8192.
+constexpr int WIDE = 16;
+bool wide(int64_t groups, int64_t span) { return groups <= 256 && span <= (groups >= 128 ? 4096 : groups >= 64 ? 2048 : 1024); }
+
 // Rows and tiles of a call: up to FEW rows a (sequence, head) go to the decode kernel.
 void tiles_of(int max_q, int g, DecArgs &p) {
     const int64_t rows = (int64_t)max_q * g;
     p.g = g;
-    p.tr = rows > FEW ? CR : 16;
+    p.tr = rows <= FEW ? 16 : CR;
     p.pr = (int)std::min<int64_t>(rows, p.tr);
     p.rt = (int)((rows + p.tr - 1) / p.tr);
 }
 // The split of a call along `span` tokens, at most (it does not fall as the span grows).
 int64_t splits_of(const DecArgs &p, int64_t groups, int64_t span) {
-    const int64_t unit = p.tr == CR ? CT : NW * TT, want = p.tr == CR ? WANT / 2 : WANT;
+    const int64_t unit = p.tr == CR ? CT : 4 * TT, want = p.tr == CR ? WANT / 2 : WANT;
     int64_t splits = (want + groups - 1) / groups;
-    if (p.tr != CR) splits = std::max(splits, std::min((span + FAR - 1) / FAR, FAR_SPLITS));
+    if (p.tr == 16) splits = std::max(splits, std::min((span + FAR - 1) / FAR, FAR_SPLITS));
     return std::max<int64_t>(1, std::min(splits, (span + unit - 1) / unit));
 }
 void plan(const Kv4Attn &a, DecArgs &p) {
     tiles_of(a.max_q, a.hq / a.geo.hkv, p);
-    const int64_t groups = (int64_t)a.b * a.geo.hkv * p.rt, unit = p.tr == CR ? CT : NW * TT;
+    const int64_t groups = (int64_t)a.b * a.geo.hkv * p.rt;
     int64_t span = (int64_t)a.width << a.geo.page_log2;
     // a window's span: that of the tile's first to its last query, and the start's rounding down
     if (a.window) span = std::min<int64_t>(span, (int64_t)a.window + p.tr / p.g + 1 + CT);
-    const int64_t splits = splits_of(p, groups, span);
+    int64_t splits = splits_of(p, groups, span);
+    p.nw = p.tr == 16 && splits > 1 && wide(groups, span) ? WIDE : 4;
+    if (p.nw == WIDE) splits = 1;
+    const int64_t unit = p.tr == CR ? CT : p.nw * TT;
     const int64_t chunk = ((span + splits - 1) / splits + unit - 1) / unit * unit;
     p.chunk = (int)chunk;
     p.splits = (int)((span + chunk - 1) / chunk);
@@ -675,7 +725,8 @@ void plan(const Kv4Attn &a, DecArgs &p) {
 
 }  // namespace
 
-// Enough for every window: a window only shortens the span, so the bound on the splits falls.
+// Enough for every window: a window only shortens the span, so the bound on the splits falls (and a call
+// that goes to the wide workgroups needs none of it).
 size_t kv4_attn_ws_bytes(int b, int max_q, int hq, const Kv4Geom &g, int width) {
     DecArgs p;
     tiles_of(max_q, hq / g.hkv, p);
@@ -694,14 +745,22 @@ hipError_t launch_kv4_attn(const Kv4Attn &a, hipStream_t s) {
         if (a.geo.d == 128) hipLaunchKernelGGL(k_kv4_chunk<128>, grid, dim3(256), 0, s, p);
         else hipLaunchKernelGGL(k_kv4_chunk<64>, grid, dim3(256), 0, s, p);
     } else {
-        if (a.geo.d == 128) hipLaunchKernelGGL(k_kv4_decode<128>, grid, dim3(64 * NW), 0, s, p);
-        else hipLaunchKernelGGL(k_kv4_decode<64>, grid, dim3(64 * NW), 0, s, p);
+#define DECODE(D, NW) hipLaunchKernelGGL((k_kv4_decode<D, NW>), grid, dim3(64 * NW), 0, s, p)
+        if (a.geo.d == 128 && p.nw == WIDE) DECODE(128, WIDE);
+        else if (a.geo.d == 128) DECODE(128, 4);
+        else if (p.nw == WIDE) DECODE(64, WIDE);
+        else DECODE(64, 4);
+#undef DECODE
     }
     hipError_t e = hipGetLastError();
     if (e == hipSuccess && p.splits > 1) {
-        const dim3 jg((unsigned)(tiles * p.pr));
-        if (a.geo.d == 128) hipLaunchKernelGGL(k_kv4_join<128>, jg, dim3(256), 0, s, p);
-        else hipLaunchKernelGGL(k_kv4_join<64>, jg, dim3(256), 0, s, p);
+        // one group a row where a row has no more splits than four groups' turns and the rows fill the device
+        const int groups = 1024 / a.geo.d, per = p.splits <= 4 && tiles * p.pr >= 8192 ? groups : 1;
+        const dim3 jg((unsigned)((tiles * p.pr + per - 1) / per));
+        if (a.geo.d == 128 && per > 1) hipLaunchKernelGGL((k_kv4_join<128, 1>), jg, dim3(256), 0, s, p);
+        else if (a.geo.d == 128) hipLaunchKernelGGL((k_kv4_join<128, 8>), jg, dim3(256), 0, s, p);
+        else if (per > 1) hipLaunchKernelGGL((k_kv4_join<64, 1>), jg, dim3(256), 0, s, p);
+        else hipLaunchKernelGGL((k_kv4_join<64, 16>), jg, dim3(256), 0, s, p);
         e = hipGetLastError();
     }
     return e;
