@@ -32,7 +32,7 @@ constexpr int BUF_FLAGS = 0x00020000;  // raw buffer descriptor word 3 (gfx9 fam
 
 struct Args8 {
     Op8 A, B;
-    int64_t M, N;
+    int M, N;  // below 2^23
     int KB;  // blocks of 128 along the contraction
     void *Y;
     int tilesM, tilesN, group;
@@ -114,13 +114,13 @@ __global__ __launch_bounds__(256, W == 4 ? 1 : 2) void k_block8_gemm(Args8 p) {
     const int last = min(((int)(blockIdx.x & 7) + 1) * tpx, tiles);
     int lg = (blockIdx.x & 7) * tpx + (blockIdx.x >> 3);
     if (lg >= last) return;
-    auto origin = [&](int l, int64_t &m0, int64_t &n0) {
+    auto origin = [&](int l, int &m0, int &n0) {
         const int grp = l / (p.group * p.tilesN), first = grp * p.group, gm = min(p.group, p.tilesM - first);
         const int in = l - grp * p.group * p.tilesN;
-        m0 = (int64_t)(first + in % gm) * T;
-        n0 = (int64_t)(in / gm) * T;
+        m0 = (first + in % gm) * T;
+        n0 = in / gm * T;
     };
-    int64_t m0, n0;
+    int m0, n0;
     origin(lg, m0, n0);
 
     // Descriptors start at a tile's first row: offsets stay small whatever the operand's size, and rows
@@ -140,9 +140,8 @@ __global__ __launch_bounds__(256, W == 4 ? 1 : 2) void k_block8_gemm(Args8 p) {
         const uint8_t *a, *b;
         int na, nb;
     };
-    auto source = [&](int64_t m, int64_t n) {
-        return Src{p.A.codes + m * p.A.ld, p.B.codes + n * p.B.ld, (int)min((int64_t)T, p.M - m) * ldA,
-                   (int)min((int64_t)T, p.N - n) * ldB};
+    auto source = [&](int m, int n) {
+        return Src{p.A.codes + m * p.A.ld, p.B.codes + n * p.B.ld, min(T, p.M - m) * ldA, min(T, p.N - n) * ldB};
     };
     auto dma = [&](uint8_t *buf, Src s, int koff, bool in) {
         rows_to_lds<2 * W>(s.a, in ? s.na : 0, buf + wave * W * 2048, offA, koff);
@@ -166,17 +165,18 @@ __global__ __launch_bounds__(256, W == 4 ? 1 : 2) void k_block8_gemm(Args8 p) {
     };
     // scale bytes of blocks 2 it and 2 it + 1 of the lane's rows
     const int iters = (p.KB + 1) / 2;
-    auto scales = [&](int64_t m, int64_t n, int it, uint32_t (&sa)[W], uint32_t (&sb)[W]) {
-        const int sel = (it >> 1), half = it & 1;
+    auto scales = [&](int m, int n, int it, uint32_t (&sa)[W], uint32_t (&sb)[W]) {
+        const uint8_t *pa = reinterpret_cast<const uint8_t *>(p.A.scales + (int64_t)(it >> 1) * p.A.srows) + (it & 1) * 2;
+        const uint8_t *pb = reinterpret_cast<const uint8_t *>(p.B.scales + (int64_t)(it >> 1) * p.B.srows) + (it & 1) * 2;
 #pragma unroll
         for (int i = 0; i < W; ++i) {
-            const int64_t r = min(m + (wm * W + i) * 32 + (lane & 31), p.M - 1);
-            sa[i] = reinterpret_cast<const uint16_t *>(p.A.scales + (int64_t)sel * p.A.srows + (r >> p.A.sshift))[half];
+            const uint32_t r = (uint32_t)min(m + (wm * W + i) * 32 + (lane & 31), p.M - 1) >> p.A.sshift;
+            sa[i] = *reinterpret_cast<const uint16_t *>(pa + r * 4);
         }
 #pragma unroll
         for (int j = 0; j < W; ++j) {
-            const int64_t r = min(n + (wn * W + j) * 32 + (lane & 31), p.N - 1);
-            sb[j] = reinterpret_cast<const uint16_t *>(p.B.scales + (int64_t)sel * p.B.srows + (r >> p.B.sshift))[half];
+            const uint32_t r = (uint32_t)min(n + (wn * W + j) * 32 + (lane & 31), p.N - 1) >> p.B.sshift;
+            sb[j] = *reinterpret_cast<const uint16_t *>(pb + r * 4);
         }
     };
 
@@ -243,7 +243,7 @@ __global__ __launch_bounds__(256, W == 4 ? 1 : 2) void k_block8_gemm(Args8 p) {
     // before lie behind its last loads.
     constexpr int STORES = W == 4 ? 32 : 0;
     constexpr int NORMAL = 0, FIRST = 1, FRESH = 2;
-    auto pair = [&](auto mode, uint8_t *u0, uint8_t *u1, const uint8_t *u2, int it, Src src, int koff, bool in, bool in2, int64_t sm_, int64_t sn, int sit) {
+    auto pair = [&](auto mode, uint8_t *u0, uint8_t *u1, const uint8_t *u2, int it, Src src, int koff, bool in, bool in2, int sm_, int sn, int sit) {
         constexpr int MODE = decltype(mode)::value;
         constexpr int W0 = (NST - 2) * D + (MODE == FIRST ? 0 : (NST - 2) / 2 * S) + (MODE == FRESH ? STORES : 0);
         constexpr int W1 = (NST - 2) * D + (MODE == FIRST && NST > 2 ? 0 : NST / 2 * S);
@@ -266,7 +266,7 @@ __global__ __launch_bounds__(256, W == 4 ? 1 : 2) void k_block8_gemm(Args8 p) {
     for (;;) {
         const int nlg = lg + per;
         const bool more = WALK && nlg < last;
-        int64_t nm0 = m0, nn0 = n0;
+        int nm0 = m0, nn0 = n0;
         if (more) origin(nlg, nm0, nn0);
         const Src nxt = source(nm0, nn0);
 #pragma unroll
@@ -342,17 +342,17 @@ __global__ __launch_bounds__(256, W == 4 ? 1 : 2) void k_block8_gemm(Args8 p) {
                         }
                     // rows lr = k RK + lane / CHUNKS of the patch: a uniform base and the lane's offset
                     constexpr int RK = 64 / CHUNKS;
-                    const int64_t row = m0 + (wm * W + i) * 32, col = n0 + (wn * W + j0) * 32;
-                    uint8_t *base = static_cast<uint8_t *>(p.Y) + (row * p.N + col) * ES;
+                    const int row = m0 + (wm * W + i) * 32, col = n0 + (wn * W + j0) * 32;
+                    uint8_t *base = static_cast<uint8_t *>(p.Y) + ((int64_t)row * p.N + col) * ES;
 #pragma unroll
                     for (int k = 0; k < 32 / RK; ++k) {
                         const u32x4 o = *reinterpret_cast<const u32x4 *>((WALK ? own_patch : sm0) + wave * PATCH +
                                                                          (k * RK + lane / CHUNKS) * 144 + lane % CHUNKS * 16);
-                        uint8_t *y = base + k * RK * p.N * ES + loff;
-                        const int rows = (int)min(p.M - row - k * RK, (int64_t)RK);  // may be <= 0, as cols
-                        const int cols = (int)min(p.N - col, (int64_t)(PJ * 32)) - lane % CHUNKS * EL;
+                        uint8_t *y = base + (int64_t)(k * RK) * p.N * ES + loff;
+                        const int rows = min(p.M - row - k * RK, RK);  // may be <= 0, as cols
+                        const int cols = min(p.N - col, PJ * 32) - lane % CHUNKS * EL;
                         if (decltype(whole)::value || (lane / CHUNKS < rows && cols >= EL)) {
-                            *reinterpret_cast<ua_u32x4 *>(y) = o;
+                            __builtin_nontemporal_store((ua_u32x4)o, reinterpret_cast<ua_u32x4 *>(y));
                         } else if (lane / CHUNKS < rows) {
 #pragma unroll
                             for (int e = 0; e < EL; ++e) {
@@ -396,8 +396,8 @@ hipError_t launch_block8_gemm(const Op8 &A, const Op8 &B, int64_t M, int64_t N, 
     Args8 p;
     p.A = A;
     p.B = B;
-    p.M = M;
-    p.N = N;
+    p.M = (int)M;
+    p.N = (int)N;
     p.KB = (int)((K + 127) / 128);
     p.Y = Y;
     p.tilesM = p.tilesN = p.group = 0;
