@@ -45,6 +45,33 @@ def test_write_read(n, h, page, d, dt):
     assert float(fp4.kv4_read(c, other)[0].abs().sum()) == 0  # nothing else was touched
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("start", [0, 1, 4, 7])
+def test_long_write_read(start, d):
+    """A prompt long enough for four tokens a lane: runs of slots that begin anywhere, gaps, repeats out of
+    the cache, a NaN, and an odd end."""
+    n, h, page = 8195, 2 if d == 128 else 4, 32
+    pages = 300
+    k, v = kv(n, h, d, 5)
+    k[40, 0, 3], v[4097, 1, 9] = float("nan"), float("inf")
+    slots = torch.arange(n) + start
+    slots[1000:1013] += 2 ** 40
+    slots[2001] = -5
+    slots[3000:3004] = torch.tensor([9503, 9502, 9501, 9500])
+    c = fp4.kv4_cache(pages, page, h, d)
+    for s in (slots, slots.clamp(max=2 ** 31 - 1).int()):
+        c.data.zero_()
+        fp4.kv4_write(c, k.to(DEV), v.to(DEV), s.to(DEV))
+        a, b = (f64(t) for t in fp4.kv4_read(c, s.to(DEV), out_dtype=torch.float32))
+        wk, wv = (ref.cache_values(np.where(np.isfinite(f64(t)), f64(t), 0)) for t in (k, v))
+        gone = (slots < 0) | (slots >= pages * page)
+        for got, want in ((a, wk), (b, wv)):
+            want[40, 0], want[4097, 1], want[gone.numpy()] = np.nan, np.nan, 0
+            assert np.array_equal(got, want, equal_nan=True)
+        left = fp4.kv4_read(c, torch.tensor([x for x in range(pages * page) if x not in set(slots.tolist())], device=DEV))
+        assert float(left[0].abs().sum()) == 0 and float(left[1].abs().sum()) == 0
+
+
 def test_write_borders_strides_and_bad_slots():
     d = 64
     k = torch.zeros(8, 2, d)
