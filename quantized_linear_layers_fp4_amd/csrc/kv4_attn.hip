@@ -260,9 +260,9 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? 3 : 1) void k_kv4_decode(DecArgs
             }
         }
         const float mx = fmaxf(m, quarter_max(max3(max3(x[0], x[1], x[2]), max3(x[3], x[4], x[5]), fmaxf(x[6], x[7]))));
-        // the maximum moves only when it would rise by more than 2^8: until then the factors stay below 2^8,
-        // which neither fp32 sums nor a bf16 factor's relative error mind, and nothing is rescaled
-        if (__builtin_amdgcn_ballot_w64(m == -INFINITY ? mx != -INFINITY : mx - m > 8.0f) != 0) {
+        // Rarely, after a row's first tiles.  (Letting factors grow to 2^8 before the maximum moves saved 1 to 3 %
+        // and cost a dominant token its exact factor of 1: 0.0021 instead of 0.0017 off in the mean.)
+        if (__builtin_amdgcn_ballot_w64(mx != m) != 0) {
             const float alpha = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m - mx);
             m = mx;
             l *= alpha;
@@ -547,15 +547,13 @@ __global__ __launch_bounds__(256, 2) void k_kv4_chunk(DecArgs p) {
                     s[u][r] = ok && tok < vhi && tok >= vlo ? s[u][r] : -INFINITY;
                 }
         }
-        // The maximum moves only when it would rise by more than 2^8: until then the factors stay below 2^8,
-        // which neither fp32 sums nor a bf16 factor's relative error mind, and nothing is rescaled.
         float mx = m;
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
             for (int r = 0; r < 16; r += 2) mx = max3(mx, s[u][r], s[u][r + 1]);
         mx = half_max(mx);
-        if (__builtin_amdgcn_ballot_w64(m == -INFINITY ? mx != -INFINITY : (mx - m) * c > 8.0f) != 0) {
+        if (__builtin_amdgcn_ballot_w64(mx != m) != 0) {
             const float alpha = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((m - mx) * c);
             m = mx;
             l *= alpha;
