@@ -444,7 +444,7 @@ class Block8:
         if n == 0:
             raise Fp4Error(f"no block-128 operand of {rows} rows, contraction {length}, mode {mode}")
         self.rows, self.length, self.mode = rows, length, mode
-        self.codes = torch.empty((rows, (length + 127) // 128 * 128), dtype=torch.uint8, device=device)
+        self.codes = torch.empty(rows, (length + 127) // 128 * 128, dtype=torch.uint8, device=device)
         self.scales = torch.empty(n, dtype=torch.uint8, device=device)
 
 
@@ -517,7 +517,7 @@ def block8_linear_forward(x: torch.Tensor, w: Block8, out_dtype: torch.dtype | N
     if K != w.length:
         raise ValueError(f"x has {K} columns, the weight a contraction of {w.length}")
     _same_device(x, w.codes)
-    Y = torch.empty((M, w.rows), dtype=out_dtype or x.dtype, device=x.device)
+    Y = torch.empty(M, w.rows, dtype=out_dtype or x.dtype, device=x.device)
     if M == 0:
         if for_backward:
             raise ValueError("no rows to contract in the backward")
@@ -546,8 +546,8 @@ def block8_linear_backward(dy: torch.Tensor, w: Block8 | None, xt: Block8 | None
         raise ValueError("the activation's operand has vector blocks")
     _same_device(dy, w.codes if w is not None else None, xt.codes if xt is not None else None)
     out_dtype = out_dtype or dy.dtype
-    dx = torch.empty((M, K), dtype=out_dtype, device=dy.device) if w is not None else None
-    dw = torch.empty((K, N), dtype=out_dtype, device=dy.device) if xt is not None else None
+    dx = torch.empty(M, K, dtype=out_dtype, device=dy.device) if w is not None else None
+    dw = torch.empty(K, N, dtype=out_dtype, device=dy.device) if xt is not None else None
     L = lib()
     ws = _block8_scratch(ws, L.fp4_block8_backward_workspace_bytes(M, N), dy.device)
     od = _out_dtype_code(out_dtype)
@@ -588,8 +588,9 @@ def kv4_write(cache: KV4Cache, k: torch.Tensor, v: torch.Tensor, slots: torch.Te
     """Quantize k and v (n x heads x d, fp32 or bf16, d contiguous) into the cache at slots (page index *
     page + offset; those outside the cache are skipped)."""
     n = k.shape[0]
+    shape = (n, cache.heads, cache.d)
     for t in (k, v):
-        if not t.is_cuda or t.shape != (n, cache.heads, cache.d) or t.stride(2) != 1:
+        if not t.is_cuda or t.shape != shape or t.stride(2) != 1:
             raise ValueError(f"expected (n, {cache.heads}, {cache.d}) on a HIP device, the last dimension contiguous")
     if k.dtype != v.dtype:
         raise TypeError("k and v must share a dtype")
@@ -608,7 +609,7 @@ def kv4_read(cache: KV4Cache, slots: torch.Tensor, d: int | None = None, out_dty
     n = slots.numel()
     sb = _slot_bytes(slots, n)
     _same_device(cache.data, slots)
-    k = torch.empty((n, cache.heads, cache.d), dtype=out_dtype, device=slots.device)
+    k = torch.empty(n, cache.heads, cache.d, dtype=out_dtype, device=slots.device)
     v = torch.empty_like(k)
     if n:
         _check(lib().fp4_kv4_read(_ptr(cache.data), cache.pages, cache.page, cache.heads, cache.d, _ptr(slots), sb, n,
@@ -638,17 +639,19 @@ def kv4_attention(q: torch.Tensor, cache: KV4Cache, pages: torch.Tensor, lens: t
     if hq == 0 or hq % cache.heads:
         raise ValueError(f"{hq} query heads over {cache.heads} key/value heads")
     b = pages.shape[0]
-    for t, shape in ((lens, (b,)), (q_start, (b + 1,))):
-        if t is not None and (t.dtype != torch.int32 or not t.is_cuda or tuple(t.shape) != shape or not t.is_contiguous()):
-            raise ValueError(f"expected int32 {shape} on a HIP device")
+    if lens.dtype != torch.int32 or not lens.is_cuda or lens.shape != (b,) or not lens.is_contiguous():
+        raise ValueError(f"expected {b} int32 lengths on a HIP device")
+    if q_start is not None and (q_start.dtype != torch.int32 or not q_start.is_cuda or q_start.shape != (b + 1,) or
+                                not q_start.is_contiguous()):
+        raise ValueError(f"expected {b + 1} int32 offsets on a HIP device")
     if pages.dtype != torch.int32 or not pages.is_cuda or pages.dim() != 2 or pages.stride(1) != 1 or \
             (b > 1 and pages.stride(0) < pages.shape[1]):
         raise ValueError("expected an int32 page table (b, width) on a HIP device, rows contiguous")
     if q_start is None and nq != b:
         raise ValueError(f"{nq} queries for {b} sequences without q_start")
     _same_device(q, cache.data, pages, lens, q_start, ws)
-    o = torch.empty((nq, hq, d), dtype=q.dtype, device=q.device)
-    lse = torch.empty((nq, hq), dtype=torch.float32, device=q.device) if return_lse else None
+    o = torch.empty_like(q, memory_format=torch.contiguous_format)
+    lse = torch.empty(nq, hq, dtype=torch.float32, device=q.device) if return_lse else None
     if nq and b:
         if ws is None:
             ws = kv4_attention_workspace(q, cache, pages, max_q)

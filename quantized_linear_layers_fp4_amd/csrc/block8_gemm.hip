@@ -16,6 +16,8 @@
 // their way while a tile's results are stored, and its stores drain under the next tile's products.
 // The product is formed transposed, so a lane holds four consecutive columns of one row; the tiles are
 // turned to row order through LDS and stored 16 bytes a lane.
+#include <algorithm>
+#include <cmath>
 #include <type_traits>
 
 #include "block8.h"
@@ -402,9 +404,19 @@ hipError_t launch_block8_gemm(const Op8 &A, const Op8 &B, int64_t M, int64_t N, 
     p.Y = Y;
     p.tilesM = p.tilesN = p.group = 0;
     if (block8_few(M, N)) return launch_block8_few(A, B, M, N, K, Y, y_dt, s);
-    // the largest tile that still gives every CU a workgroup
-    auto count = [&](int64_t t) { return ((M + t - 1) / t) * ((N + t - 1) / t); };
-    const int w = count(256) >= cus ? 4 : (count(128) >= cus ? 2 : 1);
+    // The tile with the least expected time: rounds of the device (tiles of 256 one a CU, the others two a CU, a
+    // last round of those counting by its part) times a round's, which is a K-proportional part and a fixed one,
+    // fitted in us to thirteen shapes of up to 6000 x 6000 x 4096.  Measured, tiles of 64 | 128 | 256, bf16 output at
+    // K = 4096: 512 x 4096 17.3 | 21.6 | 40.6, 2048 x 4096 63 | 35 | 45, 3000 x 4096 100 | 57 | 49, 4096 x 4096
+    // 123 | 76 | 55, 4600 x 4600 152 | 105 | 109; fp32 output 23 | 35 | 84, 82 | 59 | 95, 126 | 90 | 101, 169 | 120 | 108,
+    // 214 | 165 | 209.
+    auto count = [&](int64_t t) { return (double)(((M + t - 1) / t) * ((N + t - 1) / t)); };
+    const bool f32 = y_dt != DT_BF16;
+    const double k = (double)K / 4096;
+    const double t4 = std::ceil(count(256) / cus) * (k * (f32 ? 92 : 46) + (f32 ? 12 : 8));
+    const double t2 = std::max(count(128) / (2 * cus), 0.67) * (k * (f32 ? 54 : 33) + (f32 ? 5 : 3));
+    const double t1 = std::max(count(64) / (2 * cus), 0.7) * (k * (f32 ? 19 : 14) + 2);
+    const int w = t4 <= t2 && t4 <= t1 ? 4 : t2 <= t1 ? 2 : 1;
     if (y_dt == DT_BF16)
         return w == 4 ? launch_tiles<DT_BF16, 4>(p, cus, s)
                       : w == 2 ? launch_tiles<DT_BF16, 2>(p, cus, s) : launch_tiles<DT_BF16, 1>(p, cus, s);
