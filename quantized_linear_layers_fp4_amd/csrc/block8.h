@@ -31,11 +31,11 @@ hipError_t launch_block8_gemm(const Op8 &A, const Op8 &B, int64_t M, int64_t N, 
 // The same for few rows of A, and with A (X, rows ldx apart) quantized on the way.
 // Where: measured on a bf16 layer with the weight out of the caches, few rows' kernel | tiles of 64 x 64,
 // us, at (K, N) = (4096, 22016): 24.3 | 25.8 for 16 rows, 31.3 | 26.7 for 32; (4096, 12288): 14.1 | 14.6 for
-// 16, 20.3 | 14.7 for 32; (2048, 6144): 9.9 | 9.3 for 32, 13.5 | 9.7 for 64; (4096, 4096): 12.9 | 13.8 for 64;
-// (11008, 4096): 12.0 | 27.6 for one, 21.8 | 29.3 for 64.  Its work grows with the rows, in steps of 16;
+// 16, 20.3 | 14.7 for 32; (2048, 6144): 9.9 | 9.3 for 32, 13.5 | 9.7 for 64; (4096, 4096): 11.4 | 13.7 for 48, 12.9 | 13.8 for 64;
+// (11008, 4096): 12.0 | 27.6 for one, 18.5 | 28.9 for 48, 21.8 | 29.3 for 64.  Its work grows with the rows, in steps of 16;
 // the tiles' is a chain of K / 128 loads until they fill the device.
 inline bool block8_few(int64_t M, int64_t N) {
-    return M <= 64 && (N + 15) / 16 * (M <= 16 ? 1 : M <= 32 ? 2 : 4) <= 1024;
+    return M <= 64 && (N + 15) / 16 * ((M + 15) / 16) <= 1024;
 }
 // Quantizing in every workgroup instead of once: 20.4 | 26.9 us for one row at (4096, 22016), where four
 // rows are 27.0 | 26.8; with a workgroup or two a CU it is the shorter way up to 128 blocks (8.8 | 9.5 for four

@@ -185,8 +185,8 @@ static hipError_t launch_few(const FewArgs &p, hipStream_t s) {
 hipError_t launch_block8_few(const Op8 &A, const Op8 &B, int64_t M, int64_t N, int64_t K, void *Y, int y_dt, hipStream_t s) {
     const FewArgs p{A, B, nullptr, 0, M, N, K, (int)((K + 127) / 128), Y};
     if (y_dt == DT_BF16)
-        return M <= 16 ? launch_few<CODES, DT_BF16, 1>(p, s) : M <= 32 ? launch_few<CODES, DT_BF16, 2>(p, s) : launch_few<CODES, DT_BF16, 4>(p, s);
-    return M <= 16 ? launch_few<CODES, DT_F32, 1>(p, s) : M <= 32 ? launch_few<CODES, DT_F32, 2>(p, s) : launch_few<CODES, DT_F32, 4>(p, s);
+        return M <= 16 ? launch_few<CODES, DT_BF16, 1>(p, s) : M <= 32 ? launch_few<CODES, DT_BF16, 2>(p, s) : M <= 48 ? launch_few<CODES, DT_BF16, 3>(p, s) : launch_few<CODES, DT_BF16, 4>(p, s);
+    return M <= 16 ? launch_few<CODES, DT_F32, 1>(p, s) : M <= 32 ? launch_few<CODES, DT_F32, 2>(p, s) : M <= 48 ? launch_few<CODES, DT_F32, 3>(p, s) : launch_few<CODES, DT_F32, 4>(p, s);
 }
 
 hipError_t launch_block8_few_direct(const void *X, int x_dt, int64_t ldx, const Op8 &B, int64_t M, int64_t N, int64_t K,

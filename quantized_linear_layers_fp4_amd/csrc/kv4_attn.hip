@@ -32,8 +32,7 @@ typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
 namespace {
 
 constexpr int TT = 32;       // tokens a wave takes at once
-constexpr int CR = 128;      // rows of a workgroup of the many-rows kernel: 32 a wave
-constexpr int CT = 64;       // tokens it takes at once
+constexpr int CT = 64;       // tokens a workgroup of the many-rows kernel takes at once
 constexpr int FEW = 32;      // rows a (sequence, head) up to which the decode kernel takes them
 constexpr float LN2 = 0.69314718055994530942f;
 constexpr float LOG2E = 1.44269504088896340736f;
@@ -41,7 +40,7 @@ constexpr float LOG2E = 1.44269504088896340736f;
 struct DecArgs {
     Kv4Attn a;
     int g, rt;        // heads a group; row tiles a (sequence, head)
-    int tr;           // rows of a tile: 16 or CR
+    int tr;           // rows of a tile: 16, or 128 or 256 (the many-rows kernel, 32 a wave)
     int pr;           // rows a partial result holds: min(tr, max_q * g)
     int nw;           // waves of a workgroup
     int splits;       // workgroups along the tokens
@@ -348,17 +347,26 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? 3 : 1) void k_kv4_decode(DecArgs
     }
 }
 
-// Many rows (chunks of prompts): 128 rows of one (sequence, key/value head) a workgroup, 32 a wave.
+// Many rows (chunks of prompts): rows of one (sequence, key/value head), 32 a wave, NT / 2 a workgroup.
 // Every tile of 64 tokens is unpacked to bf16 once by the whole workgroup into one of two LDS
 // buffers, while the waves multiply the other: with 16 rows a wave, as above, unpacking in registers
 // would take more time than the products.  Tokens are rows of K's operand with bits 2 and 3 of their
 // index exchanged, so that a lane's eight scores of one V step are eight consecutive tokens.
-// Two workgroups a CU (64 KiB of LDS each), so one's softmax runs beside the other's products.
-template <int D>
-__global__ __launch_bounds__(256, 2) void k_kv4_chunk(DecArgs p) {
+// Eight waves a CU in either size.  2 x 1024 queries of 32 heads over 8192 tokens (d 128, 8 key/value heads), us:
+// 16 rows a wave 700; this with four waves 362, page indices looked up a tile earlier 341, the maximum
+// in one instruction for two scores 322; with eight waves, which halves a thread's unpacking, and bytes two
+// tiles ahead 305.  0.85 PFLOP/s then; of a SIMD's cycles about 34 % are matrix and 45 % vector instructions
+// (the exponentials first), which overlap little: a deeper interleaving within a wave (64 rows, 512
+// registers) was slower.
+template <int D, int NT>
+__global__ __launch_bounds__(NT, 2) void k_kv4_chunk(DecArgs p) {
+    constexpr int CR = NT / 2;        // rows of the workgroup
     constexpr int KC = D / 8;     // 16-byte pieces of a token's K row
     constexpr int KS = D / 16;    // contraction steps of the scores
-    constexpr int DT = D / 32;    // tiles of 32 columns; dwords of K and tokens of V a thread unpacks
+    constexpr int DT = D / 32;    // tiles of 32 columns
+    constexpr int KD = 8 * D / NT;  // dwords of K, and tokens of V, that a thread unpacks
+    constexpr int TPT = NT / 64;  // threads a token of K
+    static_assert(KD == 2 || KD == 4, "what fetch and unpack know");
     __shared__ __attribute__((aligned(16))) uint8_t sk0[CT * D * 2], sv0[D * CT * 2], sk1[CT * D * 2], sv1[D * CT * 2];
     const Kv4Attn &a = p.a;
     const int tid = threadIdx.x, lane = tid & 63, n = lane & 31, h = lane >> 5;
@@ -393,45 +401,47 @@ __global__ __launch_bounds__(256, 2) void k_kv4_chunk(DecArgs p) {
         qf[i] = __builtin_bit_cast(v8bf, x);
     }
 
-    // What a thread unpacks: DT dwords of one token's K (of one group of 32), and eight columns of DT
+    // What a thread unpacks: KD dwords of one token's K (of one group of 32), and eight columns of KD
     // consecutive tokens' V.
     const int lg = a.geo.page_log2, P = 1 << lg;
     const int64_t region = a.geo.region();
     const int32_t *table = a.pages + (int64_t)seq * a.page_rs;
-    const int kt = tid >> 2, kq = tid & 3;
-    constexpr int VP = 8 / DT;
+    const int kt = tid / TPT, kq = tid % TPT;
+    constexpr int VP = 8 / KD;
     const int vp = tid % VP, vn = tid / VP % (D / 8), vt = tid / VP / (D / 8);
-    const int vtok = vt * 8 + vp * DT;
-    uint32_t kw[DT], vw[DT], ks, vs;
+    const int vtok = vt * 8 + vp * KD;
+    // the bytes of two tiles on their way: an even tile's in set 0, an odd one's in set 1
+    uint32_t kw[2][KD], vw[2][KD], ks[2], vs[2];
     const uint8_t *const headp = a.cache + (int64_t)head * region;
     const int64_t pstride = (int64_t)a.geo.hkv * region;
     auto page_at = [&](int t) { return table[min(t, end - 1) >> lg]; };
     // pages outside the cache: their tokens' bytes are any page's, and their scores are masked
-    bool okk;
-    auto fetch = [&](int t0, int pk, int pv) {
-        okk = (uint32_t)pk < (uint64_t)a.geo.pages;
+    bool okk[2];
+    auto fetch = [&](auto set, int t0, int pk, int pv) {
+        constexpr int z = decltype(set)::value;
+        okk[z] = (uint32_t)pk < (uint64_t)a.geo.pages;
         const bool okv = (uint32_t)pv < (uint64_t)a.geo.pages;
-        const uint8_t *kb = headp + (okk ? pk : 0) * pstride, *vb = headp + (okv ? pv : 0) * pstride;
+        const uint8_t *kb = headp + (okk[z] ? pk : 0) * pstride, *vb = headp + (okv ? pv : 0) * pstride;
         const int tk = (t0 + kt) & (P - 1), tv = (t0 + vtok) & (P - 1);
-        const uint8_t *ka = kb + tk * (D / 2) + kq * (D / 8);
+        const uint8_t *ka = kb + tk * (D / 2) + kq * (KD * 4);
         const uint8_t *va = vb + a.geo.v_off() + ((tv >> 3) * (D / 8) + vn) * 32 + (tv & 7) * 4;
-        if constexpr (D == 128) {
+        if constexpr (KD == 4) {
             const u32x4 x = *reinterpret_cast<const u32x4 *>(ka), y = *reinterpret_cast<const u32x4 *>(va);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                kw[i] = x[i];
-                vw[i] = y[i];
+                kw[z][i] = x[i];
+                vw[z][i] = y[i];
             }
-            vs = *reinterpret_cast<const uint32_t *>(vb + a.geo.vs_off() + (vn >> 2) * P + tv);
+            vs[z] = *reinterpret_cast<const uint32_t *>(vb + a.geo.vs_off() + (vn >> 2) * P + tv);
         } else {
             const uint2 x = *reinterpret_cast<const uint2 *>(ka), y = *reinterpret_cast<const uint2 *>(va);
-            kw[0] = x.x;
-            kw[1] = x.y;
-            vw[0] = y.x;
-            vw[1] = y.y;
-            vs = *reinterpret_cast<const uint16_t *>(vb + a.geo.vs_off() + (vn >> 2) * P + tv);
+            kw[z][0] = x.x;
+            kw[z][1] = x.y;
+            vw[z][0] = y.x;
+            vw[z][1] = y.y;
+            vs[z] = *reinterpret_cast<const uint16_t *>(vb + a.geo.vs_off() + (vn >> 2) * P + tv);
         }
-        ks = kb[a.geo.ks_off() + (kq * D / 128) * P + tk];
+        ks[z] = kb[a.geo.ks_off() + (kq * KD / 4) * P + tk];
     };
     // K rows: KC pieces, turned so that 16 rows of one piece lie on 16 places; V rows (columns): 8
     // pieces of eight tokens, turned for the reads (32 consecutive columns) and the writes (every eighth)
@@ -445,30 +455,31 @@ __global__ __launch_bounds__(256, 2) void k_kv4_chunk(DecArgs p) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) va[i] = vpiece(n, 2 * i + h) * 16;
     const int krow = (kt & ~12) | ((kt & 4) << 1) | ((kt & 8) >> 1);
-    int kst[DT], vst[8];
+    int kst[KD], vst[8];
 #pragma unroll
-    for (int i = 0; i < DT; ++i) kst[i] = kpiece(krow, kq * DT + i) * 16;
+    for (int i = 0; i < KD; ++i) kst[i] = kpiece(krow, kq * KD + i) * 16;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) vst[j] = vpiece(vn * 8 + j, vt) * 16 + vp * DT * 2;
-    auto unpack = [&](uint8_t *dk, uint8_t *dv) {
-        v8bf kf[DT];
-        unpack_row<DT>(kw, okk ? ks : 0u, kf);
+    for (int j = 0; j < 8; ++j) vst[j] = vpiece(vn * 8 + j, vt) * 16 + vp * KD * 2;
+    auto unpack = [&](auto set, uint8_t *dk, uint8_t *dv) {
+        constexpr int z = decltype(set)::value;
+        v8bf kf[KD];
+        unpack_row<KD>(kw[z], okk[z] ? ks[z] : 0u, kf);
 #pragma unroll
-        for (int i = 0; i < DT; ++i) *reinterpret_cast<v8bf *>(dk + kst[i]) = kf[i];
-        const float sc[4] = {scale_of<0>(vs), scale_of<1>(vs), scale_of<2>(vs), scale_of<3>(vs)};
-        uint32_t x[DT][4];
+        for (int i = 0; i < KD; ++i) *reinterpret_cast<v8bf *>(dk + kst[i]) = kf[i];
+        const float sc[4] = {scale_of<0>(vs[z]), scale_of<1>(vs[z]), scale_of<2>(vs[z]), scale_of<3>(vs[z])};
+        uint32_t x[KD][4];
 #pragma unroll
-        for (int t = 0; t < DT; ++t) {
-            x[t][0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(vw[t], sc[t], 0));
-            x[t][1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(vw[t], sc[t], 1));
-            x[t][2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(vw[t], sc[t], 2));
-            x[t][3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(vw[t], sc[t], 3));
+        for (int t = 0; t < KD; ++t) {
+            x[t][0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(vw[z][t], sc[t], 0));
+            x[t][1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(vw[z][t], sc[t], 1));
+            x[t][2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(vw[z][t], sc[t], 2));
+            x[t][3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(vw[z][t], sc[t], 3));
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const uint32_t sel = j & 1 ? 0x07060302u : 0x05040100u;
             uint8_t *d = dv + vst[j];
-            if constexpr (D == 128)
+            if constexpr (KD == 4)
                 *reinterpret_cast<uint2 *>(d) = make_uint2(__builtin_amdgcn_perm(x[1][j >> 1], x[0][j >> 1], sel),
                                                            __builtin_amdgcn_perm(x[3][j >> 1], x[2][j >> 1], sel));
             else
@@ -484,9 +495,11 @@ __global__ __launch_bounds__(256, 2) void k_kv4_chunk(DecArgs p) {
     float m = -INFINITY, l = 0.0f;  // m: of the unscaled scores
 
     // whether some page of a tile lies outside the cache, from the waves that unpacked it
-    __shared__ uint64_t bad[2][4];
-    // tile t0 is multiplied while t0 + CT is unpacked, t0 + 2 CT's bytes are on their way and the page indices
-    // of t0 + 3 CT
+    __shared__ uint64_t bad[2][TPT];
+    // tile t0 is multiplied while t0 + CT is unpacked, the bytes of the next two are on their way and the page
+    // indices of t0 + 4 CT
+    using I0 = std::integral_constant<int, 0>;
+    using I1 = std::integral_constant<int, 1>;
     int pk = 0, pv = 0;
     auto pages_of = [&](int t0) {
         pk = page_at(t0 + kt);
@@ -494,13 +507,15 @@ __global__ __launch_bounds__(256, 2) void k_kv4_chunk(DecArgs p) {
     };
     if (beg < end) {
         pages_of(beg);
-        fetch(beg, pk, pv);
+        fetch(I0{}, beg, pk, pv);
         pages_of(beg + CT);
-        const uint64_t bm = ~__builtin_amdgcn_ballot_w64(okk);
-        if (lane == 0) bad[0][wave] = bm;
-        unpack(sk0, sv0);
-        fetch(beg + CT, pk, pv);
+        fetch(I1{}, beg + CT, pk, pv);
         pages_of(beg + 2 * CT);
+        const uint64_t bm = ~__builtin_amdgcn_ballot_w64(okk[0]);
+        if (lane == 0) bad[0][wave] = bm;
+        unpack(I0{}, sk0, sv0);
+        fetch(I0{}, beg + 2 * CT, pk, pv);
+        pages_of(beg + 3 * CT);
     }
     auto tile = [&](auto buf, int t0, const uint8_t *ck, const uint8_t *cv, uint8_t *nk, uint8_t *nv) {
         constexpr int b = decltype(buf)::value;
@@ -508,11 +523,12 @@ __global__ __launch_bounds__(256, 2) void k_kv4_chunk(DecArgs p) {
         // the next tile is unpacked whether there is one or not (the fetched bytes are always some page's), so
         // that it lies beside the products, which are matrix instructions
         auto next = [&] {
-            const uint64_t bm = ~__builtin_amdgcn_ballot_w64(okk);
+            using Set = std::integral_constant<int, b ^ 1>;
+            const uint64_t bm = ~__builtin_amdgcn_ballot_w64(okk[b ^ 1]);
             if (lane == 0) bad[b ^ 1][wave] = bm;
-            unpack(nk, nv);
-            fetch(t0 + 2 * CT, pk, pv);
-            pages_of(t0 + 3 * CT);
+            unpack(Set{}, nk, nv);
+            fetch(Set{}, t0 + 3 * CT, pk, pv);
+            pages_of(t0 + 4 * CT);
         };
         if (t0 >= sw.hi || t0 + CT <= sw.lo) {  // the wave's rows see nothing of it
             next();
@@ -534,7 +550,9 @@ __global__ __launch_bounds__(256, 2) void k_kv4_chunk(DecArgs p) {
             }
         __builtin_amdgcn_sched_barrier(0);
         // element r of block u: token t0 + 32 u + 16 (r / 8) + 8 h + r % 8 of row n
-        const uint64_t any = bad[b][0] | bad[b][1] | bad[b][2] | bad[b][3];
+        uint64_t any = 0;
+#pragma unroll
+        for (int w = 0; w < TPT; ++w) any |= bad[b][w];
         const bool anybad = __builtin_amdgcn_readfirstlane((int)any | (int)(any >> 32)) != 0;
         if (anybad || t0 < sw.full_lo || t0 + CT > min(sw.full_hi, end)) {
 #pragma unroll
@@ -542,8 +560,8 @@ __global__ __launch_bounds__(256, 2) void k_kv4_chunk(DecArgs p) {
 #pragma unroll
                 for (int r = 0; r < 16; ++r) {
                     const int q = 32 * u + 16 * (r >> 3) + 8 * h + (r & 7), tok = t0 + q;
-                    // token q was unpacked by threads 4 q .. 4 q + 3: bit 4 (q % 16) of wave q / 16
-                    const bool ok = ((bad[b][q >> 4] >> (4 * (q & 15))) & 1) == 0;
+                    // token q was unpacked by threads TPT q and on, 64 / TPT tokens a wave
+                    const bool ok = ((bad[b][q / (64 / TPT)] >> (TPT * (q % (64 / TPT)))) & 1) == 0;
                     s[u][r] = ok && tok < vhi && tok >= vlo ? s[u][r] : -INFINITY;
                 }
         }
@@ -578,8 +596,8 @@ __global__ __launch_bounds__(256, 2) void k_kv4_chunk(DecArgs p) {
         }
     };
     for (int t0 = beg; t0 < end; t0 += 2 * CT) {
-        tile(std::integral_constant<int, 0>{}, t0, sk0, sv0, sk1, sv1);
-        if (t0 + CT < end) tile(std::integral_constant<int, 1>{}, t0 + CT, sk1, sv1, sk0, sv0);
+        tile(I0{}, t0, sk0, sv0, sk1, sv1);
+        if (t0 + CT < end) tile(I1{}, t0 + CT, sk1, sv1, sk0, sv0);
     }
     l += __shfl_xor(l, 32, 64);
     if (!live) return;
@@ -691,23 +709,24 @@ constexpr int64_t FAR_SPLITS = 64;  // ... into at most this many: sequences of 
 constexpr int WIDE = 16;
 bool wide(int64_t groups, int64_t span) { return groups <= 256 && span <= (groups >= 128 ? 4096 : groups >= 64 ? 2048 : 1024); }
 
-// Rows and tiles of a call: up to FEW rows a (sequence, head) go to the decode kernel.
-void tiles_of(int max_q, int g, DecArgs &p) {
+// Rows and tiles of a call: up to FEW rows a (sequence, head) go to the decode kernel.  Eight waves unpack a
+// tile for 256 rows; heads of 64 have too little to unpack for that.
+void tiles_of(int max_q, int g, int d, DecArgs &p) {
     const int64_t rows = (int64_t)max_q * g;
     p.g = g;
-    p.tr = rows <= FEW ? 16 : CR;
+    p.tr = rows <= FEW ? 16 : d == 128 && rows >= 256 ? 256 : 128;
     p.pr = (int)std::min<int64_t>(rows, p.tr);
     p.rt = (int)((rows + p.tr - 1) / p.tr);
 }
 // The split of a call along `span` tokens, at most (it does not fall as the span grows).
 int64_t splits_of(const DecArgs &p, int64_t groups, int64_t span) {
-    const int64_t unit = p.tr == CR ? CT : 4 * TT, want = p.tr == CR ? WANT / 2 : WANT;
+    const int64_t unit = p.tr > 16 ? CT : 4 * TT, want = p.tr == 256 ? WANT / 4 : p.tr == 128 ? WANT / 2 : WANT;
     int64_t splits = (want + groups - 1) / groups;
     if (p.tr == 16) splits = std::max(splits, std::min((span + FAR - 1) / FAR, FAR_SPLITS));
     return std::max<int64_t>(1, std::min(splits, (span + unit - 1) / unit));
 }
 void plan(const Kv4Attn &a, DecArgs &p) {
-    tiles_of(a.max_q, a.hq / a.geo.hkv, p);
+    tiles_of(a.max_q, a.hq / a.geo.hkv, a.geo.d, p);
     const int64_t groups = (int64_t)a.b * a.geo.hkv * p.rt;
     int64_t span = (int64_t)a.width << a.geo.page_log2;
     // a window's span: that of the tile's first to its last query, and the start's rounding down
@@ -715,7 +734,7 @@ void plan(const Kv4Attn &a, DecArgs &p) {
     int64_t splits = splits_of(p, groups, span);
     p.nw = p.tr == 16 && splits > 1 && wide(groups, span) ? WIDE : 4;
     if (p.nw == WIDE) splits = 1;
-    const int64_t unit = p.tr == CR ? CT : p.nw * TT;
+    const int64_t unit = p.tr > 16 ? CT : p.nw * TT;
     const int64_t chunk = ((span + splits - 1) / splits + unit - 1) / unit * unit;
     p.chunk = (int)chunk;
     p.splits = (int)((span + chunk - 1) / chunk);
@@ -727,7 +746,7 @@ void plan(const Kv4Attn &a, DecArgs &p) {
 // that goes to the wide workgroups needs none of it).
 size_t kv4_attn_ws_bytes(int b, int max_q, int hq, const Kv4Geom &g, int width) {
     DecArgs p;
-    tiles_of(max_q, hq / g.hkv, p);
+    tiles_of(max_q, hq / g.hkv, g.d, p);
     const int64_t groups = (int64_t)b * g.hkv * p.rt, splits = splits_of(p, groups, (int64_t)width << g.page_log2);
     return splits <= 1 ? 0 : (size_t)(groups * splits) * p.pr * (g.d + 4) * 4;
 }
@@ -739,9 +758,10 @@ hipError_t launch_kv4_attn(const Kv4Attn &a, hipStream_t s) {
     plan(a, p);
     const int64_t tiles = (int64_t)a.b * p.rt * a.geo.hkv;
     const dim3 grid((unsigned)(tiles * p.splits));
-    if (p.tr == CR) {
-        if (a.geo.d == 128) hipLaunchKernelGGL(k_kv4_chunk<128>, grid, dim3(256), 0, s, p);
-        else hipLaunchKernelGGL(k_kv4_chunk<64>, grid, dim3(256), 0, s, p);
+    if (p.tr > 16) {
+        if (p.tr == 256) hipLaunchKernelGGL((k_kv4_chunk<128, 512>), grid, dim3(512), 0, s, p);
+        else if (a.geo.d == 128) hipLaunchKernelGGL((k_kv4_chunk<128, 256>), grid, dim3(256), 0, s, p);
+        else hipLaunchKernelGGL((k_kv4_chunk<64, 256>), grid, dim3(256), 0, s, p);
     } else {
 #define DECODE(D, NW) hipLaunchKernelGGL((k_kv4_decode<D, NW>), grid, dim3(64 * NW), 0, s, p)
         if (a.geo.d == 128 && p.nw == WIDE) DECODE(128, WIDE);
