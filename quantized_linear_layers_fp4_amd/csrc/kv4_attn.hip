@@ -136,12 +136,15 @@ __device__ __forceinline__ float quarter_max(float x) {
 // Few rows (single tokens, drafts): 16 rows of one (sequence, key/value head) a workgroup, its NW
 // waves taking tiles of 32 tokens in turn and joining in LDS; `splits` workgroups share the tokens.
 // Bound by the cache's bytes.
-template <int D, int NW>
+// ONE: a tile lies in one page (of 32 tokens or more), so its addresses are a scalar base and constants of the
+// lane: about 45 of 270 vector instructions a tile.
+template <int D, int NW, bool ONE>
 __global__ __launch_bounds__(64 * NW, NW == 4 ? 3 : 1) void k_kv4_decode(DecArgs p) {
     constexpr int J = D / 16;   // columns a lane owns in the O^T tiles: J n + j
     constexpr int KS = D / 32;  // contraction steps of the scores
     const Kv4Attn &a = p.a;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n = lane & 15, h = lane >> 4;
+    const int lane = threadIdx.x & 63, n = lane & 15, h = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     int id = blockIdx.x;
     const int split = id % p.splits; id /= p.splits;
     const int head = id % a.geo.hkv; id /= a.geo.hkv;
@@ -190,48 +193,49 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? 3 : 1) void k_kv4_decode(DecArgs
     auto fetch = [&](int t0, int pk, int pv, Tile &x) {
         x.okk = (uint32_t)pk < (uint64_t)a.geo.pages;
         const bool okv = (uint32_t)pv < (uint64_t)a.geo.pages;
-        const uint8_t *kb = a.cache + ((int64_t)(x.okk ? pk : 0) * a.geo.hkv + head) * region;
-        const uint8_t *vb = a.cache + ((int64_t)(okv ? pv : 0) * a.geo.hkv + head) * region;
-        const int tk = ((t0 + 8 * (n >> 2)) & (P - 1)) + (n & 3), tv = (t0 + 8 * h) & (P - 1);
+        // codes' and scales' bases of K and of V; then a lane's token in them
+        const int64_t pk0 = x.okk ? pk : 0, pv0 = okv ? pv : 0;
+        const int in = ONE ? t0 & (P - 1) : 0;
+        const uint8_t *kc = a.cache + (pk0 * a.geo.hkv + head) * region + in * (D / 2), *ks = kc + a.geo.ks_off() + in - in * (D / 2);
+        const uint8_t *vc = a.cache + (pv0 * a.geo.hkv + head) * region + a.geo.v_off() + in * (D / 2);
+        const uint8_t *vs = vc + P * (D / 2) + in - in * (D / 2);
+        const int tk = (ONE ? 8 * (n >> 2) : (t0 + 8 * (n >> 2)) & (P - 1)) + (n & 3), tv = ONE ? 8 * h : (t0 + 8 * h) & (P - 1);
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
             const int tok = tk + 4 * s;
             if constexpr (D == 128) {
-                const u32x4 w = *reinterpret_cast<const u32x4 *>(kb + tok * (D / 2) + h * (D / 8));
+                const u32x4 w = *reinterpret_cast<const u32x4 *>(kc + (uint32_t)(tok * (D / 2) + h * (D / 8)));
 #pragma unroll
                 for (int i = 0; i < 4; ++i) x.kw[s][i] = w[i];
             } else {
-                const uint2 w = *reinterpret_cast<const uint2 *>(kb + tok * (D / 2) + h * (D / 8));
+                const uint2 w = *reinterpret_cast<const uint2 *>(kc + (uint32_t)(tok * (D / 2) + h * (D / 8)));
                 x.kw[s][0] = w.x;
                 x.kw[s][1] = w.y;
             }
-            x.ks[s] = kb[a.geo.ks_off() + (h * D / 128) * P + tok];
+            x.ks[s] = ks[(uint32_t)((h * D / 128) * P + tok)];
         }
         const int dw = D == 128 ? n : n >> 1;
-        const u32x4 *src = reinterpret_cast<const u32x4 *>(vb + a.geo.v_off() + ((tv >> 3) * (D / 8) + dw) * 32);
+        const u32x4 *src = reinterpret_cast<const u32x4 *>(vc + (uint32_t)(((tv >> 3) * (D / 8) + dw) * 32));
         const u32x4 y0 = src[0], y1 = src[1];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             x.vw[i] = y0[i];
             x.vw[4 + i] = y1[i];
         }
-        x.vs = *reinterpret_cast<const uint2 *>(vb + a.geo.vs_off() + (n * J / 32) * P + tv);
+        x.vs = *reinterpret_cast<const uint2 *>(vs + (uint32_t)((n * J / 32) * P + tv));
     };
 
     // two tiles of loads in flight: the next tile's bytes and the page indices of the one after it
     const int first = beg + wave * TT;
-    Tile cur;
+    Tile even, odd;
     int pk = 0, pv = 0;
-    if (first < end) {
-        fetch(first, page_at(first + 8 * (n >> 2)), page_at(first + 8 * h), cur);
-        pk = page_at(first + NW * TT + 8 * (n >> 2));
-        pv = page_at(first + NW * TT + 8 * h);
-    }
-    for (int t0 = first; t0 < end; t0 += NW * TT) {
-        Tile nxt;
+    auto pages_of = [&](int t0) {
+        pk = page_at(ONE ? t0 : t0 + 8 * (n >> 2));
+        pv = ONE ? pk : page_at(t0 + 8 * h);
+    };
+    auto tile = [&](Tile &cur, Tile &nxt, int t0) {
         fetch(t0 + NW * TT, pk, pv, nxt);
-        pk = page_at(t0 + 2 * NW * TT + 8 * (n >> 2));
-        pv = page_at(t0 + 2 * NW * TT + 8 * h);
+        pages_of(t0 + 2 * NW * TT);
         if constexpr (D == 64) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) cur.vw[i] >>= 16 * (n & 1);
@@ -290,7 +294,22 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? 3 : 1) void k_kv4_decode(DecArgs
             PV(3)
         }
 #undef PV
-        cur = nxt;
+    };
+    if (first < end) {
+        pages_of(first);
+        fetch(first, pk, pv, even);
+        pages_of(first + NW * TT);
+    }
+    if constexpr (ONE || NW == 4 || D == 64) {
+        for (int t0 = first; t0 < end; t0 += 2 * NW * TT) {
+            tile(even, odd, t0);
+            if (t0 + NW * TT < end) tile(odd, even, t0 + NW * TT);
+        }
+    } else {  // the 128 registers of 16 waves do not hold both tiles' addresses (9.2 | 14.8 us at 777 tokens)
+        for (int t0 = first; t0 < end; t0 += NW * TT) {
+            tile(even, odd, t0);
+            even = odd;
+        }
     }
 
     // the waves join: maxima, then sums and outputs over the common maximum, in wave order
@@ -763,7 +782,11 @@ hipError_t launch_kv4_attn(const Kv4Attn &a, hipStream_t s) {
         else if (a.geo.d == 128) hipLaunchKernelGGL((k_kv4_chunk<128, 256>), grid, dim3(256), 0, s, p);
         else hipLaunchKernelGGL((k_kv4_chunk<64, 256>), grid, dim3(256), 0, s, p);
     } else {
-#define DECODE(D, NW) hipLaunchKernelGGL((k_kv4_decode<D, NW>), grid, dim3(64 * NW), 0, s, p)
+#define DECODE(D, NW)                                                                                        \
+    do {                                                                                                     \
+        if (a.geo.page_log2 >= 5) hipLaunchKernelGGL((k_kv4_decode<D, NW, true>), grid, dim3(64 * NW), 0, s, p); \
+        else hipLaunchKernelGGL((k_kv4_decode<D, NW, false>), grid, dim3(64 * NW), 0, s, p);                   \
+    } while (0)
         if (a.geo.d == 128 && p.nw == WIDE) DECODE(128, WIDE);
         else if (a.geo.d == 128) DECODE(128, 4);
         else if (p.nw == WIDE) DECODE(64, WIDE);
