@@ -93,9 +93,10 @@ __global__ __launch_bounds__(256) void k_kv4_write(uint8_t *__restrict__ cache, 
         const int tok = (int)(slot[0] & (P - 1));
         uint8_t *base = cache + ((slot[0] >> g.page_log2) * g.hkv + head) * g.region();
 #pragma unroll
-        for (int u = 0; u < U; ++u) *reinterpret_cast<uint32_t *>(base + (tok + u) * (D / 2) + lane * 4) = ck[u];
-        *reinterpret_cast<uint4 *>(base + g.v_off() + ((tok >> 3) * L + lane) * 32 + (tok & 4) * 4) =
-            make_uint4(cv[0], cv[U > 1 ? 1 : 0], cv[U > 2 ? 2 : 0], cv[U > 3 ? 3 : 0]);
+        for (int u = 0; u < U; ++u)
+            __builtin_nontemporal_store(ck[u], reinterpret_cast<uint32_t *>(base + (tok + u) * (D / 2) + lane * 4));
+        __builtin_nontemporal_store(u32x4{cv[0], cv[U > 1 ? 1 : 0], cv[U > 2 ? 2 : 0], cv[U > 3 ? 3 : 0]},
+                                    reinterpret_cast<u32x4 *>(base + g.v_off() + ((tok >> 3) * L + lane) * 32 + (tok & 4) * 4));
         if ((lane & 3) == 0) {
             uint32_t wk = 0, wv = 0;
 #pragma unroll
@@ -137,12 +138,13 @@ __device__ __forceinline__ void e2m1_unpack8(uint32_t w, float s, float v[8]) {
 template <int DT>
 __device__ __forceinline__ void store8(void *Y, int64_t elem, const float v[8]) {
     if constexpr (DT == DT_BF16) {
-        *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(Y) + elem) = make_uint4(
-            bf16_pack2(v[0], v[1]), bf16_pack2(v[2], v[3]), bf16_pack2(v[4], v[5]), bf16_pack2(v[6], v[7]));
+        __builtin_nontemporal_store(
+            u32x4{bf16_pack2(v[0], v[1]), bf16_pack2(v[2], v[3]), bf16_pack2(v[4], v[5]), bf16_pack2(v[6], v[7])},
+            reinterpret_cast<u32x4 *>(static_cast<uint16_t *>(Y) + elem));
     } else {
-        float4 *y = reinterpret_cast<float4 *>(static_cast<float *>(Y) + elem);
-        y[0] = make_float4(v[0], v[1], v[2], v[3]);
-        y[1] = make_float4(v[4], v[5], v[6], v[7]);
+        v4f *y = reinterpret_cast<v4f *>(static_cast<float *>(Y) + elem);
+        __builtin_nontemporal_store(v4f{v[0], v[1], v[2], v[3]}, y);
+        __builtin_nontemporal_store(v4f{v[4], v[5], v[6], v[7]}, y + 1);
     }
 }
 
@@ -199,7 +201,7 @@ __global__ __launch_bounds__(256) void k_kv4_read(const uint8_t *__restrict__ ca
 }
 
 // U = 4 from two workgroups a CU on (of 256): measured on 16384 tokens of 32 heads, U = 1 | 4: write 82 | 78 us,
-// read 89 | 67 us
+// read 89 | 67 us; with U = 4's stores past the caches, which leaves them to the inputs, write 51 us
 #define KV4_LAUNCH(KERNEL, DT, D, S, U, ...)                                                              \
     do {                                                                                                  \
         const int per = 256 / (D / 8) * U;                                                                \
