@@ -145,10 +145,13 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? 3 : 1) void k_kv4_decode(DecArgs
     const Kv4Attn &a = p.a;
     const int lane = threadIdx.x & 63, n = lane & 15, h = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    // heads first, splits last: consecutive workgroups go to different XCDs, and with splits first each of
+    // eight XCDs would have one split of every sequence, the far ones mostly empty (85 against 62 us for 64
+    // sequences of unlike lengths); so the empty ones also come at the end
     int id = blockIdx.x;
-    const int split = id % p.splits; id /= p.splits;
     const int head = id % a.geo.hkv; id /= a.geo.hkv;
-    const int rt = id % p.rt, seq = id / p.rt;
+    const int rt = id % p.rt; id /= p.rt;
+    const int seq = id % a.b, split = id / a.b;
     const int row0 = rt * 16;
     const Span sp = span_of(a, p.g, seq, row0, 16);
     if (row0 >= sp.rows) return;
@@ -391,9 +394,9 @@ __global__ __launch_bounds__(NT, 2) void k_kv4_chunk(DecArgs p) {
     const int tid = threadIdx.x, lane = tid & 63, n = lane & 31, h = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     int id = blockIdx.x;
-    const int split = id % p.splits; id /= p.splits;
     const int head = id % a.geo.hkv; id /= a.geo.hkv;
-    const int rt = p.rt - 1 - id % p.rt, seq = id / p.rt;  // the longest first
+    const int rt = p.rt - 1 - id % p.rt; id /= p.rt;  // the longest first
+    const int seq = id % a.b, split = id / a.b;
     const int row0 = rt * CR;
     const Span sp = span_of(a, p.g, seq, row0, CR);
     if (row0 >= sp.rows) return;
