@@ -726,8 +726,9 @@ constexpr int64_t FAR_SPLITS = 64;  // ... into at most this many: sequences of 
 
 // A call of few (sequence, head, tile)s over few tokens goes to workgroups of WIDE waves instead of several
 // of four: they join in LDS, which saves the second launch (about 4 us of the host's time).  On the
-// device, split | wide, us, d 128: 8 groups 7.3 | 7.1 at 512 tokens, 7.5 | 9.2 at 1024, 7.8 | 13.2 at 2048;
-// 64 groups 9.2 | 9.4 at 1024, 12.6 | 13.5 at 2048; 256 groups 13.1 | 8.5 at 512, 15.6 | 11.4 at 1024, 33.0 | 29.7 at 4096, 58.5 | 53.2 at 8192.
+// device, split | wide, us, d 128: 8 groups 7.1 | 7.0 at 512 tokens, 7.2 | 8.8 at 1024, 7.6 | 12.4 at 2048;
+// 64 groups 9.0 | 9.1 at 1024, 12.1 | 13.1 at 2048; 256 groups 12.5 | 8.5 at 512, 15.1 | 12.0 at 1024,
+// 30.5 | 28.9 at 4096, 53.1 | 51.4 at 8192 (where unlike lengths would leave CUs idle).
 constexpr int WIDE = 16;
 bool wide(int64_t groups, int64_t span) { return groups <= 256 && span <= (groups >= 128 ? 4096 : groups >= 64 ? 2048 : 1024); }
 
