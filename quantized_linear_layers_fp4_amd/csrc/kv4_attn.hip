@@ -745,7 +745,9 @@ void tiles_of(int max_q, int g, int d, DecArgs &p) {
 int64_t splits_of(const DecArgs &p, int64_t groups, int64_t span) {
     const int64_t unit = p.tr > 16 ? CT : 4 * TT, want = p.tr == 256 ? WANT / 4 : p.tr == 128 ? WANT / 2 : WANT;
     int64_t splits = (want + groups - 1) / groups;
-    if (p.tr == 16) splits = std::max(splits, std::min((span + FAR - 1) / FAR, FAR_SPLITS));
+    // (a launch has at most 2^22 workgroups, far below the 2^32 threads that it may have)
+    if (p.tr == 16)
+        splits = std::max(splits, std::min({(span + FAR - 1) / FAR, FAR_SPLITS, ((int64_t)1 << 22) / std::max<int64_t>(groups, 1)}));
     return std::max<int64_t>(1, std::min(splits, (span + unit - 1) / unit));
 }
 void plan(const Kv4Attn &a, DecArgs &p) {
@@ -800,7 +802,7 @@ hipError_t launch_kv4_attn(const Kv4Attn &a, hipStream_t s) {
     hipError_t e = hipGetLastError();
     if (e == hipSuccess && p.splits > 1) {
         // one group a row where a row has no more splits than four groups' turns and the rows fill the device
-        const int groups = 1024 / a.geo.d, per = p.splits <= 4 && tiles * p.pr >= 8192 ? groups : 1;
+        const int groups = 1024 / a.geo.d, per = (p.splits <= 4 && tiles * p.pr >= 8192) || tiles * p.pr >= 1 << 22 ? groups : 1;
         const dim3 jg((unsigned)((tiles * p.pr + per - 1) / per));
         if (a.geo.d == 128 && per > 1) hipLaunchKernelGGL((k_kv4_join<128, 1>), jg, dim3(256), 0, s, p);
         else if (a.geo.d == 128) hipLaunchKernelGGL((k_kv4_join<128, 8>), jg, dim3(256), 0, s, p);

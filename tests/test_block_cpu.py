@@ -85,6 +85,16 @@ def test_attention_rejects():
     assert a(q=ODD) == EALIGN and a(o=C.c_void_p(0x100008)) == EALIGN
 
 
+def test_attention_workspace_of_many_sequences():
+    """A call of many sequences is not split into more workgroups than a launch can have: 2^21 (sequence, head)s
+    over a million tokens are split in two, not in 64."""
+    L = fp4.lib()
+    row = (128 + 4) * 4
+    assert L.fp4_kv4_attention_workspace_bytes(1 << 16, 1, 32, 32, 128, 128, 8192) == (1 << 21) * 2 * row
+    assert L.fp4_kv4_attention_workspace_bytes(1 << 10, 1, 32, 32, 128, 128, 8192) == (1 << 15) * 64 * row
+    assert L.fp4_kv4_attention_workspace_bytes(64, 1, 32, 8, 128, 64, 128) == 512 * 8 * 4 * row
+
+
 def test_python_checks():
     x = torch.zeros(4, 8)
     with pytest.raises(ValueError):
