@@ -266,3 +266,32 @@ def test_large_tiles(M, N, K):
         check_product(y, va, vb, out, K)
         for _ in range(3):
             assert torch.equal(fp4.block8_gemm(a, b, out), y)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+@pytest.mark.parametrize("M,K,N", [(1, 7300, 200), (2, 6500, 33), (1, 6150, 40), (16, 9000, 100), (5, 11008, 48), (17, 3300, 130),
+                                   (33, 6500, 64), (64, 6500, 17), (48, 4224, 300)])
+def test_few_rows_long(M, K, N, dt):
+    """More blocks along K than the waves have on their way at once: every wave refills, several times, and ends
+    anywhere in its turn."""
+    x, w = data(M, K, DT[dt], M + K), data(K, N, DT[dt], N, 0.02)
+    _, wq = fp4.block8_quantize(w.to(DEV), fp4.FP4_BLOCK_SQUARE, rows=False, cols=True)
+    a, b = ref.blocks(f64(x), 1, 128), ref.blocks(f64(w), 128, 128).T
+    for out in (torch.bfloat16, torch.float32):
+        y = fp4.block8_linear_forward(x.to(DEV), wq, out_dtype=out)
+        check_product(y, a, b, out, K)
+        z, _ = fp4.block8_linear_forward(x.to(DEV), wq, out_dtype=out, for_backward=True)
+        check_product(z, a, b, out, K)
+
+
+@pytest.mark.parametrize("M", [1, 2])
+def test_few_rows_wide(M):
+    """So many columns that a workgroup has four waves, each with more blocks than it has on their way."""
+    K, N = 4000, 16400
+    x, w = data(M, K, torch.bfloat16, 21), data(K, N, torch.bfloat16, 22, 0.02)
+    _, wq = fp4.block8_quantize(w.to(DEV), fp4.FP4_BLOCK_SQUARE, rows=False, cols=True)
+    a = ref.blocks(f64(x), 1, 128)
+    for out in (torch.bfloat16, torch.float32):
+        y = fp4.block8_linear_forward(x.to(DEV), wq, out_dtype=out)
+        for cols in (slice(0, 128), slice(8064, 8192), slice(16384, N)):
+            check_product(y[:, cols], a, ref.blocks(f64(w[:, cols]), 128, 128).T, out, K)

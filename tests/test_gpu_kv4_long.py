@@ -1,0 +1,158 @@
+"""The 4-bit cache's attention where every kernel runs several tiles a workgroup (needs an MI355X).
+
+Sizes are chosen by the plan's rules (rows a head, (sequence, head)s, tokens), so that the second buffers, the
+running maxima and the joins all take part.  A score is off by the sum's d additions (2^-23 each, of the magnitudes;
+twice that and a margin of 2^-15 are allowed) and the base change; a sum over n tokens by n additions of 2^-23 more;
+the output adds P's rounding to bf16 (2^-8), the score's error as a factor on both sums, and its own rounding.
+"""
+import numpy as np
+import pytest
+import torch
+
+import block_ref as ref
+import quantized_linear_layers_fp4_amd as fp4
+from test_gpu_kv4 import DEV, Case, f64
+
+pytestmark = pytest.mark.gpu
+
+
+def put(c, i, t, k, v):
+    """Token t of sequence i becomes (k, v) (heads x d), in the cache and in the case's own copy."""
+    slot = torch.tensor([int(c.table[i, t // c.page]) * c.page + t % c.page], device=DEV)
+    fp4.kv4_write(c.cache, k[None].to(DEV), v[None].to(DEV), slot)
+    bad = ~np.isfinite(f64(k)).all(1) | ~np.isfinite(f64(v)).all(1)
+    for store, x in ((c.k, k), (c.v, v)):
+        val = ref.cache_values(np.where(np.isfinite(f64(x)), f64(x), 0)[None])[0]
+        val[bad] = np.nan
+        store[i][t] = val
+
+
+def expected(c, window, scale, hidden=None):
+    """o, lse and the magnitudes behind them in 64 bits; hidden[i]: tokens whose page is none of the cache's."""
+    nq, hq, d = c.q.shape
+    q = f64(c.q)
+    o, lse = np.zeros(q.shape), np.full((nq, hq), -np.inf)
+    omag, smag = np.zeros(q.shape), np.zeros((nq, hq))
+    for i, n in enumerate(c.lens):
+        r0, ql = c.starts[i], c.starts[i + 1] - c.starts[i]
+        hkv = c.k[i].shape[1]
+        g = hq // hkv
+        pos, tok = n - ql + np.arange(ql)[:, None], np.arange(n)[None]
+        see = (tok <= pos) & ((tok > pos - window) if window else True)
+        if hidden and i in hidden:
+            see = see & ~np.isin(tok, hidden[i])
+        if n == 0 or not ql:
+            continue
+        for h in range(hkv):
+            qq = q[r0:r0 + ql, h * g:(h + 1) * g].reshape(ql * g, d)
+            kk, vv = c.k[i][:, h], c.v[i][:, h]
+            sr = np.repeat(see, g, 0)
+            with np.errstate(invalid="ignore"):
+                s = np.where(sr, qq @ kk.T * scale, -np.inf)
+                m = s.max(1, keepdims=True)
+                p = np.exp(s - np.where(np.isneginf(m), 0, m))
+                l = p.sum(1, keepdims=True)
+                vz = np.where(np.isfinite(vv), vv, 0)
+                out = np.where(l == 0, 0, p @ vz / np.where(l == 0, 1, l))
+                mag = np.where(l == 0, 0, p @ np.abs(vz) / np.where(l == 0, 1, l))
+                ls = np.where(l == 0, -np.inf, m + np.log(np.where(l == 0, 1, l)))
+                sm = np.where(sr, np.abs(qq) @ np.abs(kk).T, 0).max(1)
+            rows, heads = slice(r0, r0 + ql), slice(h * g, (h + 1) * g)
+            o[rows, heads], omag[rows, heads] = out.reshape(ql, g, d), mag.reshape(ql, g, d)
+            lse[rows, heads], smag[rows, heads] = ls.reshape(ql, g), sm.reshape(ql, g) * abs(scale)
+    return o, lse, omag, smag
+
+
+def check(c, window=0, scale=None, hidden=None, **kw):
+    scale = c.d ** -0.5 if scale is None else scale
+    o, lse = (f64(t) for t in c.run(window, scale=scale, **kw))
+    want, wl, omag, smag = expected(c, window, scale, hidden)
+    n = max(c.lens)
+    nan, none = np.isnan(wl), np.isneginf(wl)
+    assert np.array_equal(np.isneginf(lse), none) and (o[none] == 0).all()
+    assert np.isnan(lse[nan]).all() and np.isnan(o[nan]).all()
+    ok = ~nan & ~none
+    assert np.isfinite(o[ok]).all() and np.isfinite(lse[ok]).all()
+    ds = smag[ok] * (32 * 2.0 ** -20 + c.d * 2.0 ** -23) + 2.0 ** -21
+    err = np.abs(lse[ok] - wl[ok])
+    assert (err <= ds + 2.0 ** -21 * (1 + np.abs(wl[ok])) + n * 2.0 ** -23).all(), float(err.max())
+    tol = omag[ok] * (2.0 ** -8 + 2 * ds[:, None] + 2.0 ** -16 + n * 2.0 ** -22) + np.abs(want[ok]) * 2.0 ** -8 + 1e-30
+    err = np.abs(o[ok] - want[ok])
+    assert (err <= tol).all(), float((err / tol).max())
+
+
+# lens, queries a sequence, query heads, key/value heads, page
+PATHS = {
+    # one launch of sixteen waves, several tiles a wave
+    "wide": ([3001, 2900, 2048, 1537, 33] + [1200] * 11, 1, 16, 8, 64),
+    "wide_page16": ([1000, 517, 1024, 0], 1, 10, 10, 16),
+    # four waves, split, six tiles a wave at most
+    "split": ([3000, 2999, 2500, 1, 129] + [777] * 10, 1, 20, 20, 32),
+    "split_page16": ([2100, 1800] + [400] * 13, 2, 20, 20, 16),
+    # four waves, one workgroup a (sequence, head)
+    "one": ([700, 513, 641, 2, 31] + [300] * 27, 1, 32, 32, 128),
+    # two splits of many rows, joined a group of lanes to a row
+    "join_rows": ([1500, 1499, 1000, 770] + [769] * 12, 1, 512, 32, 64),
+}
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("name", PATHS)
+def test_decode_of_several_tiles(name, d):
+    lens, t, hq, hkv, page = PATHS[name]
+    c = Case(lens, [t] * len(lens), hq, hkv, d, page)
+    for i, n in enumerate(lens[:3]):  # the maximum moves in the last and in a middle tile
+        for at in (n - 1, n // 2):
+            if 0 <= at < n:
+                g = torch.Generator().manual_seed(at)
+                put(c, i, at, (torch.randn(hkv, d, generator=g) * 6).bfloat16(), torch.randn(hkv, d, generator=g).bfloat16())
+    check(c)
+    check(c, window=600)
+
+
+# rows a head over 32, so the many-rows kernel: lens, queries, query heads, key/value heads, page
+ROWS = {
+    # one workgroup a row tile, five and fewer tiles of 64 tokens; 40 and 320 rows a head
+    "unsplit": ([300, 299, 256, 65, 64, 40, 200, 129], 40, 64, 64, 16),
+    "unsplit_wide": ([300, 257, 193, 64, 32, 128, 129, 320], 40, 256, 32, 32),
+    # three tiles a split, row tiles of 128 and of 256
+    "split": ([1300, 1215, 700, 90], 40, 16, 16, 64),
+    "split_wide": ([1400, 1399], 70, 64, 16, 128),
+    # four splits of many rows, joined a group of lanes to a row
+    "join_rows": ([800, 799, 513, 100], 100, 32, 32, 16),
+}
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("name", ROWS)
+def test_chunks_of_several_tiles(name, d):
+    lens, t, hq, hkv, page = ROWS[name]
+    c = Case(lens, [min(t, n) for n in lens], hq, hkv, d, page)
+    for i, n in enumerate(lens[:3]):
+        for at in (n - min(t, n), n // 2):
+            g = torch.Generator().manual_seed(at)
+            put(c, i, at, (torch.randn(hkv, d, generator=g) * 6).bfloat16(), torch.randn(hkv, d, generator=g).bfloat16())
+    check(c)
+    check(c, window=150)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("lens,t,hq,hkv,page", [
+    ([3000] * 4, 1, 16, 8, 64), ([2500] * 15, 1, 20, 20, 16), ([1290, 1300], 50, 16, 16, 32), ([320] * 8, 40, 64, 64, 16),
+    ([1400, 1300], 70, 64, 16, 64)])
+def test_poisoned_tokens_and_bad_pages_in_later_tiles(lens, t, hq, hkv, page, d):
+    """Hidden pages and a token with a NaN in one head, tiles apart: rows that see it are NaN in that head's
+    queries and finite in the others', and hidden tokens count nowhere."""
+    c = Case(lens, [t] * len(lens), hq, hkv, d, page)
+    table, hidden = c.table.clone(), {}
+    for i, n in enumerate(lens):
+        pages = [p for p in (1, n // page // 2, n // page - 2) if 0 < p < n // page]
+        for j, p in enumerate(pages):
+            table[i, p] = (-1, c.pages, 2 ** 31 - 1)[j % 3]
+        hidden[i] = np.concatenate([np.arange(p * page, (p + 1) * page) for p in pages])
+    bad = torch.ones(hkv, d, dtype=torch.bfloat16)
+    bad[1, 3] = float("nan")
+    at = [x for x in range(lens[0] - 20, lens[0]) if x not in hidden[0]][0]
+    put(c, 0, at, bad, torch.ones(hkv, d, dtype=torch.bfloat16))
+    check(c, hidden=hidden, pages=table.to(DEV))
+    check(c, window=200, hidden=hidden, pages=table.to(DEV))
