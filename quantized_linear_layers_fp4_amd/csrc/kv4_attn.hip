@@ -411,7 +411,9 @@ __global__ __launch_bounds__(NT, 2) void k_kv4_chunk(DecArgs p) {
     const int vhi = live ? min(pos + 1, end) : 0, vlo = a.window ? pos - a.window + 1 : 0;
     const Span sw = span_of(a, p.g, seq, row0 + wave * 32, 32);
     const bool neg = p.c < 0.0f;  // the maximum is taken before the scale: a negative one goes to q
-    const float c = neg ? -p.c : p.c;
+    // A scale of 0 becomes the smallest float: a masked score, -inf here, stays -inf under it (-inf * 0 would be
+    // NaN), and a finite one stays below 2^-21, as good as 0.
+    const float c = p.c == 0.0f ? 0x1p-149f : neg ? -p.c : p.c;
     v8bf qf[KS];
 #pragma unroll
     for (int i = 0; i < KS; ++i) {

@@ -156,3 +156,15 @@ def test_poisoned_tokens_and_bad_pages_in_later_tiles(lens, t, hq, hkv, page, d)
     put(c, 0, at, bad, torch.ones(hkv, d, dtype=torch.bfloat16))
     check(c, hidden=hidden, pages=table.to(DEV))
     check(c, window=200, hidden=hidden, pages=table.to(DEV))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("t,window", [(4, 0), (40, 0), (40, 70), (300, 0), (300, 70)])
+def test_zero_scale_is_the_mean(t, window, d):
+    """All visible tokens weigh the same, in either kernel, with hidden pages and a sequence shorter than its queries."""
+    c = Case([400, 33], [t, min(t, 40)], 4, 2, d, 16)
+    check(c, window, scale=0.0)
+    check(c, window, scale=-0.0)
+    table = c.table.clone()
+    table[0, 3] = -1
+    check(c, window, scale=0.0, hidden={0: np.arange(48, 64)}, pages=table.to(DEV))
