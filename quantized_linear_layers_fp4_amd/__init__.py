@@ -618,19 +618,22 @@ def kv4_read(cache: KV4Cache, slots: torch.Tensor, d: int | None = None, out_dty
 
 
 def kv4_attention_workspace(q: torch.Tensor, cache: KV4Cache, pages: torch.Tensor, max_q: int = 1) -> torch.Tensor:
-    """A workspace for kv4_attention with these sizes and any window."""
+    """A workspace for kv4_attention with these sizes and any window (max_q as there: q's rows if it is not given
+    with q_start)."""
     n = lib().fp4_kv4_attention_workspace_bytes(pages.shape[0], max_q, q.shape[1], cache.heads, cache.d, cache.page,
                                                 pages.shape[1])
     return torch.empty(max(n, 16), dtype=torch.uint8, device=q.device)
 
 
 def kv4_attention(q: torch.Tensor, cache: KV4Cache, pages: torch.Tensor, lens: torch.Tensor,
-                  q_start: torch.Tensor | None = None, max_q: int = 1, window: int = 0, scale: float | None = None,
+                  q_start: torch.Tensor | None = None, max_q: int | None = None, window: int = 0, scale: float | None = None,
                   return_lse: bool = False, ws: torch.Tensor | None = None):
     """Causal attention of packed bf16 queries q (nq x hq x d) over the cache.  pages: int32 page table
     (b x width); lens: int32 tokens of each sequence in the cache, its queries' own among them; q_start: int32
-    b + 1 offsets of the sequences' queries (at most max_q each), or None for one query a sequence;
-    window: tokens a query sees (0: all).  A query that sees nothing gets 0 and lse -inf."""
+    b + 1 offsets of the sequences' queries, or None for one query a sequence; max_q: the most queries of a
+    sequence (None: as many as q has, or 1 without q_start; a close bound is faster, and needs less workspace);
+    window: tokens a query sees (0: all).  A query that sees nothing gets 0 and lse -inf, and so does one past its
+    sequence's first max_q, before q_start[0] or from q_start[b] on."""
     if q.dtype != torch.bfloat16:
         raise TypeError(f"expected bfloat16 queries, got {q.dtype}")
     if not q.is_cuda or q.dim() != 3 or q.shape[2] != cache.d or q.stride(2) != 1:
@@ -649,10 +652,16 @@ def kv4_attention(q: torch.Tensor, cache: KV4Cache, pages: torch.Tensor, lens: t
         raise ValueError("expected an int32 page table (b, width) on a HIP device, rows contiguous")
     if q_start is None and nq != b:
         raise ValueError(f"{nq} queries for {b} sequences without q_start")
+    if max_q is None:
+        max_q = 1 if q_start is None else nq
     _same_device(q, cache.data, pages, lens, q_start, ws)
     o = torch.empty_like(q, memory_format=torch.contiguous_format)
     lse = torch.empty(nq, hq, dtype=torch.float32, device=q.device) if return_lse else None
-    if nq and b:
+    if nq and not b:  # no sequence owns a query
+        o.zero_()
+        if return_lse:
+            lse.fill_(float("-inf"))
+    elif nq:
         if ws is None:
             ws = kv4_attention_workspace(q, cache, pages, max_q)
         _check(lib().fp4_kv4_attention(_ptr(q), q.stride(0), q.stride(1), nq, hq, _ptr(q_start), _ptr(lens), b, max_q,

@@ -45,8 +45,15 @@ struct DecArgs {
     int nw;           // waves of a workgroup
     int splits;       // workgroups along the tokens
     int chunk;        // tokens each takes (a multiple of the unit, nw * TT or CT)
+    int work, blanks; // workgroups that attend; those after them, for the queries of no row tile
     float c;          // scale * log2(e)
 };
+
+// Entry i of a table that no kernel here writes: a scalar load where i is uniform, though other code of the kernel
+// stores first (as vector loads: 77 instead of 69 us for 64 sequences to 8192 tokens).
+__device__ __forceinline__ int fixed(const int32_t *p, int64_t i) {
+    return ((const __attribute__((address_space(4))) int32_t *)p)[i];
+}
 
 // What one workgroup's rows see: rows of sequence `seq`, tile rt.
 struct Span {
@@ -58,9 +65,9 @@ struct Span {
 
 __device__ __forceinline__ Span span_of(const Kv4Attn &a, int g, int seq, int row0, int nrows) {
     Span s;
-    s.len = a.lens[seq];
-    s.qbeg = a.q_start ? max(a.q_start[seq], 0) : seq;
-    s.qlen = a.q_start ? min(a.q_start[seq + 1], a.nq) - s.qbeg : 1;
+    s.len = fixed(a.lens, seq);
+    s.qbeg = a.q_start ? max(fixed(a.q_start, seq), 0) : seq;
+    s.qlen = a.q_start ? min(fixed(a.q_start, seq + 1), a.nq) - s.qbeg : 1;
     s.rows = min(max(s.qlen, 0), a.max_q) * g;
     const int cap = min(s.len, a.width << a.geo.page_log2);
     if (row0 >= s.rows) {
@@ -74,6 +81,26 @@ __device__ __forceinline__ Span span_of(const Kv4Attn &a, int g, int seq, int ro
     s.lo = a.window ? max(p0 - a.window + 1, 0) & ~(TT - 1) : 0;
     s.full_lo = a.window ? max(p1 - a.window + 1, 0) : 0;
     return s;
+}
+
+// Queries that no sequence's row tiles cover get zeros and lse = -inf: those past a sequence's first max_q, before
+// q_start[0] and from q_start[b] on (a padded batch).  Workgroups of their own at the grid's end do it, `id` the
+// sequence's and every p.blanks-th of the others.
+__device__ __forceinline__ void blank_rows(const DecArgs &p, int id, int threads) {
+    const Kv4Attn &a = p.a;
+    auto blank = [&](int from, int to, int step) {
+        for (int64_t i = from; i < to; i += step) {
+            u32x4 *o = reinterpret_cast<u32x4 *>(a.o + i * a.hq * a.geo.d);
+            for (int j = threadIdx.x; j < a.hq * a.geo.d / 8; j += threads) o[j] = u32x4{0, 0, 0, 0};
+            if (a.lse)
+                for (int j = threadIdx.x; j < a.hq; j += threads) a.lse[i * a.hq + j] = -INFINITY;
+        }
+    };
+    auto start = [&](int i) { return min(max(fixed(a.q_start, i), 0), a.nq); };
+    const int first = start(0), end = start(a.b);
+    if (id < first) blank(id, first, p.blanks);
+    if (id < a.nq - end) blank(end + id, a.nq, p.blanks);
+    if (id < a.b && start(id + 1) - start(id) > a.max_q) blank(start(id) + a.max_q, start(id + 1), 1);
 }
 
 // E8M0 byte I of a dword as a scale: its exponent field.
@@ -149,6 +176,7 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? 3 : 1) void k_kv4_decode(DecArgs
     // eight XCDs would have one split of every sequence, the far ones mostly empty (85 against 62 us for 64
     // sequences of unlike lengths); so the empty ones also come at the end
     int id = blockIdx.x;
+    if (id >= p.work) return blank_rows(p, id - p.work, 64 * NW);
     const int head = id % a.geo.hkv; id /= a.geo.hkv;
     const int rt = id % p.rt; id /= p.rt;
     const int seq = id % a.b, split = id / a.b;
@@ -192,7 +220,7 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? 3 : 1) void k_kv4_decode(DecArgs
         uint2 vs;
         bool okk;  // the page is one of the cache's (K's lane; V's tokens are the same pages)
     };
-    auto page_at = [&](int t) { return table[min(t, end - 1) >> lg]; };
+    auto page_at = [&](int t) { return fixed(table, min(t, end - 1) >> lg); };
     auto fetch = [&](int t0, int pk, int pv, Tile &x) {
         x.okk = (uint32_t)pk < (uint64_t)a.geo.pages;
         const bool okv = (uint32_t)pv < (uint64_t)a.geo.pages;
@@ -394,6 +422,7 @@ __global__ __launch_bounds__(NT, 2) void k_kv4_chunk(DecArgs p) {
     const int tid = threadIdx.x, lane = tid & 63, n = lane & 31, h = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     int id = blockIdx.x;
+    if (id >= p.work) return blank_rows(p, id - p.work, NT);
     const int head = id % a.geo.hkv; id /= a.geo.hkv;
     const int rt = p.rt - 1 - id % p.rt; id /= p.rt;  // the longest first
     const int seq = id % a.b, split = id / a.b;
@@ -438,7 +467,7 @@ __global__ __launch_bounds__(NT, 2) void k_kv4_chunk(DecArgs p) {
     uint32_t kw[2][KD], vw[2][KD], ks[2], vs[2];
     const uint8_t *const headp = a.cache + (int64_t)head * region;
     const int64_t pstride = (int64_t)a.geo.hkv * region;
-    auto page_at = [&](int t) { return table[min(t, end - 1) >> lg]; };
+    auto page_at = [&](int t) { return fixed(table, min(t, end - 1) >> lg); };
     // pages outside the cache: their tokens' bytes are any page's, and their scores are masked
     bool okk[2];
     auto fetch = [&](auto set, int t0, int pk, int pv) {
@@ -784,7 +813,9 @@ hipError_t launch_kv4_attn(const Kv4Attn &a, hipStream_t s) {
     p.c = a.scale * LOG2E;
     plan(a, p);
     const int64_t tiles = (int64_t)a.b * p.rt * a.geo.hkv;
-    const dim3 grid((unsigned)(tiles * p.splits));
+    p.work = (int)(tiles * p.splits);  // below 2^23
+    p.blanks = a.q_start ? std::max(a.b, std::min(a.nq, 64)) : 0;
+    const dim3 grid((unsigned)(p.work + p.blanks));
     if (p.tr > 16) {
         if (p.tr == 256) hipLaunchKernelGGL((k_kv4_chunk<128, 512>), grid, dim3(512), 0, s, p);
         else if (a.geo.d == 128) hipLaunchKernelGGL((k_kv4_chunk<128, 256>), grid, dim3(256), 0, s, p);

@@ -168,3 +168,47 @@ def test_zero_scale_is_the_mean(t, window, d):
     table = c.table.clone()
     table[0, 3] = -1
     check(c, window, scale=0.0, hidden={0: np.arange(48, 64)}, pages=table.to(DEV))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("qlens,mq", [([9, 2, 30], 3), ([80, 40, 1], 40), ([300, 5, 0], 70)])
+def test_queries_of_no_computed_row(qlens, mq, d):
+    """Queries past max_q, before the first offset and after the last are zeros and -inf, whatever the memory held."""
+    c = Case([200, 120, 500], qlens, 8, 2, d, 16)
+    front, back = 7, 11
+    q = torch.cat([c.q[:1].expand(front, -1, -1), c.q, c.q[:1].expand(back, -1, -1)]).contiguous().to(DEV)
+    starts = torch.tensor(c.starts, dtype=torch.int32, device=DEV) + front
+    want, wl = c.run(max_q=max(qlens))
+    computed = torch.zeros(q.shape[0], dtype=torch.bool, device=DEV)
+    rows = torch.cat([c.starts[i] + torch.arange(min(n, mq)) for i, n in enumerate(qlens)]).to(DEV)
+    computed[rows + front] = True
+    for _ in range(2):
+        held = [torch.full_like(q, 7.0), torch.full(q.shape[:2], 7.0, device=DEV)]
+        del held  # the outputs come from this memory
+        o, lse = c.run(q=q, q_start=starts, max_q=mq)
+        assert (o[~computed] == 0).all() and torch.isneginf(lse[~computed]).all()
+        assert torch.allclose(o[rows + front].float(), want[rows].float(), atol=2.0 ** -5, rtol=2.0 ** -6)
+        assert torch.allclose(lse[rows + front], wl[rows], atol=1e-4)
+    o = c.run(q=q, q_start=starts, max_q=mq, return_lse=False)
+    assert (o[~computed] == 0).all()
+
+
+def test_max_q_not_given():
+    """With offsets and no bound on a sequence's queries all of them are computed; without offsets there is one."""
+    c = Case([130, 50, 9], [60, 3, 2], 4, 2, 64, 16)
+    check(c, max_q=None)
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device=DEV)  # noqa: E731
+    q = c.q[:3].to(DEV)
+    assert torch.equal(fp4.kv4_attention(q, c.cache, c.table.to(DEV), i32(130, 50, 9)),
+                       fp4.kv4_attention(q, c.cache, c.table.to(DEV), i32(130, 50, 9), q_start=i32(0, 1, 2, 3), max_q=1))
+
+
+def test_no_sequences():
+    """Queries of no sequence at all: zeros and -inf."""
+    c = Case([10], [1], 4, 2, 64, 16)
+    held = [torch.full((5, 4, 64), 7.0, dtype=torch.bfloat16, device=DEV), torch.full((5, 4), 7.0, device=DEV)]
+    del held
+    e = torch.zeros(1, dtype=torch.int32, device=DEV)
+    o, lse = fp4.kv4_attention(torch.ones(5, 4, 64, dtype=torch.bfloat16, device=DEV), c.cache, c.table[:0].to(DEV), e[:0],
+                               q_start=e, return_lse=True)
+    assert (o == 0).all() and torch.isneginf(lse).all()
