@@ -422,7 +422,8 @@ fp4_status fp4_kv4_read(const uint8_t *cache, int64_t pages, int32_t page, int32
  *   q_start  device int32[b + 1]: queries q_start[i] .. q_start[i+1] - 1 belong to sequence i (at most max_q of
  *            them); or NULL: query i belongs to sequence i (nq = b, max_q = 1)
  *   lens     device int32[b]: tokens of each sequence in the cache, its queries' own among them: query j of
- *            qlen stands at position len - qlen + j
+ *            qlen stands at position len - qlen + j (a negative length counts as 0, an offset outside the queries as the
+ *            nearest one)
  *   table    device int32, b rows of `width` page indices, rows table_stride apart; entries outside the cache
  *            are as if their tokens were masked
  *   window   0, or the number of tokens a query sees, its own included

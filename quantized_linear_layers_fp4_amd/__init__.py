@@ -666,7 +666,7 @@ def kv4_attention(q: torch.Tensor, cache: KV4Cache, pages: torch.Tensor, lens: t
             ws = kv4_attention_workspace(q, cache, pages, max_q)
         _check(lib().fp4_kv4_attention(_ptr(q), q.stride(0), q.stride(1), nq, hq, _ptr(q_start), _ptr(lens), b, max_q,
                                        _ptr(pages), max(pages.stride(0), pages.shape[1]), pages.shape[1],
-                                       _ptr(cache.data), cache.pages, cache.page, cache.heads, d, window,
+                                       _ptr(cache.data), cache.pages, cache.page, cache.heads, d, min(window, 0x7FFFFFFF),
                                        d ** -0.5 if scale is None else float(scale), _ptr(o), _ptr(lse), _ptr(ws),
                                        ws.numel(), _stream(q)))
     return (o, lse) if return_lse else o

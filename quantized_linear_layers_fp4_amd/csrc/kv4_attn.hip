@@ -63,23 +63,30 @@ struct Span {
     int full_lo, full_hi;  // tokens that all of its rows see
 };
 
+// The first token that a query at position p sees (0 for p below 0, which sees none); no difference here leaves the
+// integers, whatever the window.
+__device__ __forceinline__ int first_seen(int window, int p) { return window && p >= window ? p - window + 1 : 0; }
+
+// The query at offset entry i, inside the queries whatever the entry says.
+__device__ __forceinline__ int query_at(const Kv4Attn &a, int i) { return min(max(fixed(a.q_start, i), 0), a.nq); }
+
 __device__ __forceinline__ Span span_of(const Kv4Attn &a, int g, int seq, int row0, int nrows) {
     Span s;
-    s.len = fixed(a.lens, seq);
-    s.qbeg = a.q_start ? max(fixed(a.q_start, seq), 0) : seq;
-    s.qlen = a.q_start ? min(fixed(a.q_start, seq + 1), a.nq) - s.qbeg : 1;
+    s.len = max(fixed(a.lens, seq), 0);
+    s.qbeg = a.q_start ? query_at(a, seq) : seq;
+    s.qlen = a.q_start ? query_at(a, seq + 1) - s.qbeg : 1;
     s.rows = min(max(s.qlen, 0), a.max_q) * g;
     const int cap = min(s.len, a.width << a.geo.page_log2);
-    if (row0 >= s.rows) {
-        s.lo = s.hi = s.full_lo = s.full_hi = 0;
-        return s;
-    }
+    s.lo = s.hi = s.full_lo = s.full_hi = 0;
+    if (row0 >= s.rows) return s;
     const int j0 = row0 / g, j1 = min(row0 + nrows - 1, s.rows - 1) / g;
     const int p0 = s.len - s.qlen + j0, p1 = s.len - s.qlen + j1;
-    s.hi = max(min(p1 + 1, cap), 0);
+    const int lo = first_seen(a.window, p0) & ~(TT - 1), hi = max(min(p1 + 1, cap), 0);
+    if (lo >= hi) return s;
+    s.lo = lo;
+    s.hi = hi;
+    s.full_lo = first_seen(a.window, p1);
     s.full_hi = min(p0 + 1, cap);
-    s.lo = a.window ? max(p0 - a.window + 1, 0) & ~(TT - 1) : 0;
-    s.full_lo = a.window ? max(p1 - a.window + 1, 0) : 0;
     return s;
 }
 
@@ -96,11 +103,10 @@ __device__ __forceinline__ void blank_rows(const DecArgs &p, int id, int threads
                 for (int j = threadIdx.x; j < a.hq; j += threads) a.lse[i * a.hq + j] = -INFINITY;
         }
     };
-    auto start = [&](int i) { return min(max(fixed(a.q_start, i), 0), a.nq); };
-    const int first = start(0), end = start(a.b);
+    const int first = query_at(a, 0), end = query_at(a, a.b);
     if (id < first) blank(id, first, p.blanks);
     if (id < a.nq - end) blank(end + id, a.nq, p.blanks);
-    if (id < a.b && start(id + 1) - start(id) > a.max_q) blank(start(id) + a.max_q, start(id + 1), 1);
+    if (id < a.b && query_at(a, id + 1) - query_at(a, id) > a.max_q) blank(query_at(a, id) + a.max_q, query_at(a, id + 1), 1);
 }
 
 // E8M0 byte I of a dword as a scale: its exponent field.
@@ -191,7 +197,7 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? 3 : 1) void k_kv4_decode(DecArgs
     const bool live = row < sp.rows;
     const int qi = live ? row / p.g : 0, qh = live ? head * p.g + row % p.g : 0;
     const int pos = sp.len - sp.qlen + qi;
-    const int vhi = live ? pos + 1 : 0, vlo = a.window ? pos - a.window + 1 : 0;
+    const int vhi = live ? pos + 1 : 0, vlo = first_seen(a.window, pos);
     // q: lane h owns D/4 consecutive columns, KS operands of 8
     v8bf qf[KS];
 #pragma unroll
@@ -437,7 +443,7 @@ __global__ __launch_bounds__(NT, 2) void k_kv4_chunk(DecArgs p) {
     const bool live = row < sp.rows;
     const int qi = live ? row / p.g : 0, qh = live ? head * p.g + row % p.g : 0;
     const int pos = sp.len - sp.qlen + qi;
-    const int vhi = live ? min(pos + 1, end) : 0, vlo = a.window ? pos - a.window + 1 : 0;
+    const int vhi = live ? min(pos + 1, end) : 0, vlo = first_seen(a.window, pos);
     const Span sw = span_of(a, p.g, seq, row0 + wave * 32, 32);
     const bool neg = p.c < 0.0f;  // the maximum is taken before the scale: a negative one goes to q
     // A scale of 0 becomes the smallest float: a masked score, -inf here, stays -inf under it (-inf * 0 would be

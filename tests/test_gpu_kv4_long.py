@@ -212,3 +212,31 @@ def test_no_sequences():
     o, lse = fp4.kv4_attention(torch.ones(5, 4, 64, dtype=torch.bfloat16, device=DEV), c.cache, c.table[:0].to(DEV), e[:0],
                                q_start=e, return_lse=True)
     assert (o == 0).all() and torch.isneginf(lse).all()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 + 7, 2 ** 30, 1200])
+@pytest.mark.parametrize("lens,qlens", [([2, 1500, 0, 7], [7, 2, 5, 8]), ([2, 1500, 40, 5], [40, 50, 90, 60])])
+def test_largest_windows(lens, qlens, window, d):
+    """A window of any size, with sequences of more queries than tokens: their later queries see tokens."""
+    c = Case(lens, qlens, 8, 4, d, 32)
+    check(c, window)
+    if window > 1500:
+        for got, want in zip(c.run(window), c.run(0)):
+            assert torch.allclose(got.float(), want.float(), atol=2.0 ** -5, rtol=2.0 ** -6)
+
+
+@pytest.mark.parametrize("t", [3, 40])
+def test_lengths_and_offsets_out_of_range(t):
+    """A negative length is an empty sequence, and offsets count as the nearest query: the sequences beside them are as
+    they were."""
+    c = Case([200, 90, 33], [t, t, t], 8, 2, 64, 16)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=DEV)  # noqa: E731
+    want, wl = c.run()
+    for n in (-1, -2 ** 31):
+        o, lse = c.run(lens=i32([200, n, 33]))
+        assert torch.equal(o[:t], want[:t]) and torch.equal(o[2 * t:], want[2 * t:])
+        assert (o[t:2 * t] == 0).all() and torch.isneginf(lse[t:2 * t]).all()
+    for lo, hi in ((-2 ** 31, 2 ** 31 - 1), (-7, 3 * t + 5)):
+        o, lse = c.run(q_start=i32([lo, t, 2 * t, hi]))
+        assert torch.equal(o, want) and torch.equal(lse, wl)
