@@ -395,8 +395,8 @@ fp4_status fp4_block8_backward(const void *dY, int32_t dy_dtype, int64_t M, int6
 /* ---------------------------------------------------------------------------------------------
  * 4-bit key/value cache.  `pages` pages of `page` tokens (a power of two, 16 to 1024), hkv heads of
  * size d (64 or 128).  Each group of 32 values along d is held as E2M1 codes (nearest of x * 2^-e, ties to
- * even, saturating at 6, and at 3 where e = 126, as 4 * 2^126 is no fp32 number) and the byte e + 127, e the
- * smallest integer >= -127 with max|x| <= 7 * 2^e.
+ * even, saturating at 6) and the byte e + 127, e the smallest integer >= -127 with max|x| <= 7 * 2^e, and 125 where
+ * that would be 126, whose code 4 stands for no fp32 number.
  * A token whose key or value holds a NaN or infinity in a head reads back as NaN in that head, and
  * so do the attention rows that see it.  The caller zeroes the memory once, before the first use.
  * A slot is a token's place: page index * page + offset in the page. */
@@ -405,8 +405,9 @@ fp4_status fp4_block8_backward(const void *dY, int32_t dy_dtype, int64_t M, int6
 size_t fp4_kv4_cache_bytes(int64_t pages, int32_t page, int32_t hkv, int32_t d);
 
 /* Write n tokens: K and V (n x hkv x d, dtype fp32 or bf16, d contiguous, token and head strides in elements,
- * any element alignment) to slots[i] (slot_bytes 4: int32, 8: int64).  Slots outside the cache are skipped;
- * of two equal slots in one call, either token may stay. */
+ * any element alignment) to slots[i] (slot_bytes 4: int32, 8: int64).  Slots outside the cache are skipped.
+ * The slots of one call must differ: a slot that is given twice holds parts of either token, numbers that neither has
+ * (finite, or NaN if one of the two is), and other slots are not touched. */
 fp4_status fp4_kv4_write(uint8_t *cache, int64_t pages, int32_t page, int32_t hkv, int32_t d, const void *K,
                          const void *V, int32_t dtype, int64_t n, int64_t k_token_stride, int64_t k_head_stride,
                          int64_t v_token_stride, int64_t v_head_stride, const void *slots, int32_t slot_bytes,

@@ -586,7 +586,7 @@ def _slot_bytes(t: torch.Tensor, n: int) -> int:
 
 def kv4_write(cache: KV4Cache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor) -> None:
     """Quantize k and v (n x heads x d, fp32 or bf16, d contiguous) into the cache at slots (page index *
-    page + offset; those outside the cache are skipped)."""
+    page + offset; those outside the cache are skipped, and the others must differ)."""
     n = k.shape[0]
     shape = (n, cache.heads, cache.d)
     for t in (k, v):

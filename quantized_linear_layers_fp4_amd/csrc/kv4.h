@@ -12,6 +12,7 @@
 //   V scales  D/32 x P E8M0 bytes, group-major: eight tokens' bytes of a group are 8 bytes
 // A token whose key or value holds a NaN or an infinity (in that head) has K scale bytes 255 and
 // all codes and V scales 0: its scores are NaN where it is visible, and it adds nothing elsewhere.
+// Other scale bytes are 0 .. 252, under which every code is finite.
 #pragma once
 
 #include <hip/hip_runtime.h>

@@ -1,7 +1,7 @@
 // Writing keys and values into the 4-bit paged cache, and reading them back (layout: kv4.h).
 //
-// Groups of 32 values along the head take one E8M0 scale: e is the smallest exponent >= -127 with
-// max|x| <= 7 * 2^e, and codes are the nearest E2M1 values of x * 2^-e, ties to even, saturating at
+// Groups of 32 values along the head take one E8M0 scale: e is the smallest exponent of -127 .. 125 with
+// max|x| <= 7 * 2^e (125 if there is none), and codes are the nearest E2M1 values of x * 2^-e, ties to even, saturating at
 // 6: a group's maximum in (6, 7] * 2^e loses at most a seventh, which is no more than the half step
 // of 1 that rounding costs there anyway, and the group's other values keep the finer scale.  Both
 // kernels move each byte once and are bound by memory; 8 values a lane and token, D/8 lanes a (token, head).
@@ -65,23 +65,15 @@ __global__ __launch_bounds__(256) void k_kv4_write(uint8_t *__restrict__ cache, 
         }
         const uint64_t bad_all = __builtin_amdgcn_ballot_w64(max(mk, mv) >= 0x7F800000u);
         const bool bad = ((bad_all >> ((threadIdx.x & 63) / L * L)) & ((1ull << L) - 1)) != 0;
-        ek[u] = e8m0_of(mk, 2);
-        ev[u] = e8m0_of(mv, 2);
+        // at most 125: 6 * 2^125 is the largest code under any scale byte, so whatever a token's bytes are, of two
+        // tokens written at once even, they stay finite where the token is masked (0 * inf would be NaN)
+        ek[u] = min(e8m0_of(mk, 2), 252u);
+        ev[u] = min(e8m0_of(mv, 2), 252u);
         const float fk = e8m0_inv(ek[u]), fv = e8m0_inv(ev[u]);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             k[u][i] *= fk;
             v[u][i] *= fv;
-        }
-        // 4 * 2^126 is no fp32 number: there 3 is the largest code, so that whatever is held stays
-        // finite where its token is masked (0 * inf would be NaN)
-        if (ek[u] == 253u) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) k[u][i] = fminf(fmaxf(k[u][i], -3.0f), 3.0f);
-        }
-        if (ev[u] == 253u) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[u][i] = fminf(fmaxf(v[u][i], -3.0f), 3.0f);
         }
         ck[u] = bad ? 0u : e2m1_pack8(k[u]);
         cv[u] = bad ? 0u : e2m1_pack8(v[u]);

@@ -240,3 +240,32 @@ def test_lengths_and_offsets_out_of_range(t):
     for lo, hi in ((-2 ** 31, 2 ** 31 - 1), (-7, 3 * t + 5)):
         o, lse = c.run(q_start=i32([lo, t, 2 * t, hi]))
         assert torch.equal(o, want) and torch.equal(lse, wl)
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("n", [40, 16384])
+def test_scales_under_which_every_code_is_finite(n, dt):
+    """Groups up to the type's largest value: the exponent stops at 125, so that no scale byte of the cache makes an
+    infinity of any code, and the group's other values are as near as that scale allows."""
+    h, d, page = 2, 128, 32
+    g = torch.Generator().manual_seed(3)
+    k, v = torch.randn(n, h, d, generator=g), torch.randn(n, h, d, generator=g)
+    tops = torch.tensor([1.0, 2.0 ** 60, 2.0 ** 124, 2.0 ** 125, 2.0 ** 126, 2.0 ** 127 * 1.5, torch.finfo(dt).max])
+    for x, s in ((k, 0), (v, 3)):
+        x *= (tops[(torch.arange(n) + s) % 7] / 8)[:, None, None]
+        x[torch.arange(n), :, (torch.arange(n) * 5) % d] = tops[(torch.arange(n) + s) % 7][:, None]
+    k[5, 1, 2] = float("nan")
+    k, v = k.to(dt), v.to(dt)
+    c = fp4.kv4_cache(-(-n // page), page, h, d)
+    slots = torch.arange(n, device=DEV)
+    fp4.kv4_write(c, k.to(DEV), v.to(DEV), slots)
+    region = c.data.view(-1, page * (d + d // 16)).cpu()
+    kc, vc = page * d // 2, page * d // 32  # the bytes of a head's codes and of its scales
+    ks, vs = region[:, kc:kc + vc], region[:, 2 * kc + vc:]
+    assert int(vs.max()) == 252 and set(ks[ks > 252].tolist()) == {255}
+    for got, x in zip(fp4.kv4_read(c, slots, out_dtype=torch.float32), (k, v)):
+        y = np.where(np.isfinite(f64(x)), f64(x), 0).reshape(-1, 32)
+        e = np.minimum(ref.exponent(np.abs(y).max(1, keepdims=True), 7.0), 125)
+        want = (ref.nearest(y * np.exp2(-e.astype(float)), ref.E2M1) * np.exp2(e.astype(float))).reshape(n, h, d)
+        want[5, 1] = np.nan
+        assert np.array_equal(f64(got), want, equal_nan=True)
