@@ -8,6 +8,8 @@
 // are taken across 16 lanes, column maxima through LDS, and the transposed codes are turned in LDS
 // so that both outputs are written in whole 128-byte lines.  Bound by memory: es + 2 bytes an
 // element for both outputs.
+#include <algorithm>
+
 #include "block8.h"
 
 namespace fp4 {
@@ -181,27 +183,28 @@ __global__ __launch_bounds__(256) void k_block8_dequant(const uint8_t *__restric
                                                         const uint8_t *__restrict__ scales, int64_t R, int64_t C,
                                                         int64_t ld, int64_t srows, int sshift, void *__restrict__ Y) {
     const int64_t quads = ld / 4;
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= R * quads) return;
-    const int64_t r = i / quads, c = i % quads * 4;
-    const int64_t kb = c >> 7;
-    const uint32_t b = scales[((kb >> 2) * srows + (r >> sshift)) * 4 + (kb & 3)];
-    const int w = *reinterpret_cast<const int *>(codes + r * ld + c);
-    const float s = e8m0_value(b);
-    const float v[4] = {__builtin_amdgcn_cvt_f32_fp8(w, 0) * s, __builtin_amdgcn_cvt_f32_fp8(w, 1) * s,
-                        __builtin_amdgcn_cvt_f32_fp8(w, 2) * s, __builtin_amdgcn_cvt_f32_fp8(w, 3) * s};
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < R * quads; i += (int64_t)gridDim.x * 256) {
+        const int64_t r = i / quads, c = i % quads * 4;
+        const int64_t kb = c >> 7;
+        const uint32_t b = scales[((kb >> 2) * srows + (r >> sshift)) * 4 + (kb & 3)];
+        const int w = *reinterpret_cast<const int *>(codes + r * ld + c);
+        const float s = e8m0_value(b);
+        const float v[4] = {__builtin_amdgcn_cvt_f32_fp8(w, 0) * s, __builtin_amdgcn_cvt_f32_fp8(w, 1) * s,
+                            __builtin_amdgcn_cvt_f32_fp8(w, 2) * s, __builtin_amdgcn_cvt_f32_fp8(w, 3) * s};
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-        if (c + j < C) {
-            if constexpr (YDT == DT_F32) static_cast<float *>(Y)[r * C + c + j] = v[j];
-            else static_cast<uint16_t *>(Y)[r * C + c + j] = (uint16_t)(b == 255u ? 0x7FC0u : f32_to_bf16_bits(v[j]));
-        }
+        for (int j = 0; j < 4; ++j)
+            if (c + j < C) {
+                if constexpr (YDT == DT_F32) static_cast<float *>(Y)[r * C + c + j] = v[j];
+                else static_cast<uint16_t *>(Y)[r * C + c + j] = (uint16_t)(b == 255u ? 0x7FC0u : f32_to_bf16_bits(v[j]));
+            }
+    }
 }
 
 hipError_t launch_block8_dequant(const uint8_t *codes, const uint8_t *scales, int64_t R, int64_t C, bool square,
                                  void *Y, int y_dt, hipStream_t s) {
     const int64_t ld = (C + 127) / 128 * 128, n = R * (ld / 4);
-    const dim3 g((unsigned)((n + 255) / 256)), b(256);
+    // the largest matrix would take 2^32 threads, one more than a launch may have: from half of it on, a second turn
+    const dim3 g((unsigned)std::min<int64_t>((n + 255) / 256, (int64_t)1 << 23)), b(256);
     const int64_t srows = square ? (R + 127) / 128 : R;
     if (y_dt == DT_BF16)
         hipLaunchKernelGGL(k_block8_dequant<DT_BF16>, g, b, 0, s, codes, scales, R, C, ld, srows, square ? 7 : 0, Y);

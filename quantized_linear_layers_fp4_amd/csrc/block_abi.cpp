@@ -13,7 +13,7 @@ using namespace fp4;
 namespace {
 
 constexpr int64_t SIDE_MAX = ((int64_t)1 << 23) - 128;  // a product tile's 256 rows stay below 2^31 bytes
-constexpr int64_t ELEMS_MAX = (int64_t)1 << 34;       // threads of a quantizer's launch below 2^32
+constexpr int64_t ELEMS_MAX = (int64_t)1 << 34;       // threads of a quantizer's launch at most 2^31
 
 size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 bool al16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }

@@ -295,3 +295,18 @@ def test_few_rows_wide(M):
         y = fp4.block8_linear_forward(x.to(DEV), wq, out_dtype=out)
         for cols in (slice(0, 128), slice(8064, 8192), slice(16384, N)):
             check_product(y[:, cols], a, ref.blocks(f64(w[:, cols]), 128, 128).T, out, K)
+
+
+def test_dequantize_largest():
+    """2^34 elements, the most that an operand may have (16 GiB of codes, 32 of bf16): every value is written."""
+    side = 1 << 17
+    op = fp4.Block8(side, side, fp4.FP4_BLOCK_SQUARE, DEV)
+    op.codes.fill_(0x38)   # 1
+    op.scales.fill_(128)   # 2
+    op.codes[-1, -3:] = torch.tensor([0x40, 0xB8, 0], dtype=torch.uint8, device=DEV)
+    y = fp4.block8_dequantize(op, torch.bfloat16)
+    assert y[-1, -4:].tolist() == [2.0, 4.0, -2.0, 0.0]
+    y[-1, -3:] = 2.0
+    assert all(bool((part == 2).all()) for part in y.split(1 << 13))
+    del y, op
+    torch.cuda.empty_cache()
