@@ -469,10 +469,12 @@ def _same_device(ref: torch.Tensor, *ts):
             raise ValueError("tensors must be on one device")
 
 
-def _block8_scratch(ws: torch.Tensor | None, nbytes: int, device) -> torch.Tensor:
+def _scratch(ws: torch.Tensor | None, nbytes: int, ref: torch.Tensor) -> torch.Tensor:
+    """A given workspace, all of it memory of ref's device, or a new one."""
     if ws is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+        return torch.empty(nbytes, dtype=torch.uint8, device=ref.device)
     _need_cuda(ws)
+    _same_device(ref, ws)
     return ws
 
 
@@ -524,7 +526,7 @@ def block8_linear_forward(x: torch.Tensor, w: Block8, out_dtype: torch.dtype | N
         return Y
     L = lib()
     xt = Block8(K, M, FP4_BLOCK_VECTOR, x.device) if for_backward else None
-    ws = _block8_scratch(ws, L.fp4_block8_linear_workspace_bytes(M, K, w.rows), x.device)
+    ws = _scratch(ws, L.fp4_block8_linear_workspace_bytes(M, K, w.rows), x)
     _check(L.fp4_block8_linear(_ptr(x), _dt(x), M, K, _ld(x), _ptr(w.codes), _ptr(w.scales), w.mode, w.rows, _ptr(Y),
                                _dt(Y), _ptr(xt.codes) if xt else None, _ptr(xt.scales) if xt else None, _ptr(ws),
                                ws.numel(), _stream(x)))
@@ -549,7 +551,7 @@ def block8_linear_backward(dy: torch.Tensor, w: Block8 | None, xt: Block8 | None
     dx = torch.empty(M, K, dtype=out_dtype, device=dy.device) if w is not None else None
     dw = torch.empty(K, N, dtype=out_dtype, device=dy.device) if xt is not None else None
     L = lib()
-    ws = _block8_scratch(ws, L.fp4_block8_backward_workspace_bytes(M, N), dy.device)
+    ws = _scratch(ws, L.fp4_block8_backward_workspace_bytes(M, N), dy)
     od = _out_dtype_code(out_dtype)
     _check(L.fp4_block8_backward(_ptr(dy), _dt(dy), M, K, N, _ld(dy), _ptr(w.codes) if w is not None else None,
                                  _ptr(w.scales) if w is not None else None, w.mode if w is not None else 0,
@@ -654,7 +656,9 @@ def kv4_attention(q: torch.Tensor, cache: KV4Cache, pages: torch.Tensor, lens: t
         raise ValueError(f"{nq} queries for {b} sequences without q_start")
     if max_q is None:
         max_q = 1 if q_start is None else nq
-    _same_device(q, cache.data, pages, lens, q_start, ws)
+    _same_device(q, cache.data, pages, lens, q_start)
+    if ws is not None:
+        ws = _scratch(ws, 0, q)
     o = torch.empty_like(q, memory_format=torch.contiguous_format)
     lse = torch.empty(nq, hq, dtype=torch.float32, device=q.device) if return_lse else None
     if nq and not b:  # no sequence owns a query
