@@ -649,8 +649,8 @@ def kv4_attention(q: torch.Tensor, cache: KV4Cache, pages: torch.Tensor, lens: t
     if q_start is not None and (q_start.dtype != torch.int32 or not q_start.is_cuda or q_start.shape != (b + 1,) or
                                 not q_start.is_contiguous()):
         raise ValueError(f"expected {b + 1} int32 offsets on a HIP device")
-    if pages.dtype != torch.int32 or not pages.is_cuda or pages.dim() != 2 or pages.stride(1) != 1 or \
-            (b > 1 and pages.stride(0) < pages.shape[1]):
+    if pages.dtype != torch.int32 or not pages.is_cuda or pages.dim() != 2 or \
+            (pages.shape[1] > 1 and pages.stride(1) != 1) or (b > 1 and pages.stride(0) < pages.shape[1]):
         raise ValueError("expected an int32 page table (b, width) on a HIP device, rows contiguous")
     if q_start is None and nq != b:
         raise ValueError(f"{nq} queries for {b} sequences without q_start")

@@ -269,3 +269,22 @@ def test_scales_under_which_every_code_is_finite(n, dt):
         want = (ref.nearest(y * np.exp2(-e.astype(float)), ref.E2M1) * np.exp2(e.astype(float))).reshape(n, h, d)
         want[5, 1] = np.nan
         assert np.array_equal(f64(got), want, equal_nan=True)
+
+
+def test_page_tables_of_one_column_and_of_one_row():
+    """A single column needs no stride along it, and a single row none between rows."""
+    c = Case([100, 3, 64], [1, 1, 1], 8, 2, 64, 128)
+    want, wl = c.run()
+    turned = torch.full((4, 3), -1, dtype=torch.int32, device=DEV)
+    turned[0] = c.table[:, 0]
+    for table in (turned.t()[:, :1], turned[:1].t(), torch.stack([c.table.to(DEV)[:, 0]] * 5, 1)[:, 2:3]):
+        assert table.shape == (3, 1)
+        o, lse = c.run(pages=table)
+        assert torch.equal(o, want) and torch.equal(lse, wl)
+    c = Case([100], [1], 8, 2, 64, 16)
+    want, wl = c.run()
+    o, lse = c.run(pages=c.table[0].to(DEV).as_strided((1, c.width), (0, 1)))
+    assert torch.equal(o, want) and torch.equal(lse, wl)
+    for table in (c.table.to(DEV).expand(2, -1), torch.zeros(2, 4, dtype=torch.int32, device=DEV)[:, ::2]):
+        with pytest.raises(ValueError):
+            c.run(pages=table, lens=torch.ones(2, dtype=torch.int32, device=DEV), q_start=torch.arange(3, dtype=torch.int32, device=DEV))
