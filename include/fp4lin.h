@@ -365,7 +365,10 @@ fp4_status fp4_block8_dequantize(const uint8_t *codes, const uint8_t *scales, in
                                  void *Y, int32_t y_dtype, void *stream);
 
 /* The product of two operands: Y (M x N, y_dtype) = A . B^T with A of M rows, B of N rows, both of
- * contraction length K; summed in fp32, rounded once. */
+ * contraction length K; summed in fp32, rounded once.  For a bf16 Y, of every eight neighbouring products those below
+ * 2^-13 of the largest may be left out; for an fp32 Y none is, and the operands count as the values that
+ * fp4_block8_dequantize gives in bf16: below 2^-126 multiples of 2^-133, and 256 * 2^120, which inputs from
+ * 248 * 2^120 (3.296e38) on become, is infinite. */
 fp4_status fp4_block8_gemm(const uint8_t *a_codes, const uint8_t *a_scales, int32_t a_mode, const uint8_t *b_codes,
                            const uint8_t *b_scales, int32_t b_mode, int64_t M, int64_t N, int64_t K, void *Y,
                            int32_t y_dtype, void *stream);

@@ -130,8 +130,9 @@ __device__ __forceinline__ uint32_t amax8(const float v[8]) {
 // Operands of a product with fp32 output, on the bf16 instruction at half the rate.  The scaled E4M3
 // instruction aligns its products in groups of eight to the largest and drops what lies 14 or more
 // binary places below (measured: 1.4e-5 of the result on normal data, 5e-5 with outlier channels),
-// which a bf16 output (2^-9) does not see and an fp32 one does.  E4M3 values times their power of two
-// are exact in bf16, and the conversion applies the scale.
+// which a bf16 output (2^-8) does not see and an fp32 one does.  E4M3 values times their power of two
+// are exact in bf16 but at the ends of the range (below 2^-126, and 256 * 2^120), and the conversion
+// applies the scale.
 template <int KK>
 __device__ __forceinline__ void to_bf16(const v8i &x, uint32_t s, v8bf (&f)[4]) {
     const float sc = __uint_as_float(((s >> (8 * KK)) & 255u) << 23);

@@ -16,7 +16,7 @@
 // Values.  O^T += V^T . P^T in bf16: a lane's eight P values are where the instruction wants them
 // (the token order of a tile is chosen for that), and V is unpacked in registers from 32 contiguous
 // bytes (8 tokens x 8 columns) with the scale in the converting instruction.  Unpacked V is exact in
-// bf16; P is rounded to bf16 (2^-9 of each term, as the output itself is), the sum of P is taken
+// bf16; P is rounded to bf16 (2^-8 of each term, as the output itself is), the sum of P is taken
 // before that rounding.
 #include <algorithm>
 #include <type_traits>

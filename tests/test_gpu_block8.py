@@ -310,3 +310,27 @@ def test_dequantize_largest():
     assert all(bool((part == 2).all()) for part in y.split(1 << 13))
     del y, op
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("M", [4, 40, 130])
+def test_products_at_the_ends_of_the_range(M):
+    """An fp32 output takes the operands as bf16 holds them: values next to the smallest are rounded to its multiples of
+    2^-133, and 256 * 2^120 is infinite; 240 * 2^120 is a number.  A bf16 output takes the values themselves."""
+    x, w = torch.zeros(M, 128), torch.zeros(128, 70)
+    x[0, :3], x[1, 0], x[2, 0], x[3, :2] = torch.tensor([2.0 ** -131, 2.0 ** -135, 5e-39]), 3.2e38, 3.39e38, torch.tensor([1.0, -3.0])
+    w[0, 0], w[:3, 1], w[5, 2] = 2.0 ** -100, 2.0 ** 100, 1.0
+    xq, wq = fp4.block8_quantize(x.to(DEV))[0], fp4.block8_quantize(w.to(DEV), rows=False, cols=True)[1]
+    y, yb = fp4.block8_gemm(xq, wq, torch.float32), fp4.block8_gemm(xq, wq, torch.bfloat16)
+    a, b = (f64(fp4.block8_dequantize(t, torch.bfloat16)) for t in (xq, wq))
+    with np.errstate(invalid="ignore", over="ignore"):
+        want = (a @ b.T).astype(np.float32)
+        assert np.isinf(a[2, 0]) and np.isnan(want[2, 2]) and np.isfinite(want[:2]).any()
+        got = f64(y)
+        assert np.array_equal(np.isnan(got), np.isnan(want)) and np.array_equal(np.isinf(got), np.isinf(want))
+        ok = np.isfinite(want)
+        assert (np.abs(got[ok] - want[ok]) <= 2.0 ** -20 * np.abs(want[ok])).all()
+    av, bv = ref.blocks(f64(x), 1, 128), ref.blocks(f64(w), 128, 1).T
+    cols = [0, *range(2, 70)]  # in column 1 the third value and the second leave the type's range
+    check_product(yb[:, cols], av, bv[cols], torch.bfloat16, 128)
+    check_product(yb[[0, 3], 1:2], av[[0, 3]], bv[1:2], torch.bfloat16, 128)
+    assert torch.isinf(yb[1:3, 1]).all()
