@@ -288,3 +288,31 @@ def test_page_tables_of_one_column_and_of_one_row():
     for table in (c.table.to(DEV).expand(2, -1), torch.zeros(2, 4, dtype=torch.int32, device=DEV)[:, ::2]):
         with pytest.raises(ValueError):
             c.run(pages=table, lens=torch.ones(2, dtype=torch.int32, device=DEV), q_start=torch.arange(3, dtype=torch.int32, device=DEV))
+
+
+@pytest.mark.parametrize("t,hq", [(1, 8), (6, 8), (40, 8), (70, 32)])
+def test_captured_batches_of_changing_sizes(t, hq):
+    """One captured call for a batch that fills and empties: offsets, lengths and tables change between the replays, and
+    every replay writes every row, those of no sequence too."""
+    c = Case([900, 333, 64, 500], [t] * 4, hq, 4, 64, 32)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=DEV)  # noqa: E731
+    q, table, lens, starts = c.q.to(DEV), c.table.to(DEV), i32(c.lens), i32(c.starts)
+    ws = fp4.kv4_attention_workspace(q, c.cache, table, t)
+    call = lambda: fp4.kv4_attention(q, c.cache, table, lens, q_start=starts, max_q=t, window=400, return_lse=True, ws=ws)  # noqa: E731
+    call()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        og, lg = call()
+    for qlens, ln in (([t] * 4, [900, 333, 64, 500]), ([t, 0, 0, 0], [900, 0, 0, 0]), ([1, t, 1, 0], [77, 333, 1, 0]),
+                      ([0] * 4, [0] * 4), ([t] * 4, [500, 333, 10, 499])):
+        starts.copy_(i32([0, *np.cumsum(qlens).tolist()]))
+        lens.copy_(i32(ln))
+        og.fill_(7.0)
+        lg.fill_(7.0)
+        g.replay()
+        torch.cuda.synchronize()
+        want, wl = call()
+        n = sum(qlens)
+        assert torch.equal(og, want) and torch.equal(lg, wl)
+        assert (og[n:] == 0).all() and torch.isneginf(lg[n:]).all() and not (lg[:n] == 7).any()
