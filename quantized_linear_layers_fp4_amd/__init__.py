@@ -633,7 +633,8 @@ def kv4_attention(q: torch.Tensor, cache: KV4Cache, pages: torch.Tensor, lens: t
     """Causal attention of packed bf16 queries q (nq x hq x d) over the cache.  pages: int32 page table
     (b x width); lens: int32 tokens of each sequence in the cache, its queries' own among them; q_start: int32
     b + 1 offsets of the sequences' queries, or None for one query a sequence; max_q: the most queries of a
-    sequence (None: as many as q has, or 1 without q_start; a close bound is faster, and needs less workspace);
+    sequence (None: as many as q has, or 1 without q_start; a close bound is faster, needs less workspace, and is
+    needed where b times q's rows pass what a call may have);
     window: tokens a query sees (0: all).  A query that sees nothing gets 0 and lse -inf, and so does one past its
     sequence's first max_q, before q_start[0] or from q_start[b] on."""
     if q.dtype != torch.bfloat16:
@@ -656,9 +657,9 @@ def kv4_attention(q: torch.Tensor, cache: KV4Cache, pages: torch.Tensor, lens: t
         raise ValueError(f"{nq} queries for {b} sequences without q_start")
     if max_q is None:
         max_q = 1 if q_start is None else nq
-    _same_device(q, cache.data, pages, lens, q_start)
-    if ws is not None:
-        ws = _scratch(ws, 0, q)
+    _same_device(q, cache.data, pages, lens, q_start, ws)
+    if ws is not None and not ws.is_contiguous():
+        raise ValueError("expected a contiguous workspace")
     o = torch.empty_like(q, memory_format=torch.contiguous_format)
     lse = torch.empty(nq, hq, dtype=torch.float32, device=q.device) if return_lse else None
     if nq and not b:  # no sequence owns a query
