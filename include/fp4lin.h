@@ -434,7 +434,8 @@ fp4_status fp4_kv4_read(const uint8_t *cache, int64_t pages, int32_t page, int32
  *   scale    of the scores (1 / sqrt(d) usually)
  *   o        nq x hq x d bf16 dense; lse  NULL or fp32 nq x hq: natural log of the sum of exp(score)
  * A query that sees no token gets zeros and lse = -infinity, and so does one of no sequence (before q_start[0] or
- * from q_start[b] on) and one past its sequence's first max_q.  Softmax statistics and sums are fp32.
+ * from q_start[b] on) and one past its sequence's first max_q.  Softmax statistics and sums are fp32; the
+ * probabilities are rounded to bf16 (2^-8 of a term) for the product with the values, after their sum is taken.
  * Two calls on overlapping workspaces must be ordered.  Limits: max_q * (hq / hkv) < 2^24.
  * Return FP4_OK or FP4_ERR_{NULL,SHAPE,DTYPE,WORKSPACE,ALIGN,DEVICE,HIP}. */
 size_t fp4_kv4_attention_workspace_bytes(int32_t b, int32_t max_q, int32_t hq, int32_t hkv, int32_t d, int32_t page,

@@ -6,7 +6,8 @@
 // quarter of a wave touches 16 lines and takes as many cycles: 27 instead of 17 us for 48 x 11008 x 4096.
 // A workgroup owns 16 weight rows (columns of Y) and all rows of A; its waves take the blocks along K in
 // turn, each with the loads of several blocks in flight all the time, and join in LDS in wave order, so the
-// call fills the device whatever N is, with no partial results in memory.
+// call fills the device whatever N is, with no partial results in memory.  A's codes are read by every workgroup: for
+// 48 x 11008 x 4096 that is 135 of the 183 MB that the call reads through the L2s.
 //
 // For a few rows A comes as it is, and every workgroup quantizes it into LDS while its first weights are on
 // their way: a launch less.

@@ -411,9 +411,9 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? 3 : 1) void k_kv4_decode(DecArgs
 // Eight waves a CU in either size.  2 x 1024 queries of 32 heads over 8192 tokens (d 128, 8 key/value heads), us:
 // 16 rows a wave 700; this with four waves 362, page indices looked up a tile earlier 341, the maximum
 // in one instruction for two scores 322; with eight waves, which halves a thread's unpacking, and bytes two
-// tiles ahead 305.  0.85 PFLOP/s then; of a SIMD's cycles about 34 % are matrix and 45 % vector instructions
-// (the exponentials first), which overlap little: a deeper interleaving within a wave (64 rows, 512
-// registers) was slower.
+// tiles ahead 305 (short runs; 276 once the clock is up, 0.93 PFLOP/s).  Of a busy CU's cycles matrix instructions
+// take 44 %, vector instructions (the exponentials first) 61 % and LDS 34 %: a deeper interleaving within a wave
+// (64 rows, 512 registers) was slower.
 template <int D, int NT>
 __global__ __launch_bounds__(NT, 2) void k_kv4_chunk(DecArgs p) {
     constexpr int CR = NT / 2;        // rows of the workgroup
