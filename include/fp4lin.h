@@ -446,6 +446,97 @@ fp4_status fp4_kv4_attention(const void *q, int64_t q_token_stride, int64_t q_he
                              int64_t pages, int32_t page, int32_t hkv, int32_t d, int32_t window, float scale, void *o,
                              float *lse, void *workspace, size_t ws_bytes, void *stream);
 
+/* ---------------------------------------------------------------------------------------------
+ * Page tables of a 4-bit cache, kept on the GPU.  b sequences have a row of `width` page indices each (rows table_stride
+ * apart) and a length in tokens, lens; free_pages (int32[pages]) holds the free pages in its first *free_count
+ * entries, the last of which is taken first.  All of it is device memory, updated in place in stream order, so a captured
+ * graph moves on with every replay.  The caller fills the stack once, and rows that hold nothing may hold anything.
+ * Limits: b <= 2^20, width * page <= 2^30, b * width < 2^31, n < 2^31 - 1. */
+
+/* Append: sequence i asks for new_tokens[i] tokens (NULL: 1 each; below 0 counts as 0).  The pages that they need beyond
+ * the sequence's own go from the stack into its row, in the order of sequences and pages, and lens grows.  A sequence
+ * whose row is too narrow gets no token, and neither does one that the stack or the n tokens of the call no longer
+ * suffice for (counted in the order of sequences; those that ask for no further page, or no token, are not concerned).
+ *   q_start   int32[b + 1] (out): sequence i's tokens are q_start[i] .. q_start[i+1] - 1 of the call's n, so
+ *             their number says what it got; or NULL: n = b, token i is sequence i's (more than one counts as one)
+ *   slots     int64[n] (out): each token's slot, as fp4_kv4_write takes it; -1 for tokens behind the last (or that were
+ *             refused), and where the row's entry is no page of the cache
+ *   positions int32[n] (out): each token's place in its sequence; -1 as above but for the last
+ *   workspace: at least fp4_kv4_extend_workspace_bytes(b, n) bytes (may be 0, and NULL then; 0 without q_start).
+ * Returns FP4_OK or FP4_ERR_{NULL,SHAPE,WORKSPACE,ALIGN,DEVICE,HIP}. */
+size_t fp4_kv4_extend_workspace_bytes(int32_t b, int64_t n);
+fp4_status fp4_kv4_extend(int32_t *table, int64_t table_stride, int32_t b, int32_t width, int32_t *lens, int32_t *free_pages,
+                          int32_t *free_count, int64_t pages, int32_t page, const int32_t *new_tokens, int64_t n, int64_t *slots,
+                          int32_t *positions, int32_t *q_start, void *workspace, size_t ws_bytes, void *stream);
+
+/* Give back: lens[i] becomes keep[i] where that is less (NULL: stays; below 0 counts as 0), and the pages past it go to the
+ * stack, as do those that no query from there on sees through a window of `window` tokens (0: none) beside the
+ * first `sinks` ones.  The first `shared` columns are left as they are (pages that several rows hold).  Entries given back
+ * become -1; entries that are no page of the cache are not given back.  The first page given back, in the order of sequences
+ * and pages, is the next that fp4_kv4_extend takes.  A sequence is not cut to a length inside what its window has
+ * left behind (its tokens there have no page any more).
+ *   workspace: at least fp4_kv4_release_workspace_bytes(b, width) bytes (may be 0, and NULL then).
+ * Returns FP4_OK or FP4_ERR_{NULL,SHAPE,WORKSPACE,ALIGN,DEVICE,HIP}. */
+size_t fp4_kv4_release_workspace_bytes(int32_t b, int32_t width);
+fp4_status fp4_kv4_release(int32_t *table, int64_t table_stride, int32_t b, int32_t width, int32_t *lens, int32_t *free_pages,
+                           int32_t *free_count, int64_t pages, int32_t page, const int32_t *keep, int32_t window,
+                           int32_t sinks, int32_t shared, void *workspace, size_t ws_bytes, void *stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * Norm of queries and keys for each head, with the rotation of their positions in the same pass:
+ *      y = x / sqrt(mean(x^2) + eps) * w  over the d values of a row (eps = -1: y = x, and no weights), then
+ *      (a, b) -> (a cos - b sin, b cos + a sin) for the pairs (i, i + rot / 2) of the first rot columns, or
+ *      (2 i, 2 i + 1) if interleaved (rot = 0: none, and table and positions may be NULL)
+ * computed in 64 bits and rounded to fp32, then to the type.  A row with a NaN or an infinity is NaN under the norm.
+ *   q, k      n x hq x d and n x hkv x d of dtype (fp32 or bf16), d contiguous, strides in elements, any element alignment;
+ *             hkv = 0: no k.  d a multiple of 8 from 32 to 256, rot a multiple of 16 up to d
+ *   q_weight, k_weight  d values of w_dtype, or NULL: ones
+ *   positions int32[n]; table fp32 max_pos x rot, a row the rot / 2 cosines and the rot / 2 sines of a position, 16-byte
+ *             aligned.  A negative position's rows are zeros (padding); one from max_pos on makes the rotated
+ *             columns NaN.
+ *   q_out, k_out  dense, of dtype, not overlapping the inputs
+ * Limits: n <= 2^24, n * (hq + hkv) <= 2^29.
+ * Returns FP4_OK or FP4_ERR_{NULL,SHAPE (also: eps),DTYPE,ALIGN,DEVICE,HIP}. */
+fp4_status fp4_qk_norm_rope(const void *q, int64_t q_token_stride, int64_t q_head_stride, int32_t hq, const void *k,
+                            int64_t k_token_stride, int64_t k_head_stride, int32_t hkv, int64_t n, int32_t d, int32_t dtype,
+                            const void *q_weight, const void *k_weight, int32_t w_dtype, float eps, const int32_t *positions,
+                            const float *table, int64_t max_pos, int32_t rot, int32_t interleaved, void *q_out, void *k_out,
+                            void *stream);
+
+/* The table: cos and sin of pos / factor * base^(-2 i / rot), in 64 bits, rounded once.  Limit: max_pos * rot <= 2^32.
+ * Returns FP4_OK or FP4_ERR_{NULL,SHAPE,ALIGN,DEVICE,HIP}. */
+fp4_status fp4_rope_table(float *table, int64_t max_pos, int32_t rot, double base, double factor, void *stream);
+
+/* The serving form: q_out as above, and keys (as k_out would hold them) and values to the cache's slots, bit for bit as
+ * fp4_qk_norm_rope and then fp4_kv4_write would put them there, in one launch.  d 64 or 128; v as k; slots as for
+ * fp4_kv4_write.  q_out must not overlap the inputs. */
+fp4_status fp4_kv4_norm_rope(uint8_t *cache, int64_t pages, int32_t page, const void *q, int64_t q_token_stride,
+                             int64_t q_head_stride, int32_t hq, const void *k, int64_t k_token_stride, int64_t k_head_stride,
+                             const void *v, int64_t v_token_stride, int64_t v_head_stride, int32_t hkv, int64_t n, int32_t d,
+                             int32_t dtype, const void *slots, int32_t slot_bytes, const void *q_weight, const void *k_weight,
+                             int32_t w_dtype, float eps, const int32_t *positions, const float *table, int64_t max_pos,
+                             int32_t rot, int32_t interleaved, void *q_out, void *stream);
+
+/* Gradients of fp4_qk_norm_rope from dq, dk (of its outputs) and its inputs: with g the rotation by the opposite angle of dy,
+ * r = 1 / sqrt(mean(x^2) + eps) and h = g w,
+ *      x's = r (h - x r mean(h x r)),   w's = sum over tokens and heads of g x r
+ *   q_grad, k_grad  of dtype, with strides of their own (a view into the fused projection's gradient, for one); not
+ *            overlapping the inputs
+ *   q_weight_grad, k_weight_grad  fp32[d], summed in fp32 in an order that does not change, or NULL (not wanted)
+ *   workspace: at least fp4_qk_norm_rope_backward_workspace_bytes(d) bytes if a weight's gradient is wanted.
+ * Rows of a negative position add nothing and get zeros.
+ * Returns FP4_OK or FP4_ERR_{NULL,SHAPE,DTYPE,WORKSPACE,ALIGN,DEVICE,HIP}. */
+size_t fp4_qk_norm_rope_backward_workspace_bytes(int32_t d);
+fp4_status fp4_qk_norm_rope_backward(const void *dq, int64_t dq_token_stride, int64_t dq_head_stride, const void *dk,
+                                     int64_t dk_token_stride, int64_t dk_head_stride, const void *q, int64_t q_token_stride,
+                                     int64_t q_head_stride, int32_t hq, const void *k, int64_t k_token_stride,
+                                     int64_t k_head_stride, int32_t hkv, int64_t n, int32_t d, int32_t dtype,
+                                     const void *q_weight, const void *k_weight, int32_t w_dtype, float eps,
+                                     const int32_t *positions, const float *table, int64_t max_pos, int32_t rot,
+                                     int32_t interleaved, void *q_grad, int64_t qg_token_stride, int64_t qg_head_stride,
+                                     void *k_grad, int64_t kg_token_stride, int64_t kg_head_stride, float *q_weight_grad,
+                                     float *k_weight_grad, void *workspace, size_t ws_bytes, void *stream);
+
 /* Host-only: the kernel selection, the same rule the launches use, so a caller (a profiler
  * summary, a benchmark) can name what runs.  fp4_gemm_kernel_name: the FP4 GEMM kernel that
  * fp4_gemm and fp4_linear_forward launch for an M x N x K product on a device with num_cus

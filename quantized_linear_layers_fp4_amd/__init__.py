@@ -38,6 +38,9 @@ EXPORTS = (
     "fp4_block8_gemm", "fp4_block8_linear_workspace_bytes", "fp4_block8_linear",
     "fp4_block8_backward_workspace_bytes", "fp4_block8_backward",
     "fp4_kv4_cache_bytes", "fp4_kv4_write", "fp4_kv4_read", "fp4_kv4_attention_workspace_bytes", "fp4_kv4_attention",
+    "fp4_kv4_extend_workspace_bytes", "fp4_kv4_extend", "fp4_kv4_release_workspace_bytes", "fp4_kv4_release",
+    "fp4_rope_table", "fp4_qk_norm_rope", "fp4_kv4_norm_rope", "fp4_qk_norm_rope_backward_workspace_bytes",
+    "fp4_qk_norm_rope_backward",
     "fp4_gemm_kernel_name", "fp4_comp_kernel_name", "fp4_status_string",
 )
 
@@ -104,6 +107,19 @@ def lib():
         "fp4_kv4_attention_workspace_bytes": (sz, [i32, i32, i32, i32, i32, i32, i32]),
         "fp4_kv4_attention": (i32, [vp, i64, i64, i64, i32, vp, vp, i32, i32, vp, i64, i32, vp, i64, i32, i32, i32,
                                     i32, C.c_float, vp, vp, vp, sz, vp]),
+        "fp4_kv4_extend_workspace_bytes": (sz, [i32, i64]),
+        "fp4_kv4_extend": (i32, [vp, i64, i32, i32, vp, vp, vp, i64, i32, vp, i64, vp, vp, vp, vp, sz, vp]),
+        "fp4_kv4_release_workspace_bytes": (sz, [i32, i32]),
+        "fp4_kv4_release": (i32, [vp, i64, i32, i32, vp, vp, vp, i64, i32, vp, i32, i32, i32, vp, sz, vp]),
+        "fp4_rope_table": (i32, [vp, i64, i32, dbl, dbl, vp]),
+        "fp4_qk_norm_rope": (i32, [vp, i64, i64, i32, vp, i64, i64, i32, i64, i32, i32, vp, vp, i32, C.c_float, vp, vp, i64,
+                                   i32, i32, vp, vp, vp]),
+        "fp4_kv4_norm_rope": (i32, [vp, i64, i32, vp, i64, i64, i32, vp, i64, i64, vp, i64, i64, i32, i64, i32, i32, vp, i32,
+                                    vp, vp, i32, C.c_float, vp, vp, i64, i32, i32, vp, vp]),
+        "fp4_qk_norm_rope_backward_workspace_bytes": (sz, [i32]),
+        "fp4_qk_norm_rope_backward": (i32, [vp, i64, i64, vp, i64, i64, vp, i64, i64, i32, vp, i64, i64, i32, i64, i32, i32,
+                                            vp, vp, i32, C.c_float, vp, vp, i64, i32, i32, vp, i64, i64, vp, i64, i64, vp,
+                                            vp, vp, sz, vp]),
         "fp4_gemm_kernel_name": (C.c_char_p, [i64, i64, i64, i32]),
         "fp4_comp_kernel_name": (C.c_char_p, [i64, i64]),
         "fp4_status_string": (C.c_char_p, [i32]),
@@ -675,3 +691,228 @@ def kv4_attention(q: torch.Tensor, cache: KV4Cache, pages: torch.Tensor, lens: t
                                        d ** -0.5 if scale is None else float(scale), _ptr(o), _ptr(lse), _ptr(ws),
                                        ws.numel(), _stream(q)))
     return (o, lse) if return_lse else o
+
+
+# --------------------------------------------------------------------------- page tables of the cache
+def _on_device(ref: torch.Tensor, call):
+    """call(), which enqueues on ref's device, with that device current."""
+    if ref.get_device() == torch._C._cuda_getDevice():
+        return call()
+    with torch.cuda.device(ref.device):
+        return call()
+
+
+def _int32s(name: str, t: torch.Tensor, shape, ref: torch.Tensor | None = None):
+    if t.dtype != torch.int32 or not t.is_cuda or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"expected {name} as {shape} contiguous int32 on a HIP device")
+    if ref is not None:
+        _same_device(ref, t)
+
+
+class KV4Pages:
+    """The page tables of b sequences of a cache and its free pages, all int32 on the device: table (b x width, -1
+    where there is no page), lens (b, tokens of each), free (pages) and count (1): the first count entries of free
+    are the free pages, the last of them the next to be taken."""
+    __slots__ = ("table", "lens", "free", "count", "pages", "page")
+
+    def __init__(self, table, lens, free, count, pages, page):
+        self.table, self.lens, self.free, self.count, self.pages, self.page = table, lens, free, count, pages, page
+
+    def _check(self):
+        b, width = self.table.shape
+        _int32s("the table", self.table, (b, width))
+        _int32s("the lengths", self.lens, (b,), self.table)
+        _int32s("the free pages", self.free, (self.pages,), self.table)
+        _int32s("their count", self.count, (1,), self.table)
+        return b, width
+
+
+def kv4_page_tables(b: int, width: int, pages: int, page: int, device="cuda") -> KV4Pages:
+    """Empty tables of b sequences, up to width pages each, over a cache of `pages` pages of `page` tokens, all free
+    (page 0 is taken first)."""
+    if b < 1 or width < 1 or not 1 <= pages <= 0x7FFFFFFF or page < 16 or page > 1024 or page & (page - 1):
+        raise Fp4Error(f"no page tables of {b} sequences of {width} pages over {pages} pages of {page} tokens")
+    i32 = dict(dtype=torch.int32, device=device)
+    return KV4Pages(torch.full((b, width), -1, **i32), torch.zeros(b, **i32), torch.arange(pages - 1, -1, -1, **i32),
+                    torch.full((1,), pages, **i32), pages, page)
+
+
+def kv4_extend(tables: KV4Pages, new: torch.Tensor | None = None, n: int | None = None):
+    """Append new[i] tokens (int32, b; None: one each) to sequence i: takes pages, writes the table, adds to the lengths.
+    With n, the call's tokens lie one sequence after the other: (slots, positions, q_start), slots int64 and positions
+    int32 for n tokens (-1 behind the last), q_start int32 b + 1; q_start[i+1] - q_start[i] is what sequence i got:
+    new[i], or 0 where its row, the free pages or n did not suffice.  Without n, token i is sequence i's only one:
+    (slots, positions), -1 where it got none (new[i] = 0: none; above 1 counts as 1)."""
+    b, width = tables._check()
+    if new is None and n is not None:
+        raise ValueError("n tokens need new")
+    if new is not None:
+        _int32s("the new tokens", new, (b,), tables.table)
+    if n is not None and n < 0:
+        raise ValueError(f"{n} tokens")
+    dev, L = tables.table.device, lib()
+    m = b if n is None else n
+    slots = torch.empty(m, dtype=torch.int64, device=dev)
+    pos = torch.empty(m, dtype=torch.int32, device=dev)
+    q_start = None if n is None else torch.empty(b + 1, dtype=torch.int32, device=dev)
+    need = 0 if n is None else L.fp4_kv4_extend_workspace_bytes(b, n)
+    ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    _on_device(tables.table, lambda: _check(L.fp4_kv4_extend(
+        _ptr(tables.table), width, b, width, _ptr(tables.lens), _ptr(tables.free), _ptr(tables.count), tables.pages, tables.page,
+        _ptr(new), m, _ptr(slots), _ptr(pos), _ptr(q_start), _ptr(ws), need, _stream(tables.table))))
+    return (slots, pos) if n is None else (slots, pos, q_start)
+
+
+def kv4_release(tables: KV4Pages, keep: torch.Tensor | None = None, window: int = 0, sinks: int = 0, shared: int = 0) -> None:
+    """Cut sequence i to its first keep[i] tokens (int32, b; None: all stay; 0 ends it) and give back the pages past them,
+    and with a window those that no later query sees through it beside the first `sinks` tokens.  The first
+    `shared` columns stay.  What is given back first is taken first by the next kv4_extend."""
+    b, width = tables._check()
+    if keep is not None:
+        _int32s("the lengths to keep", keep, (b,), tables.table)
+    L = lib()
+    need = L.fp4_kv4_release_workspace_bytes(b, width)
+    ws = torch.empty(need, dtype=torch.uint8, device=tables.table.device) if need else None
+    _on_device(tables.table, lambda: _check(L.fp4_kv4_release(
+        _ptr(tables.table), width, b, width, _ptr(tables.lens), _ptr(tables.free), _ptr(tables.count), tables.pages, tables.page,
+        _ptr(keep), min(window, 0x7FFFFFFF), min(sinks, 0x7FFFFFFF), min(shared, 0x7FFFFFFF), _ptr(ws), need,
+        _stream(tables.table))))
+
+
+# --------------------------------------------------------------------------- norm of queries and keys, rotation
+def rope_table(max_pos: int, rot: int, base: float = 10000.0, factor: float = 1.0, device="cuda") -> torch.Tensor:
+    """fp32 (max_pos, rot): the rot / 2 cosines, then the rot / 2 sines, of pos / factor * base^(-2 i / rot)."""
+    t = torch.empty(max_pos, rot, dtype=torch.float32, device=device)
+    if not t.is_cuda:
+        raise ValueError("expected a HIP device")
+    _on_device(t, lambda: _check(lib().fp4_rope_table(_ptr(t), max_pos, rot, float(base), float(factor), _stream(t))))
+    return t
+
+
+def _heads_like(name: str, t: torch.Tensor, n: int, d: int, ref: torch.Tensor):
+    if not t.is_cuda or t.dim() != 3 or t.shape[0] != n or t.shape[2] != d or (d > 1 and t.stride(2) != 1):
+        raise ValueError(f"expected {name} as ({n}, heads, {d}) on a HIP device, the last dimension contiguous")
+    if t.dtype != ref.dtype:
+        raise TypeError(f"{name} is {t.dtype}, expected {ref.dtype}")
+    _same_device(ref, t)
+
+
+def _rope_args(q, k, table, positions, q_weight, k_weight, eps):
+    """Checks what the calls over rows of heads share; (n, d, C arguments from the weights to rot)."""
+    if q.dim() != 3:
+        raise ValueError("expected queries (n, heads, d)")
+    n, _, d = q.shape
+    _heads_like("q", q, n, d, q)
+    if k is not None:
+        _heads_like("k", k, n, d, q)
+    elif k_weight is not None:
+        raise ValueError("weights without keys")
+    w = [t for t in (q_weight, k_weight) if t is not None]
+    for t in w:
+        if not t.is_cuda or t.shape != (d,) or not t.is_contiguous():
+            raise ValueError(f"expected {d} contiguous weights on a HIP device")
+        if t.dtype != w[0].dtype:
+            raise TypeError("the weights must share a dtype")
+        _same_device(q, t)
+    if w and eps is None:
+        raise ValueError("weights without a norm")
+    if eps is not None and not eps >= 0:
+        raise ValueError(f"eps {eps}")
+    rot = max_pos = 0
+    if table is not None:
+        if table.dtype != torch.float32 or not table.is_cuda or table.dim() != 2 or not table.is_contiguous():
+            raise ValueError("expected an fp32 table (max_pos, rot) on a HIP device")
+        if positions is None:
+            raise ValueError("a table without positions")
+        _int32s("the positions", positions, (n,), q)
+        _same_device(q, table)
+        max_pos, rot = table.shape
+        if rot < 16:
+            raise ValueError(f"a rotation of {rot} columns")
+    return n, d, (_ptr(q_weight), _ptr(k_weight), _dt(w[0]) if w else FP4_F32, -1.0 if eps is None else float(eps),
+                  _ptr(positions) if rot else None, _ptr(table), max_pos, rot)
+
+
+def _head_args(t: torch.Tensor | None):
+    return (None, 0, 0) if t is None else (t.data_ptr(), t.stride(0), t.stride(1))
+
+
+def qk_norm_rope(q: torch.Tensor, k: torch.Tensor | None, table: torch.Tensor | None = None,
+                 positions: torch.Tensor | None = None, q_weight: torch.Tensor | None = None,
+                 k_weight: torch.Tensor | None = None, eps: float | None = 1e-6, interleaved: bool = False):
+    """Norm of each head of q (n x hq x d, fp32 or bf16) and k (n x hkv x d, or None), times a weight (d, None: ones), and
+    rotation of the first columns by table (rope_table's) at positions (int32, n): dense (q, k).  eps None: no norm; table
+    None: no rotation.  Pairs are (i, i + rot / 2), or (2 i, 2 i + 1) if interleaved.  A negative position's rows
+    are zeros; one past the table makes the rotated columns NaN."""
+    n, d, args = _rope_args(q, k, table, positions, q_weight, k_weight, eps)
+    qo = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    ko = None if k is None else torch.empty(k.shape, dtype=k.dtype, device=k.device)
+    if n and q.shape[1]:
+        _on_device(q, lambda: _check(lib().fp4_qk_norm_rope(
+            *_head_args(q), q.shape[1], *_head_args(k), 0 if k is None else k.shape[1], n, d, _dt(q), *args, int(interleaved),
+            _ptr(qo), _ptr(ko), _stream(q))))
+    elif n:
+        raise ValueError("no query heads")
+    return qo, ko
+
+
+def qk_norm_rope_backward(dq: torch.Tensor, dk: torch.Tensor | None, q: torch.Tensor, k: torch.Tensor | None,
+                          table: torch.Tensor | None = None, positions: torch.Tensor | None = None,
+                          q_weight: torch.Tensor | None = None, k_weight: torch.Tensor | None = None,
+                          eps: float | None = 1e-6, interleaved: bool = False, out=None):
+    """Gradients (of q, of k, of q_weight, of k_weight) of qk_norm_rope from those of its outputs and its inputs; the weights'
+    in fp32 (None where there is no weight).  out: (tensor or None, tensor or None) for the first two, views into the
+    fused projection's gradient for one."""
+    n, d, args = _rope_args(q, k, table, positions, q_weight, k_weight, eps)
+    _heads_like("dq", dq, n, d, q)
+    if (dk is None) != (k is None):
+        raise ValueError("keys and their gradient go together")
+    if k is not None:
+        _heads_like("dk", dk, n, d, q)
+        if dk.shape != k.shape:
+            raise ValueError("dk is not like k")
+    if dq.shape != q.shape:
+        raise ValueError("dq is not like q")
+    gq, gk = out if out is not None else (None, None)
+    if gq is None:
+        gq = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    if gk is None and k is not None:
+        gk = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+    for x, g in ((q, gq), (k, gk)):
+        if g is not None:
+            _heads_like("out", g, n, d, q)
+            if x is None or g.shape != x.shape:
+                raise ValueError("out is not like the inputs")
+    wq, wk = (None if w is None else torch.empty(d, dtype=torch.float32, device=q.device) for w in (q_weight, k_weight))
+    if n == 0:
+        for w in (wq, wk):
+            if w is not None:
+                w.zero_()
+        return gq, gk, wq, wk
+    L = lib()
+    need = L.fp4_qk_norm_rope_backward_workspace_bytes(d) if wq is not None or wk is not None else 0
+    ws = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
+    _on_device(q, lambda: _check(L.fp4_qk_norm_rope_backward(
+        *_head_args(dq), *_head_args(dk), *_head_args(q), q.shape[1], *_head_args(k), 0 if k is None else k.shape[1], n, d,
+        _dt(q), *args, int(interleaved), *_head_args(gq), *_head_args(gk), _ptr(wq), _ptr(wk), _ptr(ws), need, _stream(q))))
+    return gq, gk, wq, wk
+
+
+def kv4_norm_rope(cache: KV4Cache, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor,
+                  table: torch.Tensor | None = None, positions: torch.Tensor | None = None,
+                  q_weight: torch.Tensor | None = None, k_weight: torch.Tensor | None = None, eps: float | None = 1e-6,
+                  interleaved: bool = False) -> torch.Tensor:
+    """qk_norm_rope, of which k goes with v (n x heads x d) to the cache's slots (as kv4_write takes them) in the same
+    launch: returns q."""
+    n, d, args = _rope_args(q, k, table, positions, q_weight, k_weight, eps)
+    _heads_like("v", v, n, d, q)
+    if k.shape != v.shape or k.shape[1:] != (cache.heads, cache.d):
+        raise ValueError(f"expected keys and values (n, {cache.heads}, {cache.d})")
+    sb = _slot_bytes(slots, n)
+    _same_device(q, cache.data, slots)
+    qo = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    if n:
+        _on_device(q, lambda: _check(lib().fp4_kv4_norm_rope(
+            _ptr(cache.data), cache.pages, cache.page, *_head_args(q), q.shape[1], *_head_args(k), *_head_args(v), cache.heads, n, d,
+            _dt(q), _ptr(slots), sb, *args, int(interleaved), _ptr(qo), _stream(q))))
+    return qo

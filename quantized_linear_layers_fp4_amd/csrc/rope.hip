@@ -1,0 +1,555 @@
+// Norm of queries and keys for each head with the rotation of their positions, its gradients, and the same with keys
+// and values written into the 4-bit cache (layout: kv4.h).
+//
+//      r = 1 / sqrt(mean(x^2) + eps),  y = x r w,  then over the first rot columns
+//      (a, b) -> (a cos - b sin, b cos + a sin) for pairs (i, i + rot / 2), or (2 i, 2 i + 1) if interleaved
+//
+// Gradients: g = the rotation by the opposite angle of dy, dw = sum over tokens and heads of g x r, and with h = g w
+// dx = r (h - x r mean(h x r)).
+//
+// Each value is read once and written once (backward: x and dy once, dx once): bound by memory.  A lane holds 8 columns,
+// d / 8 lanes a row (rounded up to a power of two, L); a lane group stays with one token and goes through a
+// run of its heads, so that angles and weights are fetched once a run and not once a row.
+// Forward in 64 bits: with the products w cos and w sin made once a run it takes 7 operations a value, which memory
+// hides, no input overflows in its square, and a key's value does not depend on the order of its sum: the fused write
+// puts into the cache what the norm and kv4_write put there one after the other, bit for bit.
+#include <algorithm>
+
+#include "block8.h"
+#include "serve.h"
+
+namespace fp4 {
+
+namespace {
+
+constexpr int BWD_BLOCKS = 1024;  // workgroups of a backward at most: rows of partial weight gradients
+
+// Sum over the L lanes of a group, in each of them.
+template <int L>
+__device__ __forceinline__ double group_sum(double x) {
+#pragma unroll
+    for (int off = L / 2; off > 0; off >>= 1) x += __shfl_xor(x, off, 64);
+    return x;
+}
+template <int L>
+__device__ __forceinline__ float group_sum(float x) {
+#pragma unroll
+    for (int off = L / 2; off > 0; off >>= 1) x += __shfl_xor(x, off, 64);
+    return x;
+}
+
+// 1 / sqrt(v) from the instruction's 2^-23 by one step of the series (1 - e)^(-1/2) = 1 + e / 2 + 3 e^2 / 8 + ...
+__device__ __forceinline__ double rsqrt64(double v) {
+    const double r = __builtin_amdgcn_rsq(v);
+    const double e = __builtin_fma(-v * r, r, 1.0);
+    return __builtin_fma(r * e, __builtin_fma(0.375, e, 0.5), r);
+}
+
+template <int DT>
+struct Raw {
+    u32x4 w[DT == DT_BF16 ? 1 : 2];
+};
+
+template <int DT>
+__device__ __forceinline__ Raw<DT> load_raw(const void *x, int64_t elem, bool live) {
+    Raw<DT> r;
+#pragma unroll
+    for (auto &q : r.w) q = u32x4{0, 0, 0, 0};
+    if (!live) return r;
+    if constexpr (DT == DT_BF16) {
+        r.w[0] = *reinterpret_cast<const ua_u32x4 *>(static_cast<const uint16_t *>(x) + elem);
+    } else {
+        const float *p = static_cast<const float *>(x) + elem;
+        r.w[0] = *reinterpret_cast<const ua_u32x4 *>(p);
+        r.w[1] = *reinterpret_cast<const ua_u32x4 *>(p + 4);
+    }
+    return r;
+}
+
+template <int DT>
+__device__ __forceinline__ void values(const Raw<DT> &r, float (&v)[8]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (DT == DT_BF16) {
+            v[2 * i] = __uint_as_float(r.w[0][i] << 16);
+            v[2 * i + 1] = __uint_as_float(r.w[0][i] & 0xFFFF0000u);
+        } else {
+            v[i] = __uint_as_float(r.w[0][i]);
+            v[4 + i] = __uint_as_float(r.w[1][i]);
+        }
+    }
+}
+
+// The values that the lane's are paired with: of another lane, or its own neighbours.
+template <int DT, bool IL>
+__device__ __forceinline__ void partners(const Raw<DT> &r, int from, float (&v)[8]) {
+    if constexpr (IL) {
+        float u[8];
+        values<DT>(r, u);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = u[i ^ 1];
+    } else {
+        Raw<DT> p;
+#pragma unroll
+        for (int q = 0; q < (DT == DT_BF16 ? 1 : 2); ++q)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) p.w[q][i] = (uint32_t)__shfl((int)r.w[q][i], from, 64);
+        values<DT>(p, v);
+    }
+}
+
+template <int DT>
+__device__ __forceinline__ void store_row(void *y, int64_t elem, const float (&v)[8]) {
+    typedef unsigned int ua4 __attribute__((ext_vector_type(4), aligned(2)));
+    if constexpr (DT == DT_BF16) {
+        *reinterpret_cast<ua4 *>(static_cast<uint16_t *>(y) + elem) =
+            ua4{bf16_pack2(v[0], v[1]), bf16_pack2(v[2], v[3]), bf16_pack2(v[4], v[5]), bf16_pack2(v[6], v[7])};
+    } else {
+        float *p = static_cast<float *>(y) + elem;
+        *reinterpret_cast<ua4 *>(p) = ua4{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])};
+        *reinterpret_cast<ua4 *>(p + 4) = ua4{__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7])};
+    }
+}
+
+__device__ __forceinline__ float weight_at(const NormRope &a, const void *w, int col) {
+    if (!w) return 1.0f;
+    return a.w_dt == DT_BF16 ? bf16_to_f32(static_cast<const uint16_t *>(w)[col]) : static_cast<const float *>(w)[col];
+}
+
+// A lane's part of a token: its columns, their partners' place, the angles.  State 0: rows of zeros (a negative
+// position); 1: as computed.  A position past the table gives NaN angles.
+template <bool IL>
+struct Turn {
+    int col;         // first of the lane's 8 columns
+    bool live, zero; // its columns are the row's; the token's rows are zeros
+    int from;        // lane of the partners
+    float c[8], s[8];
+
+    __device__ __forceinline__ Turn(const NormRope &a, int64_t t, int lane, int lanes) {
+        col = lane * 8;
+        live = col < a.d;
+        zero = false;
+        const int me = threadIdx.x & 63, half = a.rot / 16;
+        from = IL || lane >= 2 * half ? me : lane < half ? me + half : me - half;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            c[i] = 1.0f;
+            s[i] = 0.0f;
+        }
+        if (!a.rot) return;
+        const int pos = a.positions[t];
+        zero = pos < 0;
+        if (col >= a.rot) return;
+        const bool in = (uint64_t)pos < (uint64_t)a.max_pos;
+        const float *row = a.table + (in ? (int64_t)pos : 0) * a.rot;
+        if constexpr (IL) {
+            const float4 x = *reinterpret_cast<const float4 *>(row + col / 2);
+            const float4 y = *reinterpret_cast<const float4 *>(row + a.rot / 2 + col / 2);
+            const float cs[4] = {x.x, x.y, x.z, x.w}, sn[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                c[i] = cs[i >> 1];
+                s[i] = i & 1 ? sn[i >> 1] : -sn[i >> 1];
+            }
+        } else {
+            const bool second = lane >= half;
+            const float *p = row + (second ? col - a.rot / 2 : col);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                c[i] = p[i];
+                s[i] = second ? p[a.rot / 2 + i] : -p[a.rot / 2 + i];
+            }
+        }
+        if (!in && !zero) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) c[i] = s[i] = __uint_as_float(0x7FC00000u);
+        }
+    }
+
+    __device__ __forceinline__ int partner_col(const NormRope &a, int i) const {
+        if constexpr (IL) return col + (i ^ 1);
+        const int half = a.rot / 2;
+        return col >= a.rot ? col + i : col < half ? col + i + half : col + i - half;
+    }
+};
+
+// A token's weights times its angles: y = r (x u + partner v).
+template <bool IL>
+__device__ __forceinline__ void factors(const NormRope &a, const void *w, const Turn<IL> &t, double (&u)[8], double (&v)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        u[i] = t.live ? (double)weight_at(a, w, t.col + i) * (double)t.c[i] : 0.0;
+        v[i] = t.live ? (double)weight_at(a, w, t.partner_col(a, i)) * (double)t.s[i] : 0.0;
+    }
+}
+
+template <int DT, int L, bool IL>
+__device__ __forceinline__ void turn_row(const NormRope &a, const Raw<DT> &raw, const Turn<IL> &t, const double (&u)[8],
+                                         const double (&v)[8], float (&y)[8]) {
+    float x[8], p[8];
+    values<DT>(raw, x);
+    partners<DT, IL>(raw, t.from, p);
+    double r = 1.0;
+    if (a.norm) {
+        double ss = 0.0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) ss = __builtin_fma((double)x[i], (double)x[i], ss);
+        r = rsqrt64(group_sum<L>(ss) / a.d + (double)a.eps);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float f = (float)(r * __builtin_fma((double)p[i], v[i], (double)x[i] * u[i]));
+        y[i] = t.zero ? 0.0f : f;
+    }
+}
+
+struct FwdArgs {
+    NormRope a;
+    void *qo, *ko;
+    int hp;               // heads a lane group goes through
+    int qc, kc;           // runs of query heads and of key heads
+};
+
+}  // namespace
+
+template <int DT, int L, bool IL>
+__global__ __launch_bounds__(256) void k_norm_rope(FwdArgs f) {
+    const NormRope &a = f.a;
+    const int lane = threadIdx.x % L;
+    int run = blockIdx.x % (f.qc + f.kc);
+    const int64_t t = (int64_t)(blockIdx.x / (f.qc + f.kc)) * (256 / L) + threadIdx.x / L;
+    const int64_t tc = min(t, a.n - 1);  // lanes past the last token stay for the exchanges, with its data
+    const bool isq = run < f.qc;
+    const HeadRows &in = isq ? a.q : a.k;
+    void *out = isq ? f.qo : f.ko;
+    run = isq ? run : run - f.qc;
+    const int h0 = run * f.hp, h1 = min(h0 + f.hp, in.heads);
+    const Turn<IL> turn(a, tc, lane, L);
+    double u[8], v[8];
+    factors<IL>(a, in.w, turn, u, v);
+    const int64_t row = tc * in.ts + turn.col;
+    Raw<DT> next = load_raw<DT>(in.x, row + h0 * in.hs, turn.live);
+    for (int h = h0; h < h1; ++h) {
+        const Raw<DT> raw = next;
+        if (h + 1 < h1) next = load_raw<DT>(in.x, row + (h + 1) * in.hs, turn.live);
+        float y[8];
+        turn_row<DT, L, IL>(a, raw, turn, u, v, y);
+        if (turn.live && t < a.n) store_row<DT>(out, (t * in.heads + h) * a.d + turn.col, y);
+    }
+}
+
+namespace {
+
+struct FillArgs {
+    NormRope a;
+    HeadRows v;
+    void *qo;
+    uint8_t *cache;
+    Kv4Geom g;
+    const void *slots;
+    bool slots64;
+    int hp, qc, kc;
+};
+
+}  // namespace
+
+// Queries as above; a key/value head's rows of a token go into the cache as k_kv4_write puts them there.
+template <int DT, int D, bool IL>
+__global__ __launch_bounds__(256) void k_norm_rope_kv4(FillArgs f) {
+    constexpr int L = D / 8;
+    const NormRope &a = f.a;
+    const int lane = threadIdx.x % L;
+    int run = blockIdx.x % (f.qc + f.kc);
+    const int64_t t = (int64_t)(blockIdx.x / (f.qc + f.kc)) * (256 / L) + threadIdx.x / L;
+    const int64_t tc = min(t, a.n - 1);
+    const bool isq = run < f.qc;
+    const HeadRows &in = isq ? a.q : a.k;
+    run = isq ? run : run - f.qc;
+    const int h0 = run * f.hp, h1 = min(h0 + f.hp, in.heads);
+    const Turn<IL> turn(a, tc, lane, L);
+    double u[8], v[8];
+    factors<IL>(a, in.w, turn, u, v);
+    const int64_t row = tc * in.ts + turn.col;
+    Raw<DT> next = load_raw<DT>(in.x, row + h0 * in.hs, true);
+    if (isq) {
+        for (int h = h0; h < h1; ++h) {
+            const Raw<DT> raw = next;
+            if (h + 1 < h1) next = load_raw<DT>(in.x, row + (h + 1) * in.hs, true);
+            float y[8];
+            turn_row<DT, L, IL>(a, raw, turn, u, v, y);
+            if (t < a.n) store_row<DT>(f.qo, (t * in.heads + h) * D + turn.col, y);
+        }
+        return;
+    }
+    const int64_t vrow = tc * f.v.ts + turn.col;
+    Raw<DT> vnext = load_raw<DT>(f.v.x, vrow + h0 * f.v.hs, true);
+    const int64_t slot = f.slots64 ? static_cast<const int64_t *>(f.slots)[tc] : static_cast<const int32_t *>(f.slots)[tc];
+    const bool ok = t < a.n && slot >= 0 && slot < f.g.pages << f.g.page_log2;
+    const int P = 1 << f.g.page_log2, tok = ok ? (int)(slot & (P - 1)) : 0;
+    for (int h = h0; h < h1; ++h) {
+        const Raw<DT> raw = next, vraw = vnext;
+        if (h + 1 < h1) {
+            next = load_raw<DT>(in.x, row + (h + 1) * in.hs, true);
+            vnext = load_raw<DT>(f.v.x, vrow + (h + 1) * f.v.hs, true);
+        }
+        float y[8], z[8];
+        turn_row<DT, L, IL>(a, raw, turn, u, v, y);
+        values<DT>(vraw, z);
+        if constexpr (DT == DT_BF16) {  // the key as the norm's own output holds it
+#pragma unroll
+            for (int i = 0; i < 8; i += 2) {
+                const uint32_t b = bf16_pack2(y[i], y[i + 1]);
+                y[i] = __uint_as_float(b << 16);
+                y[i + 1] = __uint_as_float(b & 0xFFFF0000u);
+            }
+        }
+        uint32_t mk = amax8(y), mv = amax8(z);
+#pragma unroll
+        for (int off = 2; off > 0; off >>= 1) {
+            mk = max(mk, (uint32_t)__shfl_xor((int)mk, off, 64));
+            mv = max(mv, (uint32_t)__shfl_xor((int)mv, off, 64));
+        }
+        const uint64_t bad_all = __builtin_amdgcn_ballot_w64(max(mk, mv) >= 0x7F800000u);
+        const bool bad = ((bad_all >> ((threadIdx.x & 63) / L * L)) & ((1ull << L) - 1)) != 0;
+        const uint32_t ek = min(e8m0_of(mk, 2), 252u), ev = min(e8m0_of(mv, 2), 252u);
+        const float fk = e8m0_inv(ek), fv = e8m0_inv(ev);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            y[i] *= fk;
+            z[i] *= fv;
+        }
+        if (!ok) continue;
+        uint8_t *base = f.cache + ((slot >> f.g.page_log2) * f.g.hkv + h) * f.g.region();
+        *reinterpret_cast<uint32_t *>(base + tok * (D / 2) + lane * 4) = bad ? 0u : e2m1_pack8(y);
+        *reinterpret_cast<uint32_t *>(base + f.g.v_off() + ((tok >> 3) * L + lane) * 32 + (tok & 7) * 4) = bad ? 0u : e2m1_pack8(z);
+        if ((lane & 3) == 0) {
+            base[f.g.ks_off() + (lane >> 2) * P + tok] = (uint8_t)(bad ? 255u : ek);
+            base[f.g.vs_off() + (lane >> 2) * P + tok] = (uint8_t)(bad ? 0u : ev);
+        }
+    }
+}
+
+namespace {
+
+struct BwdArgs {
+    NormRope a;
+    RopeGrads g;
+    int hp, qc, kc;    // as above
+    int qb, kb;        // workgroups of queries and of keys
+    float *part;       // a row of d sums each, or NULL
+};
+
+}  // namespace
+
+template <int DT, int L, bool IL>
+__global__ __launch_bounds__(256) void k_norm_rope_bwd(BwdArgs f) {
+    const NormRope &a = f.a;
+    const int lane = threadIdx.x % L;
+    const bool isq = (int)blockIdx.x < f.qb;
+    const HeadRows &in = isq ? a.q : a.k, &dy = isq ? f.g.dq : f.g.dk;
+    void *dx = isq ? f.g.dxq : f.g.dxk;
+    const int64_t dx_ts = isq ? f.g.dxq_ts : f.g.dxk_ts, dx_hs = isq ? f.g.dxq_hs : f.g.dxk_hs;
+    const int runs = isq ? f.qc : f.kc, blocks = isq ? f.qb : f.kb, me = isq ? blockIdx.x : blockIdx.x - f.qb;
+    const int64_t items = (a.n + 256 / L - 1) / (256 / L) * runs;
+    float dw[8] = {0, 0, 0, 0, 0, 0, 0, 0}, w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = lane * 8 < a.d ? weight_at(a, in.w, lane * 8 + i) : 0.0f;
+    for (int64_t item = me; item < items; item += blocks) {
+        const int64_t t = item / runs * (256 / L) + threadIdx.x / L, tc = min(t, a.n - 1);
+        const int h0 = (int)(item % runs) * f.hp, h1 = min(h0 + f.hp, in.heads);
+        const Turn<IL> turn(a, tc, lane, L);
+        const bool off = turn.zero || t >= a.n;
+        const int64_t xr = tc * in.ts + turn.col, yr = tc * dy.ts + turn.col;
+        Raw<DT> xn = load_raw<DT>(in.x, xr + h0 * in.hs, turn.live), yn = load_raw<DT>(dy.x, yr + h0 * dy.hs, turn.live);
+        for (int h = h0; h < h1; ++h) {
+            const Raw<DT> xw = xn, yw = yn;
+            if (h + 1 < h1) {
+                xn = load_raw<DT>(in.x, xr + (h + 1) * in.hs, turn.live);
+                yn = load_raw<DT>(dy.x, yr + (h + 1) * dy.hs, turn.live);
+            }
+            float x[8], y[8], p[8], g[8];
+            values<DT>(xw, x);
+            values<DT>(yw, y);
+            partners<DT, IL>(yw, turn.from, p);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) g[i] = __builtin_fmaf(-turn.s[i], p[i], y[i] * turn.c[i]);
+            if (a.norm) {
+                double ss = 0.0;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) ss = __builtin_fma((double)x[i], (double)x[i], ss);
+                const double r = rsqrt64(group_sum<L>(ss) / a.d + (double)a.eps);
+                float dot = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    x[i] = (float)(x[i] * r);
+                    const float e = off ? 0.0f : g[i] * x[i];
+                    dw[i] += e;
+                    g[i] *= w[i];
+                    dot = __builtin_fmaf(g[i], x[i], dot);
+                }
+                dot = group_sum<L>(dot) / a.d;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) g[i] = (float)r * __builtin_fmaf(-x[i], dot, g[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) g[i] = off ? 0.0f : g[i];
+            if (turn.live && t < a.n) store_row<DT>(dx, t * dx_ts + h * dx_hs + turn.col, g);
+        }
+    }
+    if (!f.part) return;
+    // the lane groups' sums in order: those of a wave by exchanges, then the waves'
+    __shared__ float sums[4][L * 8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int off = L; off < 64; off <<= 1) dw[i] += __shfl_xor(dw[i], off, 64);
+    if ((threadIdx.x & 63) < L) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sums[threadIdx.x >> 6][lane * 8 + i] = dw[i];
+    }
+    __syncthreads();
+    if ((int)threadIdx.x < a.d)
+        f.part[(int64_t)blockIdx.x * a.d + threadIdx.x] =
+            (sums[0][threadIdx.x] + sums[1][threadIdx.x]) + (sums[2][threadIdx.x] + sums[3][threadIdx.x]);
+}
+
+// Partial weight gradients (rows of d) to their sums: 16 rows at once for 16 columns, then the 16 in order.
+__global__ __launch_bounds__(256) void k_rope_dw(const float *__restrict__ part, int qb, int kb, int d, float *dwq, float *dwk) {
+    const bool isq = blockIdx.y == 0;
+    float *out = isq ? dwq : dwk;
+    if (!out) return;
+    const int first = isq ? 0 : qb, rows = isq ? qb : kb;
+    const int col = blockIdx.x * 16 + threadIdx.x % 16, r = threadIdx.x / 16;
+    float s = 0.0f;
+    if (col < d)
+        for (int i = r; i < rows; i += 16) s += part[(int64_t)(first + i) * d + col];
+    __shared__ float sums[16][17];
+    sums[r][threadIdx.x % 16] = s;
+    __syncthreads();
+    if (r == 0 && col < d) {
+        s = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s += sums[i][threadIdx.x];
+        out[col] = s;
+    }
+}
+
+// cos and sin of (pos / factor) * base^(-2 i / rot), in 64 bits, rounded once.
+__global__ __launch_bounds__(256) void k_rope_table(float *__restrict__ table, int64_t max_pos, int rot, double base, double factor) {
+    const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int half = rot / 2;
+    if (id >= max_pos * half) return;
+    const int64_t pos = id / half;
+    const int i = (int)(id % half);
+    double s, c;
+    sincos((double)pos / factor * pow(base, -2.0 * i / rot), &s, &c);
+    table[pos * rot + i] = (float)c;
+    table[pos * rot + half + i] = (float)s;
+}
+
+hipError_t launch_rope_table(float *table, int64_t max_pos, int rot, double base, double factor, hipStream_t s) {
+    hipLaunchKernelGGL(k_rope_table, dim3((unsigned)((max_pos * (rot / 2) + 255) / 256)), dim3(256), 0, s, table, max_pos, rot,
+                       base, factor);
+    return hipGetLastError();
+}
+
+namespace {
+
+int lanes_of(int d) { return d <= 32 ? 4 : d <= 64 ? 8 : d <= 128 ? 16 : 32; }
+
+// Heads a lane group goes through: as many as leave 2048 workgroups, 8 at most.
+int heads_a_run(int64_t n, int d, int heads) {
+    const int64_t blocks = (n + 256 / lanes_of(d) - 1) / (256 / lanes_of(d));
+    return (int)std::max<int64_t>(1, std::min<int64_t>(8, blocks * heads / 2048));
+}
+
+}  // namespace
+
+#define ROPE_L(KERNEL, DT, IL, ...)                                                                  \
+    switch (lanes_of(a.d)) {                                                                         \
+        case 4: hipLaunchKernelGGL((KERNEL<DT, 4, IL>), grid, dim3(256), 0, s, __VA_ARGS__); break;  \
+        case 8: hipLaunchKernelGGL((KERNEL<DT, 8, IL>), grid, dim3(256), 0, s, __VA_ARGS__); break;  \
+        case 16: hipLaunchKernelGGL((KERNEL<DT, 16, IL>), grid, dim3(256), 0, s, __VA_ARGS__); break; \
+        default: hipLaunchKernelGGL((KERNEL<DT, 32, IL>), grid, dim3(256), 0, s, __VA_ARGS__);       \
+    }
+#define ROPE_DISPATCH(KERNEL, ...)                                                     \
+    do {                                                                               \
+        if (a.dt == DT_BF16 && a.interleaved) { ROPE_L(KERNEL, DT_BF16, true, __VA_ARGS__) } \
+        else if (a.dt == DT_BF16) { ROPE_L(KERNEL, DT_BF16, false, __VA_ARGS__) }      \
+        else if (a.interleaved) { ROPE_L(KERNEL, DT_F32, true, __VA_ARGS__) }          \
+        else { ROPE_L(KERNEL, DT_F32, false, __VA_ARGS__) }                            \
+    } while (0)
+
+hipError_t launch_norm_rope(const NormRope &a, void *qo, void *ko, hipStream_t s) {
+    FwdArgs f;
+    f.a = a;
+    f.qo = qo;
+    f.ko = ko;
+    f.hp = heads_a_run(a.n, a.d, a.q.heads + a.k.heads);
+    f.qc = (a.q.heads + f.hp - 1) / f.hp;
+    f.kc = (a.k.heads + f.hp - 1) / f.hp;
+    const int per = 256 / lanes_of(a.d);
+    const dim3 grid((unsigned)((a.n + per - 1) / per * (f.qc + f.kc)));
+    ROPE_DISPATCH(k_norm_rope, f);
+    return hipGetLastError();
+}
+
+hipError_t launch_norm_rope_kv4(const NormRope &a, const HeadRows &v, void *qo, uint8_t *cache, const Kv4Geom &g,
+                                const void *slots, bool slots64, hipStream_t s) {
+    FillArgs f;
+    f.a = a;
+    f.v = v;
+    f.qo = qo;
+    f.cache = cache;
+    f.g = g;
+    f.slots = slots;
+    f.slots64 = slots64;
+    f.hp = heads_a_run(a.n, a.d, a.q.heads + 2 * a.k.heads);
+    f.qc = (a.q.heads + f.hp - 1) / f.hp;
+    f.kc = (a.k.heads + f.hp - 1) / f.hp;
+    const int per = 256 / lanes_of(a.d);
+    const dim3 grid((unsigned)((a.n + per - 1) / per * (f.qc + f.kc)));
+#define FILL(DT, D)                                                                                                  \
+    do {                                                                                                             \
+        if (a.interleaved) hipLaunchKernelGGL((k_norm_rope_kv4<DT, D, true>), grid, dim3(256), 0, s, f);             \
+        else hipLaunchKernelGGL((k_norm_rope_kv4<DT, D, false>), grid, dim3(256), 0, s, f);                          \
+    } while (0)
+    if (a.dt == DT_BF16 && a.d == 128) FILL(DT_BF16, 128);
+    else if (a.dt == DT_BF16) FILL(DT_BF16, 64);
+    else if (a.d == 128) FILL(DT_F32, 128);
+    else FILL(DT_F32, 64);
+#undef FILL
+    return hipGetLastError();
+}
+
+static void bwd_blocks(const NormRope &a, BwdArgs &f) {
+    f.hp = heads_a_run(a.n, a.d, a.q.heads + a.k.heads);
+    f.qc = (a.q.heads + f.hp - 1) / f.hp;
+    f.kc = (a.k.heads + f.hp - 1) / f.hp;
+    const int per = 256 / lanes_of(a.d);
+    const int64_t tb = (a.n + per - 1) / per, qi = tb * f.qc, ki = tb * f.kc;
+    const int64_t all = qi + ki, most = std::min<int64_t>(all, BWD_BLOCKS);
+    // shared in proportion to the work, one at least for each tensor
+    f.kb = ki ? (int)std::max<int64_t>(1, std::min(ki, most * ki / all)) : 0;
+    f.qb = (int)std::min(qi, std::max<int64_t>(1, most - f.kb));
+}
+
+size_t norm_rope_bwd_ws_bytes(int d) { return (size_t)(BWD_BLOCKS + 1) * d * 4; }
+
+hipError_t launch_norm_rope_bwd(const NormRope &a, const RopeGrads &g, float *ws, hipStream_t s) {
+    BwdArgs f;
+    f.a = a;
+    f.g = g;
+    f.part = a.norm && (g.dwq || g.dwk) ? ws : nullptr;
+    bwd_blocks(a, f);
+    const dim3 grid((unsigned)(f.qb + f.kb));
+    ROPE_DISPATCH(k_norm_rope_bwd, f);
+    hipError_t e = hipGetLastError();
+    if (f.part && e == hipSuccess) {
+        hipLaunchKernelGGL(k_rope_dw, dim3((unsigned)((a.d + 15) / 16), 2), dim3(256), 0, s, ws, f.qb, f.kb, a.d, g.dwq, g.dwk);
+        e = hipGetLastError();
+    }
+    return e;
+}
+
+}  // namespace fp4
