@@ -446,6 +446,29 @@ fp4_status fp4_kv4_attention(const void *q, int64_t q_token_stride, int64_t q_he
                              int64_t pages, int32_t page, int32_t hkv, int32_t d, int32_t window, float scale, void *o,
                              float *lse, void *workspace, size_t ws_bytes, void *stream);
 
+/* The same with a window and a few first tokens that stay visible: query j at position p sees the tokens t <= p with
+ * t > p - window or t < sinks.  Tokens between need no page (fp4_kv4_release gives theirs back).  Without a window,
+ * or with sinks = 0, it is fp4_kv4_attention; the workspace is that call's too. */
+fp4_status fp4_kv4_attention_sinks(const void *q, int64_t q_token_stride, int64_t q_head_stride, int64_t nq, int32_t hq,
+                                   const int32_t *q_start, const int32_t *lens, int32_t b, int32_t max_q,
+                                   const int32_t *table, int64_t table_stride, int32_t width, const uint8_t *cache,
+                                   int64_t pages, int32_t page, int32_t hkv, int32_t d, int32_t window, int32_t sinks,
+                                   float scale, void *o, float *lse, void *workspace, size_t ws_bytes, void *stream);
+
+/* The same (without a window) for sequences whose first pages are shared: the first `shared` (1 .. width) pages of
+ * every row are taken to be those of row 0, whose bytes are read once for the queries of all sequences, not once for each
+ * sequence.  lens count the shared tokens; a sequence may be shorter than they are.  Results are those of
+ * fp4_kv4_attention within the roundings of its sums.
+ * Further limit: nq * (hq / hkv) < 2^24.
+ *   workspace: at least fp4_kv4_attention_shared_workspace_bytes(...) bytes (0: invalid arguments). */
+size_t fp4_kv4_attention_shared_workspace_bytes(int64_t nq, int32_t b, int32_t max_q, int32_t hq, int32_t hkv, int32_t d,
+                                                int32_t page, int32_t width, int32_t shared);
+fp4_status fp4_kv4_attention_shared(const void *q, int64_t q_token_stride, int64_t q_head_stride, int64_t nq, int32_t hq,
+                                    const int32_t *q_start, const int32_t *lens, int32_t b, int32_t max_q,
+                                    const int32_t *table, int64_t table_stride, int32_t width, const uint8_t *cache,
+                                    int64_t pages, int32_t page, int32_t hkv, int32_t d, int32_t shared, float scale, void *o,
+                                    float *lse, void *workspace, size_t ws_bytes, void *stream);
+
 /* ---------------------------------------------------------------------------------------------
  * Page tables of a 4-bit cache, kept on the GPU.  b sequences have a row of `width` page indices each (rows table_stride
  * apart) and a length in tokens, lens; free_pages (int32[pages]) holds the free pages in its first *free_count

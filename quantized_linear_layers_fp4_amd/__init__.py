@@ -38,6 +38,7 @@ EXPORTS = (
     "fp4_block8_gemm", "fp4_block8_linear_workspace_bytes", "fp4_block8_linear",
     "fp4_block8_backward_workspace_bytes", "fp4_block8_backward",
     "fp4_kv4_cache_bytes", "fp4_kv4_write", "fp4_kv4_read", "fp4_kv4_attention_workspace_bytes", "fp4_kv4_attention",
+    "fp4_kv4_attention_sinks", "fp4_kv4_attention_shared_workspace_bytes", "fp4_kv4_attention_shared",
     "fp4_kv4_extend_workspace_bytes", "fp4_kv4_extend", "fp4_kv4_release_workspace_bytes", "fp4_kv4_release",
     "fp4_rope_table", "fp4_qk_norm_rope", "fp4_kv4_norm_rope", "fp4_qk_norm_rope_backward_workspace_bytes",
     "fp4_qk_norm_rope_backward",
@@ -107,6 +108,11 @@ def lib():
         "fp4_kv4_attention_workspace_bytes": (sz, [i32, i32, i32, i32, i32, i32, i32]),
         "fp4_kv4_attention": (i32, [vp, i64, i64, i64, i32, vp, vp, i32, i32, vp, i64, i32, vp, i64, i32, i32, i32,
                                     i32, C.c_float, vp, vp, vp, sz, vp]),
+        "fp4_kv4_attention_sinks": (i32, [vp, i64, i64, i64, i32, vp, vp, i32, i32, vp, i64, i32, vp, i64, i32, i32, i32,
+                                          i32, i32, C.c_float, vp, vp, vp, sz, vp]),
+        "fp4_kv4_attention_shared_workspace_bytes": (sz, [i64, i32, i32, i32, i32, i32, i32, i32, i32]),
+        "fp4_kv4_attention_shared": (i32, [vp, i64, i64, i64, i32, vp, vp, i32, i32, vp, i64, i32, vp, i64, i32, i32, i32,
+                                           i32, C.c_float, vp, vp, vp, sz, vp]),
         "fp4_kv4_extend_workspace_bytes": (sz, [i32, i64]),
         "fp4_kv4_extend": (i32, [vp, i64, i32, i32, vp, vp, vp, i64, i32, vp, i64, vp, vp, vp, vp, sz, vp]),
         "fp4_kv4_release_workspace_bytes": (sz, [i32, i32]),
@@ -635,23 +641,30 @@ def kv4_read(cache: KV4Cache, slots: torch.Tensor, d: int | None = None, out_dty
     return k, v
 
 
-def kv4_attention_workspace(q: torch.Tensor, cache: KV4Cache, pages: torch.Tensor, max_q: int = 1) -> torch.Tensor:
-    """A workspace for kv4_attention with these sizes and any window (max_q as there: q's rows if it is not given
+def kv4_attention_workspace(q: torch.Tensor, cache: KV4Cache, pages: torch.Tensor, max_q: int = 1,
+                            shared: int = 0) -> torch.Tensor:
+    """A workspace for kv4_attention with these sizes and any window and sinks (max_q as there: q's rows if it is not given
     with q_start)."""
-    n = lib().fp4_kv4_attention_workspace_bytes(pages.shape[0], max_q, q.shape[1], cache.heads, cache.d, cache.page,
-                                                pages.shape[1])
+    b, width = pages.shape
+    if shared and b and q.shape[0]:
+        n = lib().fp4_kv4_attention_shared_workspace_bytes(q.shape[0], b, max_q, q.shape[1], cache.heads, cache.d, cache.page,
+                                                           width, shared)
+    else:
+        n = lib().fp4_kv4_attention_workspace_bytes(b, max_q, q.shape[1], cache.heads, cache.d, cache.page, width)
     return torch.empty(max(n, 16), dtype=torch.uint8, device=q.device)
 
 
 def kv4_attention(q: torch.Tensor, cache: KV4Cache, pages: torch.Tensor, lens: torch.Tensor,
                   q_start: torch.Tensor | None = None, max_q: int | None = None, window: int = 0, scale: float | None = None,
-                  return_lse: bool = False, ws: torch.Tensor | None = None):
+                  return_lse: bool = False, ws: torch.Tensor | None = None, sinks: int = 0, shared: int = 0):
     """Causal attention of packed bf16 queries q (nq x hq x d) over the cache.  pages: int32 page table
     (b x width); lens: int32 tokens of each sequence in the cache, its queries' own among them; q_start: int32
     b + 1 offsets of the sequences' queries, or None for one query a sequence; max_q: the most queries of a
     sequence (None: as many as q has, or 1 without q_start; a close bound is faster, needs less workspace, and is
     needed where b times q's rows pass what a call may have);
-    window: tokens a query sees (0: all).  A query that sees nothing gets 0 and lse -inf, and so does one past its
+    window: tokens a query sees (0: all); sinks: with a window, the first tokens of a sequence that stay visible;
+    shared: the first pages of every row that are taken to be row 0's and read once for all sequences (not with
+    a window; ws of kv4_attention_workspace with the same shared).  A query that sees nothing gets 0 and lse -inf, and so does one past its
     sequence's first max_q, before q_start[0] or from q_start[b] on."""
     if q.dtype != torch.bfloat16:
         raise TypeError(f"expected bfloat16 queries, got {q.dtype}")
@@ -673,6 +686,10 @@ def kv4_attention(q: torch.Tensor, cache: KV4Cache, pages: torch.Tensor, lens: t
         raise ValueError(f"{nq} queries for {b} sequences without q_start")
     if max_q is None:
         max_q = 1 if q_start is None else nq
+    if sinks < 0 or shared < 0:
+        raise ValueError(f"sinks {sinks}, shared {shared}")
+    if shared and window:
+        raise ValueError("shared pages and a window do not go together")
     _same_device(q, cache.data, pages, lens, q_start, ws)
     if ws is not None and not ws.is_contiguous():
         raise ValueError("expected a contiguous workspace")
@@ -684,12 +701,14 @@ def kv4_attention(q: torch.Tensor, cache: KV4Cache, pages: torch.Tensor, lens: t
             lse.fill_(float("-inf"))
     elif nq:
         if ws is None:
-            ws = kv4_attention_workspace(q, cache, pages, max_q)
-        _check(lib().fp4_kv4_attention(_ptr(q), q.stride(0), q.stride(1), nq, hq, _ptr(q_start), _ptr(lens), b, max_q,
-                                       _ptr(pages), max(pages.stride(0), pages.shape[1]), pages.shape[1],
-                                       _ptr(cache.data), cache.pages, cache.page, cache.heads, d, min(window, 0x7FFFFFFF),
-                                       d ** -0.5 if scale is None else float(scale), _ptr(o), _ptr(lse), _ptr(ws),
-                                       ws.numel(), _stream(q)))
+            ws = kv4_attention_workspace(q, cache, pages, max_q, shared)
+        L, most = lib(), 0x7FFFFFFF
+        f, seen = (L.fp4_kv4_attention_shared, (shared,)) if shared else \
+            (L.fp4_kv4_attention_sinks, (min(window, most), min(sinks, most)))
+        _on_device(q, lambda: _check(f(
+            _ptr(q), q.stride(0), q.stride(1), nq, hq, _ptr(q_start), _ptr(lens), b, max_q, _ptr(pages),
+            max(pages.stride(0), pages.shape[1]), pages.shape[1], _ptr(cache.data), cache.pages, cache.page, cache.heads, d,
+            *seen, d ** -0.5 if scale is None else float(scale), _ptr(o), _ptr(lse), _ptr(ws), ws.numel(), _stream(q))))
     return (o, lse) if return_lse else o
 
 

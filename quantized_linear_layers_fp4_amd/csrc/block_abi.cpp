@@ -222,26 +222,26 @@ size_t fp4_kv4_attention_workspace_bytes(int32_t b, int32_t max_q, int32_t hq, i
     return kv4_attn_ws_bytes(b, max_q, hq, g, width);
 }
 
-fp4_status fp4_kv4_attention(const void *q, int64_t q_token_stride, int64_t q_head_stride, int64_t nq, int32_t hq,
-                             const int32_t *q_start, const int32_t *lens, int32_t b, int32_t max_q,
-                             const int32_t *table, int64_t table_stride, int32_t width, const uint8_t *cache,
-                             int64_t pages, int32_t page, int32_t hkv, int32_t d, int32_t window, float scale, void *o,
-                             float *lse, void *workspace, size_t ws_bytes, void *stream) {
-    if (!q || !lens || !table || !cache || !o) return FP4_ERR_NULL;
-    Kv4Geom g;
-    if (!geom(pages, page, hkv, d, g) || !attn_shape(b, max_q, hq, hkv, width, page, window)) return FP4_ERR_SHAPE;
+// What the attention calls check and hand over alike; need: the workspace's bytes.
+static fp4_status attention_check(const void *q, int64_t nq, int32_t hq, const int32_t *q_start, const int32_t *lens, int32_t b,
+                                  int32_t max_q, const int32_t *table, int64_t table_stride, int32_t width,
+                                  const uint8_t *cache, void *o, float *lse, void *workspace, size_t ws_bytes, size_t need) {
     if (nq < 1 || nq > 0x7FFFFFFF / hq || table_stride < width || (!q_start && (nq != b || max_q != 1)))
         return FP4_ERR_SHAPE;
-    const size_t need = kv4_attn_ws_bytes(b, max_q, hq, g, width);
     if (need && !workspace) return FP4_ERR_NULL;
     if (ws_bytes < need) return FP4_ERR_WORKSPACE;
     if (!al_elem(q, FP4_BF16) || !al16(cache) || !al16(o) || !al_elem(lse, FP4_F32) || !al16(workspace) ||
         !al_elem(lens, FP4_F32) || !al_elem(table, FP4_F32) || !al_elem(q_start, FP4_F32))
         return FP4_ERR_ALIGN;
     int cus;
-    const fp4_status st = device_check(&cus);
-    if (st != FP4_OK) return st;
-    Kv4Attn a;
+    return device_check(&cus);
+}
+
+static Kv4Attn attention_args(const void *q, int64_t q_token_stride, int64_t q_head_stride, int64_t nq, int32_t hq,
+                              const int32_t *q_start, const int32_t *lens, int32_t b, int32_t max_q, const int32_t *table,
+                              int64_t table_stride, int32_t width, const uint8_t *cache, const Kv4Geom &g, float scale,
+                              void *o, float *lse, void *workspace) {
+    Kv4Attn a{};
     a.q = static_cast<const uint16_t *>(q);
     a.q_ts = q_token_stride;
     a.q_hs = q_head_stride;
@@ -256,12 +256,68 @@ fp4_status fp4_kv4_attention(const void *q, int64_t q_token_stride, int64_t q_he
     a.nq = (int)nq;
     a.hq = hq;
     a.max_q = max_q;
-    a.window = window;
     a.scale = scale;
     a.o = static_cast<uint16_t *>(o);
     a.lse = lse;
     a.ws = static_cast<uint8_t *>(workspace);
+    return a;
+}
+
+fp4_status fp4_kv4_attention_sinks(const void *q, int64_t q_token_stride, int64_t q_head_stride, int64_t nq, int32_t hq,
+                                   const int32_t *q_start, const int32_t *lens, int32_t b, int32_t max_q,
+                                   const int32_t *table, int64_t table_stride, int32_t width, const uint8_t *cache,
+                                   int64_t pages, int32_t page, int32_t hkv, int32_t d, int32_t window, int32_t sinks,
+                                   float scale, void *o, float *lse, void *workspace, size_t ws_bytes, void *stream) {
+    if (!q || !lens || !table || !cache || !o) return FP4_ERR_NULL;
+    Kv4Geom g;
+    if (!geom(pages, page, hkv, d, g) || !attn_shape(b, max_q, hq, hkv, width, page, window) || sinks < 0) return FP4_ERR_SHAPE;
+    const fp4_status st = attention_check(q, nq, hq, q_start, lens, b, max_q, table, table_stride, width, cache, o, lse,
+                                          workspace, ws_bytes, kv4_attn_ws_bytes(b, max_q, hq, g, width));
+    if (st != FP4_OK) return st;
+    Kv4Attn a = attention_args(q, q_token_stride, q_head_stride, nq, hq, q_start, lens, b, max_q, table, table_stride, width,
+                               cache, g, scale, o, lse, workspace);
+    a.window = window;
+    a.sinks = sinks;
     return hip_status(launch_kv4_attn(a, hs(stream)));
+}
+
+fp4_status fp4_kv4_attention(const void *q, int64_t q_token_stride, int64_t q_head_stride, int64_t nq, int32_t hq,
+                             const int32_t *q_start, const int32_t *lens, int32_t b, int32_t max_q,
+                             const int32_t *table, int64_t table_stride, int32_t width, const uint8_t *cache,
+                             int64_t pages, int32_t page, int32_t hkv, int32_t d, int32_t window, float scale, void *o,
+                             float *lse, void *workspace, size_t ws_bytes, void *stream) {
+    return fp4_kv4_attention_sinks(q, q_token_stride, q_head_stride, nq, hq, q_start, lens, b, max_q, table, table_stride,
+                                   width, cache, pages, page, hkv, d, window, 0, scale, o, lse, workspace, ws_bytes, stream);
+}
+
+// The shared pages' rows are all queries': the limits of attn_shape, as of one sequence with nq queries.
+static bool shared_shape(int64_t nq, int32_t b, int32_t max_q, int32_t hq, int32_t hkv, int32_t width, int32_t page, int32_t shared) {
+    return attn_shape(b, max_q, hq, hkv, width, page, 0) && shared >= 1 && shared <= width && nq >= 1 && nq <= (1 << 24) &&
+           attn_shape(1, (int32_t)nq, hq, hkv, width, page, 0);
+}
+
+size_t fp4_kv4_attention_shared_workspace_bytes(int64_t nq, int32_t b, int32_t max_q, int32_t hq, int32_t hkv, int32_t d,
+                                                int32_t page, int32_t width, int32_t shared) {
+    Kv4Geom g;
+    if (!geom(1, page, hkv, d, g) || !shared_shape(nq, b, max_q, hq, hkv, width, page, shared)) return 0;
+    return kv4_attn_shared_ws_bytes(nq, b, max_q, hq, g, width, shared);
+}
+
+fp4_status fp4_kv4_attention_shared(const void *q, int64_t q_token_stride, int64_t q_head_stride, int64_t nq, int32_t hq,
+                                    const int32_t *q_start, const int32_t *lens, int32_t b, int32_t max_q,
+                                    const int32_t *table, int64_t table_stride, int32_t width, const uint8_t *cache,
+                                    int64_t pages, int32_t page, int32_t hkv, int32_t d, int32_t shared, float scale, void *o,
+                                    float *lse, void *workspace, size_t ws_bytes, void *stream) {
+    if (!q || !lens || !table || !cache || !o) return FP4_ERR_NULL;
+    Kv4Geom g;
+    if (!geom(pages, page, hkv, d, g) || !shared_shape(nq, b, max_q, hq, hkv, width, page, shared)) return FP4_ERR_SHAPE;
+    const fp4_status st = attention_check(q, nq, hq, q_start, lens, b, max_q, table, table_stride, width, cache, o, lse,
+                                          workspace, ws_bytes, kv4_attn_shared_ws_bytes(nq, b, max_q, hq, g, width, shared));
+    if (st != FP4_OK) return st;
+    Kv4Attn a = attention_args(q, q_token_stride, q_head_stride, nq, hq, q_start, lens, b, max_q, table, table_stride, width,
+                               cache, g, scale, o, lse, workspace);
+    a.shared = shared;
+    return hip_status(launch_kv4_attn_shared(a, hs(stream)));
 }
 
 }  // extern "C"

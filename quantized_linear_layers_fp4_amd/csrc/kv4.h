@@ -41,6 +41,8 @@ struct Kv4Attn {
     const uint8_t *cache;
     Kv4Geom geo;
     int b, nq, hq, max_q, window;
+    int sinks;                  // with a window: first tokens that stay visible
+    int shared;                 // first pages that all rows have in common (launch_kv4_attn_shared)
     float scale;                // of the scores
     uint16_t *o;                // nq x hq x d bf16
     float *lse;                 // nq x hq, or NULL
@@ -54,5 +56,7 @@ hipError_t launch_kv4_read(const uint8_t *cache, const Kv4Geom &g, const void *s
                            void *V, int dt, hipStream_t s);
 size_t kv4_attn_ws_bytes(int b, int max_q, int hq, const Kv4Geom &g, int width);
 hipError_t launch_kv4_attn(const Kv4Attn &a, hipStream_t s);
+size_t kv4_attn_shared_ws_bytes(int64_t nq, int b, int max_q, int hq, const Kv4Geom &g, int width, int shared);
+hipError_t launch_kv4_attn_shared(const Kv4Attn &a, hipStream_t s);
 
 }  // namespace fp4

@@ -37,6 +37,16 @@ constexpr int FEW = 32;      // rows a (sequence, head) up to which the decode k
 constexpr float LN2 = 0.69314718055994530942f;
 constexpr float LOG2E = 1.44269504088896340736f;
 
+// What a kernel's tokens are.
+//   PLAIN   a sequence's, or those of its window
+//   SINKS   those of its window and the first a.sinks ones: tokens are counted along an axis that leaves out those
+//           between (Span::turn, gap), so the tiles, splits and joins are those of PLAIN
+//   PREFIX  the first a.shared pages of row 0 of the table, for the queries of all sequences at once: rows are those of one
+//           long sequence, and more rows a tile read the bytes once
+//   OWN     a sequence's after those
+// PREFIX and OWN leave partial results, which one join brings together.
+enum : int { PLAIN, SINKS, PREFIX, OWN };
+
 struct DecArgs {
     Kv4Attn a;
     int g, rt;        // heads a group; row tiles a (sequence, head)
@@ -47,6 +57,10 @@ struct DecArgs {
     int chunk;        // tokens each takes (a multiple of the unit, nw * TT or CT)
     int work, blanks; // workgroups that attend; those after them, for the queries of no row tile
     float c;          // scale * log2(e)
+    float *part;      // partial results
+    // of the join of OWN: PREFIX's tile rows, rows a partial holds, splits and partial results
+    int ptr_, ppr, psplits;
+    const float *ppart;
 };
 
 // Entry i of a table that no kernel here writes: a scalar load where i is uniform, though other code of the kernel
@@ -61,6 +75,8 @@ struct Span {
     int rows;         // qlen * g
     int lo, hi;       // tokens any of the tile's rows sees: [lo, hi), lo a multiple of TT
     int full_lo, full_hi;  // tokens that all of its rows see
+    // SINKS: token t of the axis stands for t, or from `turn` on (a multiple of CT) for t + gap; the window's tokens
+    int turn, gap, wlo, whi;
 };
 
 // The first token that a query at position p sees (0 for p below 0, which sees none); no difference here leaves the
@@ -70,24 +86,86 @@ __device__ __forceinline__ int first_seen(int window, int p) { return window && 
 // The query at offset entry i, inside the queries whatever the entry says.
 __device__ __forceinline__ int query_at(const Kv4Attn &a, int i) { return min(max(fixed(a.q_start, i), 0), a.nq); }
 
+// The tokens that all rows share.
+__device__ __forceinline__ int prefix_of(const Kv4Attn &a) { return a.shared << a.geo.page_log2; }
+
+template <int MODE>
 __device__ __forceinline__ Span span_of(const Kv4Attn &a, int g, int seq, int row0, int nrows) {
     Span s;
+    if constexpr (MODE == PREFIX) {
+        s.len = s.hi = s.full_hi = prefix_of(a);
+        s.qbeg = s.lo = s.full_lo = 0;
+        s.qlen = a.nq;
+        s.rows = a.nq * g;
+        return s;
+    }
     s.len = max(fixed(a.lens, seq), 0);
     s.qbeg = a.q_start ? query_at(a, seq) : seq;
     s.qlen = a.q_start ? query_at(a, seq + 1) - s.qbeg : 1;
     s.rows = min(max(s.qlen, 0), a.max_q) * g;
     const int cap = min(s.len, a.width << a.geo.page_log2);
     s.lo = s.hi = s.full_lo = s.full_hi = 0;
+    if constexpr (MODE == SINKS) s.turn = s.gap = s.wlo = s.whi = 0;
     if (row0 >= s.rows) return s;
     const int j0 = row0 / g, j1 = min(row0 + nrows - 1, s.rows - 1) / g;
     const int p0 = s.len - s.qlen + j0, p1 = s.len - s.qlen + j1;
-    const int lo = first_seen(a.window, p0) & ~(TT - 1), hi = max(min(p1 + 1, cap), 0);
-    if (lo >= hi) return s;
-    s.lo = lo;
-    s.hi = hi;
-    s.full_lo = first_seen(a.window, p1);
+    const int lo = (MODE == OWN ? prefix_of(a) : first_seen(a.window, p0)) & ~(TT - 1), hi = max(min(p1 + 1, cap), 0);
+    if constexpr (MODE == SINKS) {
+        s.wlo = lo;
+        s.whi = hi;
+        if (hi <= 0) return s;
+        const int turn = (int)(((int64_t)min(a.sinks, hi) + CT - 1) & ~(int64_t)(CT - 1));
+        if (turn < lo) {
+            s.turn = turn;
+            s.gap = lo - turn;  // a window that the table's row ends before leaves the first tokens alone
+        }
+        s.hi = turn < lo ? turn + max(hi - lo, 0) : hi;
+    } else {
+        if (lo >= hi) return s;
+        s.lo = lo;
+        s.hi = hi;
+    }
+    s.full_lo = MODE == OWN ? prefix_of(a) : first_seen(a.window, p1);
     s.full_hi = min(p0 + 1, cap);
     return s;
+}
+
+// A place of the axis as a token.
+template <int MODE>
+__device__ __forceinline__ int token_at(const Span &s, int t) {
+    if constexpr (MODE == SINKS) return t >= s.turn ? t + s.gap : t;
+    return t;
+}
+
+// The sequence that owns a query, -1 if none does or if it is past the sequence's first max_q.
+__device__ __forceinline__ int owner_of(const Kv4Attn &a, int query) {
+    if (!a.q_start) return query;
+    int lo = 0, hi = a.b + 1;  // the number of offsets up to `query`
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (a.q_start[mid] <= query) lo = mid + 1;
+        else hi = mid;
+    }
+    if (lo == 0 || lo > a.b || query - query_at(a, lo - 1) >= a.max_q) return -1;
+    return lo - 1;
+}
+
+// PREFIX: whether some sequence has queries that do not see all shared tokens (all threads of the workgroup call it).
+__device__ __forceinline__ bool some_short(const Kv4Attn &a, int threads) {
+    bool s = false;
+    for (int i = threadIdx.x; i < a.b; i += threads) {
+        const int ql = a.q_start ? query_at(a, i + 1) - query_at(a, i) : 1;
+        s = s || (ql > 0 && (int64_t)max(a.lens[i], 0) - ql + 1 < prefix_of(a));
+    }
+    return __syncthreads_or(s) != 0;
+}
+
+// PREFIX: the number of shared tokens that a row sees, `row` one of the call's.
+__device__ __forceinline__ int prefix_seen(const Kv4Attn &a, int g, int row) {
+    const int query = row / g, seq = owner_of(a, query);
+    if (seq < 0) return prefix_of(a);  // of a row that nothing is made of
+    const int beg = a.q_start ? query_at(a, seq) : query, ql = a.q_start ? query_at(a, seq + 1) - beg : 1;
+    return min(max(max(a.lens[seq], 0) - ql + (query - beg) + 1, 0), prefix_of(a));
 }
 
 // Queries that no sequence's row tiles cover get zeros and lse = -inf: those past a sequence's first max_q, before
@@ -171,7 +249,7 @@ __device__ __forceinline__ float quarter_max(float x) {
 // Bound by the cache's bytes.
 // ONE: a tile lies in one page (of 32 tokens or more), so its addresses are a scalar base and constants of the
 // lane: about 45 of 270 vector instructions a tile.
-template <int D, int NW, bool ONE>
+template <int D, int NW, bool ONE, int MODE>
 __global__ __launch_bounds__(64 * NW, NW == 4 ? 3 : 1) void k_kv4_decode(DecArgs p) {
     constexpr int J = D / 16;   // columns a lane owns in the O^T tiles: J n + j
     constexpr int KS = D / 32;  // contraction steps of the scores
@@ -185,19 +263,28 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? 3 : 1) void k_kv4_decode(DecArgs
     if (id >= p.work) return blank_rows(p, id - p.work, 64 * NW);
     const int head = id % a.geo.hkv; id /= a.geo.hkv;
     const int rt = id % p.rt; id /= p.rt;
-    const int seq = id % a.b, split = id / a.b;
+    const int seq = MODE == PREFIX ? 0 : id % a.b, split = MODE == PREFIX ? id : id / a.b;
     const int row0 = rt * 16;
-    const Span sp = span_of(a, p.g, seq, row0, 16);
+    Span sp = span_of<MODE>(a, p.g, seq, row0, 16);
     if (row0 >= sp.rows) return;
     const int beg = sp.lo + split * p.chunk, end = min(sp.hi, beg + p.chunk);
-    if (p.splits > 1 && beg >= end) return;  // the joining kernel counts the splits the same way
+    if ((p.splits > 1 || MODE >= PREFIX) && beg >= end) return;  // the joining kernel counts the splits the same way
 
     // this lane's row
     const int row = row0 + n;
     const bool live = row < sp.rows;
     const int qi = live ? row / p.g : 0, qh = live ? head * p.g + row % p.g : 0;
     const int pos = sp.len - sp.qlen + qi;
-    const int vhi = live ? pos + 1 : 0, vlo = first_seen(a.window, pos);
+    int vhi = live ? (MODE == PREFIX ? sp.len : pos + 1) : 0;
+    const int vlo = MODE == OWN ? prefix_of(a) : first_seen(a.window, pos);
+    if constexpr (MODE == PREFIX) {
+        if (some_short(a, 64 * NW)) {
+            vhi = live ? prefix_seen(a, p.g, row) : 0;
+            sp.full_hi = 0;
+        }
+    }
+    // the first token that nobody sees: of the window where the axis has two parts
+    const int stop = MODE == SINKS ? sp.whi : end;
     // q: lane h owns D/4 consecutive columns, KS operands of 8
     v8bf qf[KS];
 #pragma unroll
@@ -226,8 +313,9 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? 3 : 1) void k_kv4_decode(DecArgs
         uint2 vs;
         bool okk;  // the page is one of the cache's (K's lane; V's tokens are the same pages)
     };
-    auto page_at = [&](int t) { return fixed(table, min(t, end - 1) >> lg); };
-    auto fetch = [&](int t0, int pk, int pv, Tile &x) {
+    auto page_at = [&](int t) { return fixed(table, min(t, stop - 1) >> lg); };
+    auto fetch = [&](int at, int pk, int pv, Tile &x) {
+        const int t0 = token_at<MODE>(sp, at);
         x.okk = (uint32_t)pk < (uint64_t)a.geo.pages;
         const bool okv = (uint32_t)pv < (uint64_t)a.geo.pages;
         // codes' and scales' bases of K and of V; then a lane's token in them
@@ -266,13 +354,15 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? 3 : 1) void k_kv4_decode(DecArgs
     const int first = beg + wave * TT;
     Tile even, odd;
     int pk = 0, pv = 0;
-    auto pages_of = [&](int t0) {
+    auto pages_of = [&](int at) {
+        const int t0 = token_at<MODE>(sp, at);
         pk = page_at(ONE ? t0 : t0 + 8 * (n >> 2));
         pv = ONE ? pk : page_at(t0 + 8 * h);
     };
-    auto tile = [&](Tile &cur, Tile &nxt, int t0) {
-        fetch(t0 + NW * TT, pk, pv, nxt);
-        pages_of(t0 + 2 * NW * TT);
+    auto tile = [&](Tile &cur, Tile &nxt, int at) {
+        fetch(at + NW * TT, pk, pv, nxt);
+        pages_of(at + 2 * NW * TT);
+        const int t0 = token_at<MODE>(sp, at);
         if constexpr (D == 64) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) cur.vw[i] >>= 16 * (n & 1);
@@ -290,13 +380,14 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? 3 : 1) void k_kv4_decode(DecArgs
 #pragma unroll
             for (int r = 0; r < 4; ++r) x[4 * s + r] = d[r] * p.c;
         }
-        if (okm != ~0ull || t0 < sp.full_lo || t0 + TT > min(sp.full_hi, end)) {  // some token is masked
+        const bool before = t0 < sp.full_lo && !(MODE == SINKS && t0 + TT <= a.sinks);
+        if (okm != ~0ull || before || t0 + TT > min(sp.full_hi, stop)) {  // some token is masked
             const bool okp = ((okm >> (4 * h)) & 1) != 0;  // of the lane's score tokens' page
-            const int hi = okp ? min(vhi, end) : 0;
+            const int hi = okp ? min(vhi, stop) : 0;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const int tok = t0 + 8 * h + i;
-                x[i] = tok < hi && tok >= vlo ? x[i] : -INFINITY;
+                x[i] = tok < hi && (tok >= vlo || (MODE == SINKS && tok < a.sinks)) ? x[i] : -INFINITY;
             }
         }
         const float mx = fmaxf(m, quarter_max(max3(max3(x[0], x[1], x[2]), max3(x[3], x[4], x[5]), fmaxf(x[6], x[7]))));
@@ -384,7 +475,7 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? 3 : 1) void k_kv4_decode(DecArgs
             o[2] += v.z * f;
             o[3] += v.w * f;
         }
-        if (p.splits == 1) {
+        if (p.splits == 1 && MODE < PREFIX) {
             const int64_t out = (int64_t)(sp.qbeg + (row0 + r) / p.g) * a.hq + head * p.g + (row0 + r) % p.g;
             const float inv = L == 0.0f ? 0.0f : 1.0f / L;
             *reinterpret_cast<uint2 *>(a.o + out * D + col) =
@@ -392,7 +483,7 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? 3 : 1) void k_kv4_decode(DecArgs
             if (a.lse && col == 0) a.lse[out] = L == 0.0f ? -INFINITY : (M + __builtin_amdgcn_logf(L)) * LN2;
         } else {
             // partial row: D sums, then the maximum and the sum of the split
-            float *w = reinterpret_cast<float *>(a.ws) +
+            float *w = p.part +
                        (((((int64_t)seq * p.rt + rt) * a.geo.hkv + head) * p.splits + split) * p.pr + r) * (D + 4);
             *reinterpret_cast<float4 *>(w + col) = make_float4(o[0], o[1], o[2], o[3]);
             if (col == 0) {
@@ -414,7 +505,7 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? 3 : 1) void k_kv4_decode(DecArgs
 // tiles ahead 305 (short runs; 276 once the clock is up, 0.93 PFLOP/s).  Of a busy CU's cycles matrix instructions
 // take 44 %, vector instructions (the exponentials first) 61 % and LDS 34 %: a deeper interleaving within a wave
 // (64 rows, 512 registers) was slower.
-template <int D, int NT>
+template <int D, int NT, int MODE>
 __global__ __launch_bounds__(NT, 2) void k_kv4_chunk(DecArgs p) {
     constexpr int CR = NT / 2;        // rows of the workgroup
     constexpr int KC = D / 8;     // 16-byte pieces of a token's K row
@@ -431,20 +522,29 @@ __global__ __launch_bounds__(NT, 2) void k_kv4_chunk(DecArgs p) {
     if (id >= p.work) return blank_rows(p, id - p.work, NT);
     const int head = id % a.geo.hkv; id /= a.geo.hkv;
     const int rt = p.rt - 1 - id % p.rt; id /= p.rt;  // the longest first
-    const int seq = id % a.b, split = id / a.b;
+    const int seq = MODE == PREFIX ? 0 : id % a.b, split = MODE == PREFIX ? id : id / a.b;
     const int row0 = rt * CR;
-    const Span sp = span_of(a, p.g, seq, row0, CR);
+    const Span sp = span_of<MODE>(a, p.g, seq, row0, CR);
     if (row0 >= sp.rows) return;
     const int beg = sp.lo + split * p.chunk, end = min(sp.hi, beg + p.chunk);
-    if (p.splits > 1 && beg >= end) return;  // the joining kernel counts the splits the same way
+    if ((p.splits > 1 || MODE >= PREFIX) && beg >= end) return;  // the joining kernel counts the splits the same way
+    const int stop = MODE == SINKS ? sp.whi : end;  // the first token that nobody sees
 
     // this lane's row, and what the wave's rows see
     const int row = row0 + wave * 32 + n;
     const bool live = row < sp.rows;
     const int qi = live ? row / p.g : 0, qh = live ? head * p.g + row % p.g : 0;
     const int pos = sp.len - sp.qlen + qi;
-    const int vhi = live ? min(pos + 1, end) : 0, vlo = first_seen(a.window, pos);
-    const Span sw = span_of(a, p.g, seq, row0 + wave * 32, 32);
+    int vhi = live ? min(MODE == PREFIX ? sp.len : pos + 1, stop) : 0;
+    const int vlo = MODE == OWN ? prefix_of(a) : first_seen(a.window, pos);
+    Span sw = span_of<MODE>(a, p.g, seq, row0 + wave * 32, 32);
+    if constexpr (MODE == PREFIX) {
+        if (row0 + wave * 32 >= sp.rows) sw.hi = 0;
+        if (some_short(a, NT)) {
+            vhi = live ? min(prefix_seen(a, p.g, row), stop) : 0;
+            sw.full_hi = 0;
+        }
+    }
     const bool neg = p.c < 0.0f;  // the maximum is taken before the scale: a negative one goes to q
     // A scale of 0 becomes the smallest float: a masked score, -inf here, stays -inf under it (-inf * 0 would be
     // NaN), and a finite one stays below 2^-21, as good as 0.
@@ -473,11 +573,12 @@ __global__ __launch_bounds__(NT, 2) void k_kv4_chunk(DecArgs p) {
     uint32_t kw[2][KD], vw[2][KD], ks[2], vs[2];
     const uint8_t *const headp = a.cache + (int64_t)head * region;
     const int64_t pstride = (int64_t)a.geo.hkv * region;
-    auto page_at = [&](int t) { return fixed(table, min(t, end - 1) >> lg); };
+    auto page_at = [&](int t) { return fixed(table, min(t, stop - 1) >> lg); };
     // pages outside the cache: their tokens' bytes are any page's, and their scores are masked
     bool okk[2];
-    auto fetch = [&](auto set, int t0, int pk, int pv) {
+    auto fetch = [&](auto set, int at, int pk, int pv) {
         constexpr int z = decltype(set)::value;
+        const int t0 = token_at<MODE>(sp, at);
         okk[z] = (uint32_t)pk < (uint64_t)a.geo.pages;
         const bool okv = (uint32_t)pv < (uint64_t)a.geo.pages;
         const uint8_t *kb = headp + (okk[z] ? pk : 0) * pstride, *vb = headp + (okv ? pv : 0) * pstride;
@@ -560,7 +661,8 @@ __global__ __launch_bounds__(NT, 2) void k_kv4_chunk(DecArgs p) {
     using I0 = std::integral_constant<int, 0>;
     using I1 = std::integral_constant<int, 1>;
     int pk = 0, pv = 0;
-    auto pages_of = [&](int t0) {
+    auto pages_of = [&](int at) {
+        const int t0 = token_at<MODE>(sp, at);
         pk = page_at(t0 + kt);
         pv = page_at(t0 + vtok);
     };
@@ -576,7 +678,7 @@ __global__ __launch_bounds__(NT, 2) void k_kv4_chunk(DecArgs p) {
         fetch(I0{}, beg + 2 * CT, pk, pv);
         pages_of(beg + 3 * CT);
     }
-    auto tile = [&](auto buf, int t0, const uint8_t *ck, const uint8_t *cv, uint8_t *nk, uint8_t *nv) {
+    auto tile = [&](auto buf, int at, const uint8_t *ck, const uint8_t *cv, uint8_t *nk, uint8_t *nv) {
         constexpr int b = decltype(buf)::value;
         __syncthreads();  // tile t0 is in buffer b, and nobody reads the other any more
         // the next tile is unpacked whether there is one or not (the fetched bytes are always some page's), so
@@ -586,10 +688,13 @@ __global__ __launch_bounds__(NT, 2) void k_kv4_chunk(DecArgs p) {
             const uint64_t bm = ~__builtin_amdgcn_ballot_w64(okk[b ^ 1]);
             if (lane == 0) bad[b ^ 1][wave] = bm;
             unpack(Set{}, nk, nv);
-            fetch(Set{}, t0 + 3 * CT, pk, pv);
-            pages_of(t0 + 4 * CT);
+            fetch(Set{}, at + 3 * CT, pk, pv);
+            pages_of(at + 4 * CT);
         };
-        if (t0 >= sw.hi || t0 + CT <= sw.lo) {  // the wave's rows see nothing of it
+        const int t0 = token_at<MODE>(sp, at);
+        const bool behind = t0 >= (MODE == SINKS ? sw.whi : sw.hi);
+        const bool ahead = MODE == SINKS ? t0 + CT <= sw.wlo && t0 >= a.sinks : t0 + CT <= sw.lo;
+        if (behind || ahead) {  // the wave's rows see nothing of it
             next();
             return;
         }
@@ -613,7 +718,8 @@ __global__ __launch_bounds__(NT, 2) void k_kv4_chunk(DecArgs p) {
 #pragma unroll
         for (int w = 0; w < TPT; ++w) any |= bad[b][w];
         const bool anybad = __builtin_amdgcn_readfirstlane((int)any | (int)(any >> 32)) != 0;
-        if (anybad || t0 < sw.full_lo || t0 + CT > min(sw.full_hi, end)) {
+        const bool before = t0 < sw.full_lo && !(MODE == SINKS && t0 + CT <= a.sinks);
+        if (anybad || before || t0 + CT > min(sw.full_hi, stop)) {
 #pragma unroll
             for (int u = 0; u < 2; ++u)
 #pragma unroll
@@ -621,7 +727,7 @@ __global__ __launch_bounds__(NT, 2) void k_kv4_chunk(DecArgs p) {
                     const int q = 32 * u + 16 * (r >> 3) + 8 * h + (r & 7), tok = t0 + q;
                     // token q was unpacked by threads TPT q and on, 64 / TPT tokens a wave
                     const bool ok = ((bad[b][q / (64 / TPT)] >> (TPT * (q % (64 / TPT)))) & 1) == 0;
-                    s[u][r] = ok && tok < vhi && tok >= vlo ? s[u][r] : -INFINITY;
+                    s[u][r] = ok && tok < vhi && (tok >= vlo || (MODE == SINKS && tok < a.sinks)) ? s[u][r] : -INFINITY;
                 }
         }
         float mx = m;
@@ -661,7 +767,7 @@ __global__ __launch_bounds__(NT, 2) void k_kv4_chunk(DecArgs p) {
     l += __shfl_xor(l, 32, 64);
     if (!live) return;
     // element r of tile j: column 32 j + 8 (r / 4) + 4 h + r % 4 of row n
-    if (p.splits == 1) {
+    if (p.splits == 1 && MODE < PREFIX) {
         const int64_t out = (int64_t)(sp.qbeg + qi) * a.hq + qh;
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll
@@ -673,7 +779,7 @@ __global__ __launch_bounds__(NT, 2) void k_kv4_chunk(DecArgs p) {
                                bf16_pack2(acc[j][4 * q + 2] * inv, acc[j][4 * q + 3] * inv));
         if (a.lse && h == 0) a.lse[out] = l == 0.0f ? -INFINITY : (m * c + __builtin_amdgcn_logf(l)) * LN2;
     } else {
-        float *w = reinterpret_cast<float *>(a.ws) +
+        float *w = p.part +
                    (((((int64_t)seq * p.rt + rt) * a.geo.hkv + head) * p.splits + split) * p.pr + wave * 32 + n) * (D + 4);
 #pragma unroll
         for (int j = 0; j < DT; ++j)
@@ -691,7 +797,7 @@ __global__ __launch_bounds__(NT, 2) void k_kv4_chunk(DecArgs p) {
 // Joins the splits of a row: D / 4 lanes to a split's columns, so a workgroup has 8 (D = 128) or 16 lane
 // groups; G of them read a row's splits at once (all, or one where there are few splits and many rows).
 // Each group sums its splits in ascending order, then the groups are summed in order.
-template <int D, int G>
+template <int D, int G, int MODE>
 __global__ __launch_bounds__(256) void k_kv4_join(DecArgs p) {
     constexpr int L = D / 4, RW = 256 / L / G;  // RW rows a workgroup
     const Kv4Attn &a = p.a;
@@ -702,18 +808,25 @@ __global__ __launch_bounds__(256) void k_kv4_join(DecArgs p) {
     const int rt = (int)(id % p.rt);
     const int seq = (int)(id / p.rt);
     if (seq >= a.b) return;  // (of a workgroup that joins one row, all or none)
-    const Span sp = span_of(a, p.g, seq, rt * p.tr, p.tr);
+    const Span sp = span_of<MODE>(a, p.g, seq, rt * p.tr, p.tr);
     const int row = rt * p.tr + r;
     if (row >= sp.rows) return;
     const int ns = sp.hi > sp.lo ? (sp.hi - sp.lo + p.chunk - 1) / p.chunk : 0;
     const int64_t SS = (int64_t)p.pr * (D + 4);
-    const float *w = reinterpret_cast<const float *>(a.ws) +
-                     ((((int64_t)seq * p.rt + rt) * a.geo.hkv + head) * p.splits * p.pr + r) * (D + 4);
+    const float *w = p.part + ((((int64_t)seq * p.rt + rt) * a.geo.hkv + head) * p.splits * p.pr + r) * (D + 4);
+    const float *pw = nullptr;  // the shared tokens' partial results of the row
+    const int64_t PS = (int64_t)p.ppr * (D + 4);
+    if constexpr (MODE == OWN) {
+        const int64_t prow = (int64_t)sp.qbeg * p.g + row;
+        pw = p.ppart + ((prow / p.ptr_ * a.geo.hkv + head) * p.psplits * p.ppr + prow % p.ptr_) * (D + 4);
+    }
     float M = -INFINITY, Lsum = 0.0f, o[4] = {0, 0, 0, 0};
+    const int parts = MODE == OWN ? ns + p.psplits : ns;
 #pragma unroll 4
-    for (int s = grp; s < ns; s += G) {
-        const float4 v = *reinterpret_cast<const float4 *>(w + s * SS + lane * 4);
-        const float2 ml = *reinterpret_cast<const float2 *>(w + s * SS + D);
+    for (int s = grp; s < parts; s += G) {
+        const float *ws = MODE == OWN && s >= ns ? pw + (s - ns) * PS : w + s * SS;
+        const float4 v = *reinterpret_cast<const float4 *>(ws + lane * 4);
+        const float2 ml = *reinterpret_cast<const float2 *>(ws + D);
         const float nm = fmaxf(M, ml.x), mu = nm == -INFINITY ? 0.0f : nm;
         const float f0 = __builtin_amdgcn_exp2f(M - mu), f1 = __builtin_amdgcn_exp2f(ml.x - mu);
         M = nm;
@@ -787,12 +900,8 @@ int64_t splits_of(const DecArgs &p, int64_t groups, int64_t span) {
         splits = std::max(splits, std::min({(span + FAR - 1) / FAR, FAR_SPLITS, ((int64_t)1 << 22) / std::max<int64_t>(groups, 1)}));
     return std::max<int64_t>(1, std::min(splits, (span + unit - 1) / unit));
 }
-void plan(const Kv4Attn &a, DecArgs &p) {
-    tiles_of(a.max_q, a.hq / a.geo.hkv, a.geo.d, p);
-    const int64_t groups = (int64_t)a.b * a.geo.hkv * p.rt;
-    int64_t span = (int64_t)a.width << a.geo.page_log2;
-    // a window's span: that of the tile's first to its last query, and the start's rounding down
-    if (a.window) span = std::min<int64_t>(span, (int64_t)a.window + p.tr / p.g + 1 + CT);
+// The rest of a call's plan: `groups` of rows, each over `span` tokens at most.
+void split(DecArgs &p, int64_t groups, int64_t span) {
     int64_t splits = splits_of(p, groups, span);
     p.nw = p.tr == 16 && splits > 1 && wide(groups, span) ? WIDE : 4;
     if (p.nw == WIDE) splits = 1;
@@ -800,7 +909,71 @@ void plan(const Kv4Attn &a, DecArgs &p) {
     const int64_t chunk = ((span + splits - 1) / splits + unit - 1) / unit * unit;
     p.chunk = (int)chunk;
     p.splits = (int)((span + chunk - 1) / chunk);
+    p.work = (int)(groups * p.splits);  // below 2^23
+    p.blanks = 0;
 }
+
+DecArgs args_of(const Kv4Attn &a) {
+    DecArgs p{};
+    p.a = a;
+    p.c = a.scale * LOG2E;
+    p.part = reinterpret_cast<float *>(a.ws);
+    return p;
+}
+
+// Of PREFIX and OWN: the one's results lie behind the other's in the workspace.
+size_t own_ws_bytes(int b, int max_q, int hq, const Kv4Geom &g, int width, int shared) {
+    DecArgs p;
+    tiles_of(max_q, hq / g.hkv, g.d, p);
+    const int64_t groups = (int64_t)b * g.hkv * p.rt, span = (((int64_t)width - shared) << g.page_log2) + TT;
+    return ((size_t)(groups * splits_of(p, groups, span)) * p.pr * (g.d + 4) * 4 + 255) & ~(size_t)255;
+}
+
+template <int MODE>
+hipError_t launch_attend(const DecArgs &p, hipStream_t s) {
+    const Kv4Attn &a = p.a;
+    const dim3 grid((unsigned)(p.work + p.blanks));
+    if (p.tr > 16) {
+        if (p.tr == 256) hipLaunchKernelGGL((k_kv4_chunk<128, 512, MODE>), grid, dim3(512), 0, s, p);
+        else if (a.geo.d == 128) hipLaunchKernelGGL((k_kv4_chunk<128, 256, MODE>), grid, dim3(256), 0, s, p);
+        else hipLaunchKernelGGL((k_kv4_chunk<64, 256, MODE>), grid, dim3(256), 0, s, p);
+    } else {
+#define DECODE(D, NW)                                                                                              \
+    do {                                                                                                           \
+        if (a.geo.page_log2 >= 5) hipLaunchKernelGGL((k_kv4_decode<D, NW, true, MODE>), grid, dim3(64 * NW), 0, s, p); \
+        else hipLaunchKernelGGL((k_kv4_decode<D, NW, false, MODE>), grid, dim3(64 * NW), 0, s, p);                   \
+    } while (0)
+        if (a.geo.d == 128 && p.nw == WIDE) DECODE(128, WIDE);
+        else if (a.geo.d == 128) DECODE(128, 4);
+        else if (p.nw == WIDE) DECODE(64, WIDE);
+        else DECODE(64, 4);
+#undef DECODE
+    }
+    return hipGetLastError();
+}
+
+template <int MODE>
+hipError_t launch_join(const DecArgs &p, hipStream_t s) {
+    const Kv4Attn &a = p.a;
+    const int64_t tiles = (int64_t)a.b * p.rt * a.geo.hkv;
+    // one group a row where a row has no more splits than four groups' turns and the rows fill the device
+    const int parts = p.splits + p.psplits;
+    const int groups = 1024 / a.geo.d, per = (parts <= 4 && tiles * p.pr >= 8192) || tiles * p.pr >= 1 << 22 ? groups : 1;
+    const dim3 jg((unsigned)((tiles * p.pr + per - 1) / per));
+    if (a.geo.d == 128 && per > 1) hipLaunchKernelGGL((k_kv4_join<128, 1, MODE>), jg, dim3(256), 0, s, p);
+    else if (a.geo.d == 128) hipLaunchKernelGGL((k_kv4_join<128, 8, MODE>), jg, dim3(256), 0, s, p);
+    else if (per > 1) hipLaunchKernelGGL((k_kv4_join<64, 1, MODE>), jg, dim3(256), 0, s, p);
+    else hipLaunchKernelGGL((k_kv4_join<64, 16, MODE>), jg, dim3(256), 0, s, p);
+    return hipGetLastError();
+}
+
+template <int MODE>
+hipError_t attend_and_join(const DecArgs &p, hipStream_t s) {
+    const hipError_t e = launch_attend<MODE>(p, s);
+    return e == hipSuccess && p.splits > 1 ? launch_join<MODE>(p, s) : e;
+}
+
+int blanks_of(const Kv4Attn &a) { return a.q_start ? std::max(a.b, std::min(a.nq, 64)) : 0; }
 
 }  // namespace
 
@@ -814,42 +987,40 @@ size_t kv4_attn_ws_bytes(int b, int max_q, int hq, const Kv4Geom &g, int width) 
 }
 
 hipError_t launch_kv4_attn(const Kv4Attn &a, hipStream_t s) {
+    DecArgs p = args_of(a);
+    tiles_of(a.max_q, a.hq / a.geo.hkv, a.geo.d, p);
+    int64_t span = (int64_t)a.width << a.geo.page_log2;
+    // a window's span: that of the tile's first to its last query, and the start's rounding down; and the sinks'
+    const bool sinks = a.window && a.sinks;
+    if (a.window) span = std::min<int64_t>(span, (int64_t)a.window + p.tr / p.g + 1 + CT + (sinks ? (int64_t)a.sinks + CT : 0));
+    split(p, (int64_t)a.b * a.geo.hkv * p.rt, span);
+    p.blanks = blanks_of(a);
+    return sinks ? attend_and_join<SINKS>(p, s) : attend_and_join<PLAIN>(p, s);
+}
+
+size_t kv4_attn_shared_ws_bytes(int64_t nq, int b, int max_q, int hq, const Kv4Geom &g, int width, int shared) {
     DecArgs p;
-    p.a = a;
-    p.c = a.scale * LOG2E;
-    plan(a, p);
-    const int64_t tiles = (int64_t)a.b * p.rt * a.geo.hkv;
-    p.work = (int)(tiles * p.splits);  // below 2^23
-    p.blanks = a.q_start ? std::max(a.b, std::min(a.nq, 64)) : 0;
-    const dim3 grid((unsigned)(p.work + p.blanks));
-    if (p.tr > 16) {
-        if (p.tr == 256) hipLaunchKernelGGL((k_kv4_chunk<128, 512>), grid, dim3(512), 0, s, p);
-        else if (a.geo.d == 128) hipLaunchKernelGGL((k_kv4_chunk<128, 256>), grid, dim3(256), 0, s, p);
-        else hipLaunchKernelGGL((k_kv4_chunk<64, 256>), grid, dim3(256), 0, s, p);
-    } else {
-#define DECODE(D, NW)                                                                                        \
-    do {                                                                                                     \
-        if (a.geo.page_log2 >= 5) hipLaunchKernelGGL((k_kv4_decode<D, NW, true>), grid, dim3(64 * NW), 0, s, p); \
-        else hipLaunchKernelGGL((k_kv4_decode<D, NW, false>), grid, dim3(64 * NW), 0, s, p);                   \
-    } while (0)
-        if (a.geo.d == 128 && p.nw == WIDE) DECODE(128, WIDE);
-        else if (a.geo.d == 128) DECODE(128, 4);
-        else if (p.nw == WIDE) DECODE(64, WIDE);
-        else DECODE(64, 4);
-#undef DECODE
-    }
-    hipError_t e = hipGetLastError();
-    if (e == hipSuccess && p.splits > 1) {
-        // one group a row where a row has no more splits than four groups' turns and the rows fill the device
-        const int groups = 1024 / a.geo.d, per = (p.splits <= 4 && tiles * p.pr >= 8192) || tiles * p.pr >= 1 << 22 ? groups : 1;
-        const dim3 jg((unsigned)((tiles * p.pr + per - 1) / per));
-        if (a.geo.d == 128 && per > 1) hipLaunchKernelGGL((k_kv4_join<128, 1>), jg, dim3(256), 0, s, p);
-        else if (a.geo.d == 128) hipLaunchKernelGGL((k_kv4_join<128, 8>), jg, dim3(256), 0, s, p);
-        else if (per > 1) hipLaunchKernelGGL((k_kv4_join<64, 1>), jg, dim3(256), 0, s, p);
-        else hipLaunchKernelGGL((k_kv4_join<64, 16>), jg, dim3(256), 0, s, p);
-        e = hipGetLastError();
-    }
-    return e;
+    tiles_of((int)nq, hq / g.hkv, g.d, p);
+    const int64_t groups = (int64_t)g.hkv * p.rt, splits = splits_of(p, groups, (int64_t)shared << g.page_log2);
+    return own_ws_bytes(b, max_q, hq, g, width, shared) + (size_t)(groups * splits) * p.pr * (g.d + 4) * 4;
+}
+
+hipError_t launch_kv4_attn_shared(const Kv4Attn &a, hipStream_t s) {
+    DecArgs pre = args_of(a), own = args_of(a);
+    tiles_of(a.nq, a.hq / a.geo.hkv, a.geo.d, pre);
+    split(pre, (int64_t)a.geo.hkv * pre.rt, (int64_t)a.shared << a.geo.page_log2);
+    pre.part = reinterpret_cast<float *>(a.ws + own_ws_bytes(a.b, a.max_q, a.hq, a.geo, a.width, a.shared));
+    hipError_t e = launch_attend<PREFIX>(pre, s);
+    if (e != hipSuccess) return e;
+    tiles_of(a.max_q, a.hq / a.geo.hkv, a.geo.d, own);
+    split(own, (int64_t)a.b * a.geo.hkv * own.rt, (((int64_t)a.width - a.shared) << a.geo.page_log2) + TT);
+    own.blanks = blanks_of(a);
+    own.ptr_ = pre.tr;
+    own.ppr = pre.pr;
+    own.psplits = pre.splits;
+    own.ppart = pre.part;
+    e = launch_attend<OWN>(own, s);
+    return e == hipSuccess ? launch_join<OWN>(own, s) : e;
 }
 
 }  // namespace fp4
