@@ -703,8 +703,12 @@ def kv4_attention(q: torch.Tensor, cache: KV4Cache, pages: torch.Tensor, lens: t
         if ws is None:
             ws = kv4_attention_workspace(q, cache, pages, max_q, shared)
         L, most = lib(), 0x7FFFFFFF
-        f, seen = (L.fp4_kv4_attention_shared, (shared,)) if shared else \
-            (L.fp4_kv4_attention_sinks, (min(window, most), min(sinks, most)))
+        if shared:
+            f, seen = L.fp4_kv4_attention_shared, (shared,)
+        elif sinks and window:
+            f, seen = L.fp4_kv4_attention_sinks, (min(window, most), min(sinks, most))
+        else:
+            f, seen = L.fp4_kv4_attention, (min(window, most),)
         _on_device(q, lambda: _check(f(
             _ptr(q), q.stride(0), q.stride(1), nq, hq, _ptr(q_start), _ptr(lens), b, max_q, _ptr(pages),
             max(pages.stride(0), pages.shape[1]), pages.shape[1], _ptr(cache.data), cache.pages, cache.page, cache.heads, d,
@@ -715,7 +719,7 @@ def kv4_attention(q: torch.Tensor, cache: KV4Cache, pages: torch.Tensor, lens: t
 # --------------------------------------------------------------------------- page tables of the cache
 def _on_device(ref: torch.Tensor, call):
     """call(), which enqueues on ref's device, with that device current."""
-    if ref.get_device() == torch._C._cuda_getDevice():
+    if not torch.cuda.is_initialized() or ref.get_device() == torch._C._cuda_getDevice():
         return call()
     with torch.cuda.device(ref.device):
         return call()
