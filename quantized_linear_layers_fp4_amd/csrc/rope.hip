@@ -10,9 +10,12 @@
 // Each value is read once and written once (backward: x and dy once, dx once): bound by memory.  A lane holds 8 columns,
 // d / 8 lanes a row (rounded up to a power of two, L); a lane group stays with one token and goes through a
 // run of its heads, so that angles and weights are fetched once a run and not once a row.
-// Forward in 64 bits: with the products w cos and w sin made once a run it takes 7 operations a value, which memory
-// hides, no input overflows in its square, and a key's value does not depend on the order of its sum: the fused write
-// puts into the cache what the norm and kv4_write put there one after the other, bit for bit.
+// Keys are made in 64 bits and rounded to fp32 and then to the type, so that their values do not depend on the order of
+// a sum: the fused write puts into the cache what the norm and kv4_write put there one after the other, bit for bit, and a
+// code of the cache next to a border is the right one.  Queries and gradients are made in fp32 (half the
+// instructions), but for rows whose mean square leaves 2^-80 .. 2^120.
+// A layer's forward (8192 tokens of 32 + 8 heads of 128, bf16: 168 MB) takes 36 us, 4.6 TB/s where a large copy reaches
+// 4.8; its gradients (252 MB) 53 and the weights' sums 3; 16384 tokens into the cache (353 MB) 81.
 #include <algorithm>
 
 #include "block8.h"
@@ -22,19 +25,33 @@ namespace fp4 {
 
 namespace {
 
+// Heads of a run of a large call, in bf16 and in fp32.  The angles and weights of a run cost about as much as two rows:
+// a layer's forward (8192 tokens of 40 heads of 128, bf16) takes 45 us with runs of 2, 38 of 4, 36 of 8; the write into the
+// cache (16384 tokens, 32 and 8 heads) 95 of 2, 82 of 4, 86 of 8, whose registers leave two waves.
+constexpr int FWD16 = 8, FWD32 = 4, FILL16 = 4, FILL32 = 2, BWD16 = 4, BWD32 = 2;
 constexpr int BWD_BLOCKS = 1024;  // workgroups of a backward at most: rows of partial weight gradients
 
-// Sum over the L lanes of a group, in each of them.
-template <int L>
-__device__ __forceinline__ double group_sum(double x) {
-#pragma unroll
-    for (int off = L / 2; off > 0; off >>= 1) x += __shfl_xor(x, off, 64);
-    return x;
+// x of another lane of the 16 that a DPP row is.
+template <int CTRL>
+__device__ __forceinline__ float lane_of(float x) {
+    return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), CTRL, 0xF, 0xF, true));
 }
-template <int L>
-__device__ __forceinline__ float group_sum(float x) {
-#pragma unroll
-    for (int off = L / 2; off > 0; off >>= 1) x += __shfl_xor(x, off, 64);
+template <int CTRL>
+__device__ __forceinline__ double lane_of(double x) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, x);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_mov_dpp((int)b, CTRL, 0xF, 0xF, true);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_mov_dpp((int)(b >> 32), CTRL, 0xF, 0xF, true);
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+// Sum over the L lanes of a group, in each of them: neighbours, neighbouring pairs, then mirrored halves of 8 and of 16,
+// whose lanes hold the same by then.
+template <int L, typename T>
+__device__ __forceinline__ T group_sum(T x) {
+    x += lane_of<0xB1>(x);   // quad_perm 1 0 3 2
+    x += lane_of<0x4E>(x);   // quad_perm 2 3 0 1
+    if constexpr (L >= 8) x += lane_of<0x141>(x);   // row_half_mirror
+    if constexpr (L >= 16) x += lane_of<0x140>(x);  // row_mirror
+    if constexpr (L >= 32) x += __shfl_xor(x, 16, 64);
     return x;
 }
 
@@ -98,22 +115,33 @@ __device__ __forceinline__ void partners(const Raw<DT> &r, int from, float (&v)[
     }
 }
 
-template <int DT>
+// PAST: past the caches, which leaves them to the inputs.
+template <int DT, bool PAST>
 __device__ __forceinline__ void store_row(void *y, int64_t elem, const float (&v)[8]) {
-    typedef unsigned int ua4 __attribute__((ext_vector_type(4), aligned(2)));
+    auto put = [](ua_u32x4 w, void *p) {
+        if constexpr (PAST) __builtin_nontemporal_store(w, static_cast<ua_u32x4 *>(p));
+        else *static_cast<ua_u32x4 *>(p) = w;
+    };
     if constexpr (DT == DT_BF16) {
-        *reinterpret_cast<ua4 *>(static_cast<uint16_t *>(y) + elem) =
-            ua4{bf16_pack2(v[0], v[1]), bf16_pack2(v[2], v[3]), bf16_pack2(v[4], v[5]), bf16_pack2(v[6], v[7])};
+        put(ua_u32x4{bf16_pack2(v[0], v[1]), bf16_pack2(v[2], v[3]), bf16_pack2(v[4], v[5]), bf16_pack2(v[6], v[7])},
+            static_cast<uint16_t *>(y) + elem);
     } else {
         float *p = static_cast<float *>(y) + elem;
-        *reinterpret_cast<ua4 *>(p) = ua4{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])};
-        *reinterpret_cast<ua4 *>(p + 4) = ua4{__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7])};
+        put(__builtin_bit_cast(ua_u32x4, v4f{v[0], v[1], v[2], v[3]}), p);
+        put(__builtin_bit_cast(ua_u32x4, v4f{v[4], v[5], v[6], v[7]}), p + 4);
     }
 }
 
-__device__ __forceinline__ float weight_at(const NormRope &a, const void *w, int col) {
-    if (!w) return 1.0f;
-    return a.w_dt == DT_BF16 ? bf16_to_f32(static_cast<const uint16_t *>(w)[col]) : static_cast<const float *>(w)[col];
+// Eight weights from a column on.
+__device__ __forceinline__ void weights_at(const NormRope &a, const void *w, int col, float (&v)[8]) {
+    if (!w) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = 1.0f;
+    } else if (a.w_dt == DT_BF16) {
+        values<DT_BF16>(load_raw<DT_BF16>(w, col, true), v);
+    } else {
+        values<DT_F32>(load_raw<DT_F32>(w, col, true), v);
+    }
 }
 
 // A lane's part of a token: its columns, their partners' place, the angles.  State 0: rows of zeros (a negative
@@ -153,11 +181,13 @@ struct Turn {
             }
         } else {
             const bool second = lane >= half;
-            const float *p = row + (second ? col - a.rot / 2 : col);
+            const float4 *p = reinterpret_cast<const float4 *>(row + (second ? col - a.rot / 2 : col));
+            const float4 x = p[0], y = p[1], z = p[a.rot / 8], w = p[a.rot / 8 + 1];
+            const float cs[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w}, sn[8] = {z.x, z.y, z.z, z.w, w.x, w.y, w.z, w.w};
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                c[i] = p[i];
-                s[i] = second ? p[a.rot / 2 + i] : -p[a.rot / 2 + i];
+                c[i] = cs[i];
+                s[i] = second ? sn[i] : -sn[i];
             }
         }
         if (!in && !zero) {
@@ -165,22 +195,44 @@ struct Turn {
             for (int i = 0; i < 8; ++i) c[i] = s[i] = __uint_as_float(0x7FC00000u);
         }
     }
-
-    __device__ __forceinline__ int partner_col(const NormRope &a, int i) const {
-        if constexpr (IL) return col + (i ^ 1);
-        const int half = a.rot / 2;
-        return col >= a.rot ? col + i : col < half ? col + i + half : col + i - half;
-    }
 };
 
 // A token's weights times its angles: y = r (x u + partner v).
-template <bool IL>
-__device__ __forceinline__ void factors(const NormRope &a, const void *w, const Turn<IL> &t, double (&u)[8], double (&v)[8]) {
+template <bool IL, typename T>
+__device__ __forceinline__ void factors(const NormRope &a, const void *w, const Turn<IL> &t, T (&u)[8], T (&v)[8]) {
+    float own[8], other[8];
+    const int half = a.rot / 2;
+    weights_at(a, w, t.live ? t.col : 0, own);
+    if constexpr (IL) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        u[i] = t.live ? (double)weight_at(a, w, t.col + i) * (double)t.c[i] : 0.0;
-        v[i] = t.live ? (double)weight_at(a, w, t.partner_col(a, i)) * (double)t.s[i] : 0.0;
+        for (int i = 0; i < 8; ++i) other[i] = own[i ^ 1];
+    } else {
+        weights_at(a, w, t.col >= a.rot ? 0 : t.col < half ? t.col + half : t.col - half, other);
     }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {  // (columns past the rotated ones: c = 1, s = 0; past the row's: x = 0)
+        u[i] = (T)own[i] * (T)t.c[i];
+        v[i] = (T)other[i] * (T)t.s[i];
+    }
+}
+
+// 1 / sqrt(mean(x^2) + eps) of the lane group's row.
+template <int L>
+__device__ __forceinline__ double row_scale64(const NormRope &a, const float (&x)[8]) {
+    double ss = 0.0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) ss = __builtin_fma((double)x[i], (double)x[i], ss);
+    return rsqrt64(__builtin_fma(group_sum<L>(ss), a.inv_d, (double)a.eps));
+}
+// The same in fp32; false (for the whole wave) where some row's squares may have left fp32's range.
+template <int L>
+__device__ __forceinline__ bool row_scale32(const NormRope &a, const float (&x)[8], float &r) {
+    float ss = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) ss = __builtin_fmaf(x[i], x[i], ss);
+    const float v = __builtin_fmaf(group_sum<L>(ss), (float)a.inv_d, a.eps);
+    r = __builtin_amdgcn_rsqf(v);
+    return __builtin_amdgcn_ballot_w64(!(v >= 0x1p-80f && v <= 0x1p120f)) == 0;
 }
 
 template <int DT, int L, bool IL>
@@ -189,16 +241,32 @@ __device__ __forceinline__ void turn_row(const NormRope &a, const Raw<DT> &raw, 
     float x[8], p[8];
     values<DT>(raw, x);
     partners<DT, IL>(raw, t.from, p);
-    double r = 1.0;
-    if (a.norm) {
-        double ss = 0.0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) ss = __builtin_fma((double)x[i], (double)x[i], ss);
-        r = rsqrt64(group_sum<L>(ss) / a.d + (double)a.eps);
-    }
+    const double r = a.norm ? row_scale64<L>(a, x) : 1.0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const float f = (float)(r * __builtin_fma((double)p[i], v[i], (double)x[i] * u[i]));
+        y[i] = t.zero ? 0.0f : f;
+    }
+}
+template <int DT, int L, bool IL>
+__device__ __forceinline__ void turn_row(const NormRope &a, const Raw<DT> &raw, const Turn<IL> &t, const float (&u)[8],
+                                         const float (&v)[8], float (&y)[8]) {
+    float x[8], p[8];
+    values<DT>(raw, x);
+    partners<DT, IL>(raw, t.from, p);
+    float r = 1.0f;
+    if (a.norm && !row_scale32<L>(a, x, r)) {
+        const double rd = row_scale64<L>(a, x);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float f = (float)(rd * __builtin_fma((double)p[i], (double)v[i], (double)x[i] * (double)u[i]));
+            y[i] = t.zero ? 0.0f : f;
+        }
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float f = r * __builtin_fmaf(p[i], v[i], x[i] * u[i]);
         y[i] = t.zero ? 0.0f : f;
     }
 }
@@ -206,13 +274,13 @@ __device__ __forceinline__ void turn_row(const NormRope &a, const Raw<DT> &raw, 
 struct FwdArgs {
     NormRope a;
     void *qo, *ko;
-    int hp;               // heads a lane group goes through
     int qc, kc;           // runs of query heads and of key heads
 };
 
 }  // namespace
 
-template <int DT, int L, bool IL>
+// HP: heads of a run, all of whose loads are on their way before the first is used.
+template <int DT, int L, bool IL, int HP>
 __global__ __launch_bounds__(256) void k_norm_rope(FwdArgs f) {
     const NormRope &a = f.a;
     const int lane = threadIdx.x % L;
@@ -220,22 +288,28 @@ __global__ __launch_bounds__(256) void k_norm_rope(FwdArgs f) {
     const int64_t t = (int64_t)(blockIdx.x / (f.qc + f.kc)) * (256 / L) + threadIdx.x / L;
     const int64_t tc = min(t, a.n - 1);  // lanes past the last token stay for the exchanges, with its data
     const bool isq = run < f.qc;
-    const HeadRows &in = isq ? a.q : a.k;
+    const HeadRows in = isq ? a.q : a.k;
     void *out = isq ? f.qo : f.ko;
     run = isq ? run : run - f.qc;
-    const int h0 = run * f.hp, h1 = min(h0 + f.hp, in.heads);
+    const int h0 = run * HP, h1 = min(h0 + HP, in.heads);
+    const int64_t row = tc * in.ts + lane * 8;
+    Raw<DT> raw[HP];
+#pragma unroll
+    for (int j = 0; j < HP; ++j) raw[j] = load_raw<DT>(in.x, row + min(h0 + j, h1 - 1) * in.hs, lane * 8 < a.d);
     const Turn<IL> turn(a, tc, lane, L);
-    double u[8], v[8];
-    factors<IL>(a, in.w, turn, u, v);
-    const int64_t row = tc * in.ts + turn.col;
-    Raw<DT> next = load_raw<DT>(in.x, row + h0 * in.hs, turn.live);
-    for (int h = h0; h < h1; ++h) {
-        const Raw<DT> raw = next;
-        if (h + 1 < h1) next = load_raw<DT>(in.x, row + (h + 1) * in.hs, turn.live);
-        float y[8];
-        turn_row<DT, L, IL>(a, raw, turn, u, v, y);
-        if (turn.live && t < a.n) store_row<DT>(out, (t * in.heads + h) * a.d + turn.col, y);
-    }
+    auto rows = [&](auto zero) {
+        decltype(zero) u[8], v[8];
+        factors<IL>(a, in.w, turn, u, v);
+#pragma unroll
+        for (int j = 0; j < HP; ++j) {
+            if (h0 + j >= h1) break;
+            float y[8];
+            turn_row<DT, L, IL>(a, raw[j], turn, u, v, y);
+            if (turn.live && t < a.n) store_row<DT, (HP > 1)>(out, (t * in.heads + h0 + j) * a.d + turn.col, y);
+        }
+    };
+    if (isq) rows(0.0f);
+    else rows(0.0);
 }
 
 namespace {
@@ -248,13 +322,13 @@ struct FillArgs {
     Kv4Geom g;
     const void *slots;
     bool slots64;
-    int hp, qc, kc;
+    int qc, kc;
 };
 
 }  // namespace
 
 // Queries as above; a key/value head's rows of a token go into the cache as k_kv4_write puts them there.
-template <int DT, int D, bool IL>
+template <int DT, int D, bool IL, int HP>
 __global__ __launch_bounds__(256) void k_norm_rope_kv4(FillArgs f) {
     constexpr int L = D / 8;
     const NormRope &a = f.a;
@@ -263,38 +337,42 @@ __global__ __launch_bounds__(256) void k_norm_rope_kv4(FillArgs f) {
     const int64_t t = (int64_t)(blockIdx.x / (f.qc + f.kc)) * (256 / L) + threadIdx.x / L;
     const int64_t tc = min(t, a.n - 1);
     const bool isq = run < f.qc;
-    const HeadRows &in = isq ? a.q : a.k;
+    const HeadRows in = isq ? a.q : a.k;
     run = isq ? run : run - f.qc;
-    const int h0 = run * f.hp, h1 = min(h0 + f.hp, in.heads);
+    const int h0 = run * HP, h1 = min(h0 + HP, in.heads);
+    const int64_t row = tc * in.ts + lane * 8, vrow = tc * f.v.ts + lane * 8;
+    Raw<DT> raw[HP], vraw[HP];
+#pragma unroll
+    for (int j = 0; j < HP; ++j) raw[j] = load_raw<DT>(in.x, row + min(h0 + j, h1 - 1) * in.hs, true);
+    if (!isq) {
+#pragma unroll
+        for (int j = 0; j < HP; ++j) vraw[j] = load_raw<DT>(f.v.x, vrow + min(h0 + j, h1 - 1) * f.v.hs, true);
+    }
     const Turn<IL> turn(a, tc, lane, L);
-    double u[8], v[8];
-    factors<IL>(a, in.w, turn, u, v);
-    const int64_t row = tc * in.ts + turn.col;
-    Raw<DT> next = load_raw<DT>(in.x, row + h0 * in.hs, true);
     if (isq) {
-        for (int h = h0; h < h1; ++h) {
-            const Raw<DT> raw = next;
-            if (h + 1 < h1) next = load_raw<DT>(in.x, row + (h + 1) * in.hs, true);
+        float u[8], v[8];
+        factors<IL>(a, in.w, turn, u, v);
+#pragma unroll
+        for (int j = 0; j < HP; ++j) {
+            if (h0 + j >= h1) break;
             float y[8];
-            turn_row<DT, L, IL>(a, raw, turn, u, v, y);
-            if (t < a.n) store_row<DT>(f.qo, (t * in.heads + h) * D + turn.col, y);
+            turn_row<DT, L, IL>(a, raw[j], turn, u, v, y);
+            if (t < a.n) store_row<DT, (HP > 1)>(f.qo, (t * in.heads + h0 + j) * D + turn.col, y);
         }
         return;
     }
-    const int64_t vrow = tc * f.v.ts + turn.col;
-    Raw<DT> vnext = load_raw<DT>(f.v.x, vrow + h0 * f.v.hs, true);
     const int64_t slot = f.slots64 ? static_cast<const int64_t *>(f.slots)[tc] : static_cast<const int32_t *>(f.slots)[tc];
     const bool ok = t < a.n && slot >= 0 && slot < f.g.pages << f.g.page_log2;
     const int P = 1 << f.g.page_log2, tok = ok ? (int)(slot & (P - 1)) : 0;
-    for (int h = h0; h < h1; ++h) {
-        const Raw<DT> raw = next, vraw = vnext;
-        if (h + 1 < h1) {
-            next = load_raw<DT>(in.x, row + (h + 1) * in.hs, true);
-            vnext = load_raw<DT>(f.v.x, vrow + (h + 1) * f.v.hs, true);
-        }
+    double u[8], v[8];
+    factors<IL>(a, in.w, turn, u, v);
+#pragma unroll
+    for (int j = 0; j < HP; ++j) {
+        const int h = h0 + j;
+        if (h >= h1) break;
         float y[8], z[8];
-        turn_row<DT, L, IL>(a, raw, turn, u, v, y);
-        values<DT>(vraw, z);
+        turn_row<DT, L, IL>(a, raw[j], turn, u, v, y);
+        values<DT>(vraw[j], z);
         if constexpr (DT == DT_BF16) {  // the key as the norm's own output holds it
 #pragma unroll
             for (int i = 0; i < 8; i += 2) {
@@ -334,66 +412,72 @@ namespace {
 struct BwdArgs {
     NormRope a;
     RopeGrads g;
-    int hp, qc, kc;    // as above
+    int qc, kc;        // as above
     int qb, kb;        // workgroups of queries and of keys
     float *part;       // a row of d sums each, or NULL
 };
 
 }  // namespace
 
-template <int DT, int L, bool IL>
+template <int DT, int L, bool IL, int HP>
 __global__ __launch_bounds__(256) void k_norm_rope_bwd(BwdArgs f) {
     const NormRope &a = f.a;
     const int lane = threadIdx.x % L;
     const bool isq = (int)blockIdx.x < f.qb;
-    const HeadRows &in = isq ? a.q : a.k, &dy = isq ? f.g.dq : f.g.dk;
+    const HeadRows in = isq ? a.q : a.k, dy = isq ? f.g.dq : f.g.dk;
     void *dx = isq ? f.g.dxq : f.g.dxk;
     const int64_t dx_ts = isq ? f.g.dxq_ts : f.g.dxk_ts, dx_hs = isq ? f.g.dxq_hs : f.g.dxk_hs;
     const int runs = isq ? f.qc : f.kc, blocks = isq ? f.qb : f.kb, me = isq ? blockIdx.x : blockIdx.x - f.qb;
     const int64_t items = (a.n + 256 / L - 1) / (256 / L) * runs;
     float dw[8] = {0, 0, 0, 0, 0, 0, 0, 0}, w[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = lane * 8 < a.d ? weight_at(a, in.w, lane * 8 + i) : 0.0f;
+    weights_at(a, in.w, lane * 8 < a.d ? lane * 8 : 0, w);
     for (int64_t item = me; item < items; item += blocks) {
         const int64_t t = item / runs * (256 / L) + threadIdx.x / L, tc = min(t, a.n - 1);
-        const int h0 = (int)(item % runs) * f.hp, h1 = min(h0 + f.hp, in.heads);
+        const int h0 = (int)(item % runs) * HP, h1 = min(h0 + HP, in.heads);
+        const int64_t xr = tc * in.ts + lane * 8, yr = tc * dy.ts + lane * 8;
+        Raw<DT> xw[HP], yw[HP];
+#pragma unroll
+        for (int j = 0; j < HP; ++j) {
+            const int h = min(h0 + j, h1 - 1);
+            xw[j] = load_raw<DT>(in.x, xr + h * in.hs, lane * 8 < a.d);
+            yw[j] = load_raw<DT>(dy.x, yr + h * dy.hs, lane * 8 < a.d);
+        }
         const Turn<IL> turn(a, tc, lane, L);
         const bool off = turn.zero || t >= a.n;
-        const int64_t xr = tc * in.ts + turn.col, yr = tc * dy.ts + turn.col;
-        Raw<DT> xn = load_raw<DT>(in.x, xr + h0 * in.hs, turn.live), yn = load_raw<DT>(dy.x, yr + h0 * dy.hs, turn.live);
-        for (int h = h0; h < h1; ++h) {
-            const Raw<DT> xw = xn, yw = yn;
-            if (h + 1 < h1) {
-                xn = load_raw<DT>(in.x, xr + (h + 1) * in.hs, turn.live);
-                yn = load_raw<DT>(dy.x, yr + (h + 1) * dy.hs, turn.live);
-            }
+#pragma unroll
+        for (int j = 0; j < HP; ++j) {
+            if (h0 + j >= h1) break;
             float x[8], y[8], p[8], g[8];
-            values<DT>(xw, x);
-            values<DT>(yw, y);
-            partners<DT, IL>(yw, turn.from, p);
+            values<DT>(xw[j], x);
+            values<DT>(yw[j], y);
+            partners<DT, IL>(yw[j], turn.from, p);
 #pragma unroll
             for (int i = 0; i < 8; ++i) g[i] = __builtin_fmaf(-turn.s[i], p[i], y[i] * turn.c[i]);
             if (a.norm) {
-                double ss = 0.0;
+                float r, dot = 0.0f;
+                if (row_scale32<L>(a, x, r)) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) ss = __builtin_fma((double)x[i], (double)x[i], ss);
-                const double r = rsqrt64(group_sum<L>(ss) / a.d + (double)a.eps);
-                float dot = 0.0f;
+                    for (int i = 0; i < 8; ++i) x[i] *= r;
+                } else {
+                    const double rd = row_scale64<L>(a, x);
+                    r = (float)rd;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) x[i] = (float)(x[i] * rd);
+                }
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    x[i] = (float)(x[i] * r);
                     const float e = off ? 0.0f : g[i] * x[i];
                     dw[i] += e;
                     g[i] *= w[i];
                     dot = __builtin_fmaf(g[i], x[i], dot);
                 }
-                dot = group_sum<L>(dot) / a.d;
+                dot = group_sum<L>(dot) * (float)a.inv_d;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) g[i] = (float)r * __builtin_fmaf(-x[i], dot, g[i]);
+                for (int i = 0; i < 8; ++i) g[i] = r * __builtin_fmaf(-x[i], dot, g[i]);
             }
 #pragma unroll
             for (int i = 0; i < 8; ++i) g[i] = off ? 0.0f : g[i];
-            if (turn.live && t < a.n) store_row<DT>(dx, t * dx_ts + h * dx_hs + turn.col, g);
+            if (turn.live && t < a.n) store_row<DT, (HP > 1)>(dx, t * dx_ts + (h0 + j) * dx_hs + turn.col, g);
         }
     }
     if (!f.part) return;
@@ -413,23 +497,25 @@ __global__ __launch_bounds__(256) void k_norm_rope_bwd(BwdArgs f) {
             (sums[0][threadIdx.x] + sums[1][threadIdx.x]) + (sums[2][threadIdx.x] + sums[3][threadIdx.x]);
 }
 
-// Partial weight gradients (rows of d) to their sums: 16 rows at once for 16 columns, then the 16 in order.
-__global__ __launch_bounds__(256) void k_rope_dw(const float *__restrict__ part, int qb, int kb, int d, float *dwq, float *dwk) {
+// Partial weight gradients (rows of d) to their sums: 64 rows at once for 16 columns, then the 64 in order.
+__global__ __launch_bounds__(1024) void k_rope_dw(const float *__restrict__ part, int qb, int kb, int d, float *dwq, float *dwk) {
     const bool isq = blockIdx.y == 0;
     float *out = isq ? dwq : dwk;
     if (!out) return;
     const int first = isq ? 0 : qb, rows = isq ? qb : kb;
     const int col = blockIdx.x * 16 + threadIdx.x % 16, r = threadIdx.x / 16;
     float s = 0.0f;
-    if (col < d)
-        for (int i = r; i < rows; i += 16) s += part[(int64_t)(first + i) * d + col];
-    __shared__ float sums[16][17];
+    if (col < d) {
+#pragma unroll 8
+        for (int i = r; i < rows; i += 64) s += part[(int64_t)(first + i) * d + col];
+    }
+    __shared__ float sums[64][17];
     sums[r][threadIdx.x % 16] = s;
     __syncthreads();
     if (r == 0 && col < d) {
         s = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) s += sums[i][threadIdx.x];
+        for (int i = 0; i < 64; ++i) s += sums[i][threadIdx.x];
         out[col] = s;
     }
 }
@@ -457,27 +543,32 @@ namespace {
 
 int lanes_of(int d) { return d <= 32 ? 4 : d <= 64 ? 8 : d <= 128 ? 16 : 32; }
 
-// Heads a lane group goes through: as many as leave 2048 workgroups, 8 at most.
-int heads_a_run(int64_t n, int d, int heads) {
+// One head a run where `most` would leave fewer than 1024 workgroups.
+int heads_a_run(int64_t n, int d, int heads, int most) {
     const int64_t blocks = (n + 256 / lanes_of(d) - 1) / (256 / lanes_of(d));
-    return (int)std::max<int64_t>(1, std::min<int64_t>(8, blocks * heads / 2048));
+    return blocks * heads >= 1024 * most ? most : 1;
 }
 
 }  // namespace
 
-#define ROPE_L(KERNEL, DT, IL, ...)                                                                  \
-    switch (lanes_of(a.d)) {                                                                         \
-        case 4: hipLaunchKernelGGL((KERNEL<DT, 4, IL>), grid, dim3(256), 0, s, __VA_ARGS__); break;  \
-        case 8: hipLaunchKernelGGL((KERNEL<DT, 8, IL>), grid, dim3(256), 0, s, __VA_ARGS__); break;  \
-        case 16: hipLaunchKernelGGL((KERNEL<DT, 16, IL>), grid, dim3(256), 0, s, __VA_ARGS__); break; \
-        default: hipLaunchKernelGGL((KERNEL<DT, 32, IL>), grid, dim3(256), 0, s, __VA_ARGS__);       \
+#define ROPE_L(KERNEL, DT, IL, HP, ...)                                                                  \
+    switch (lanes_of(a.d)) {                                                                             \
+        case 4: hipLaunchKernelGGL((KERNEL<DT, 4, IL, HP>), grid, dim3(256), 0, s, __VA_ARGS__); break;  \
+        case 8: hipLaunchKernelGGL((KERNEL<DT, 8, IL, HP>), grid, dim3(256), 0, s, __VA_ARGS__); break;  \
+        case 16: hipLaunchKernelGGL((KERNEL<DT, 16, IL, HP>), grid, dim3(256), 0, s, __VA_ARGS__); break; \
+        default: hipLaunchKernelGGL((KERNEL<DT, 32, IL, HP>), grid, dim3(256), 0, s, __VA_ARGS__);       \
     }
-#define ROPE_DISPATCH(KERNEL, ...)                                                     \
-    do {                                                                               \
-        if (a.dt == DT_BF16 && a.interleaved) { ROPE_L(KERNEL, DT_BF16, true, __VA_ARGS__) } \
-        else if (a.dt == DT_BF16) { ROPE_L(KERNEL, DT_BF16, false, __VA_ARGS__) }      \
-        else if (a.interleaved) { ROPE_L(KERNEL, DT_F32, true, __VA_ARGS__) }          \
-        else { ROPE_L(KERNEL, DT_F32, false, __VA_ARGS__) }                            \
+#define ROPE_HP(KERNEL, DT, IL, HP, ...)                            \
+    do {                                                            \
+        if (hp == 1) { ROPE_L(KERNEL, DT, IL, 1, __VA_ARGS__) }     \
+        else { ROPE_L(KERNEL, DT, IL, HP, __VA_ARGS__) }            \
+    } while (0)
+#define ROPE_DISPATCH(KERNEL, H16, H32, ...)                                                 \
+    do {                                                                                     \
+        if (a.dt == DT_BF16 && a.interleaved) ROPE_HP(KERNEL, DT_BF16, true, H16, __VA_ARGS__); \
+        else if (a.dt == DT_BF16) ROPE_HP(KERNEL, DT_BF16, false, H16, __VA_ARGS__);         \
+        else if (a.interleaved) ROPE_HP(KERNEL, DT_F32, true, H32, __VA_ARGS__);             \
+        else ROPE_HP(KERNEL, DT_F32, false, H32, __VA_ARGS__);                               \
     } while (0)
 
 hipError_t launch_norm_rope(const NormRope &a, void *qo, void *ko, hipStream_t s) {
@@ -485,12 +576,12 @@ hipError_t launch_norm_rope(const NormRope &a, void *qo, void *ko, hipStream_t s
     f.a = a;
     f.qo = qo;
     f.ko = ko;
-    f.hp = heads_a_run(a.n, a.d, a.q.heads + a.k.heads);
-    f.qc = (a.q.heads + f.hp - 1) / f.hp;
-    f.kc = (a.k.heads + f.hp - 1) / f.hp;
+    const int hp = heads_a_run(a.n, a.d, a.q.heads + a.k.heads, a.dt == DT_BF16 ? FWD16 : FWD32);
+    f.qc = (a.q.heads + hp - 1) / hp;
+    f.kc = (a.k.heads + hp - 1) / hp;
     const int per = 256 / lanes_of(a.d);
     const dim3 grid((unsigned)((a.n + per - 1) / per * (f.qc + f.kc)));
-    ROPE_DISPATCH(k_norm_rope, f);
+    ROPE_DISPATCH(k_norm_rope, FWD16, FWD32, f);
     return hipGetLastError();
 }
 
@@ -504,28 +595,33 @@ hipError_t launch_norm_rope_kv4(const NormRope &a, const HeadRows &v, void *qo, 
     f.g = g;
     f.slots = slots;
     f.slots64 = slots64;
-    f.hp = heads_a_run(a.n, a.d, a.q.heads + 2 * a.k.heads);
-    f.qc = (a.q.heads + f.hp - 1) / f.hp;
-    f.kc = (a.k.heads + f.hp - 1) / f.hp;
+    const int hp = heads_a_run(a.n, a.d, a.q.heads + 2 * a.k.heads, a.dt == DT_BF16 ? FILL16 : FILL32);
+    f.qc = (a.q.heads + hp - 1) / hp;
+    f.kc = (a.k.heads + hp - 1) / hp;
     const int per = 256 / lanes_of(a.d);
     const dim3 grid((unsigned)((a.n + per - 1) / per * (f.qc + f.kc)));
-#define FILL(DT, D)                                                                                                  \
-    do {                                                                                                             \
-        if (a.interleaved) hipLaunchKernelGGL((k_norm_rope_kv4<DT, D, true>), grid, dim3(256), 0, s, f);             \
-        else hipLaunchKernelGGL((k_norm_rope_kv4<DT, D, false>), grid, dim3(256), 0, s, f);                          \
+#define FILL_HP(DT, D, HP)                                                                                \
+    do {                                                                                                  \
+        if (a.interleaved) hipLaunchKernelGGL((k_norm_rope_kv4<DT, D, true, HP>), grid, dim3(256), 0, s, f); \
+        else hipLaunchKernelGGL((k_norm_rope_kv4<DT, D, false, HP>), grid, dim3(256), 0, s, f);           \
     } while (0)
-    if (a.dt == DT_BF16 && a.d == 128) FILL(DT_BF16, 128);
-    else if (a.dt == DT_BF16) FILL(DT_BF16, 64);
-    else if (a.d == 128) FILL(DT_F32, 128);
-    else FILL(DT_F32, 64);
+#define FILL(DT, D, HP)                       \
+    do {                                      \
+        if (hp == 1) FILL_HP(DT, D, 1);       \
+        else FILL_HP(DT, D, HP);              \
+    } while (0)
+    if (a.dt == DT_BF16 && a.d == 128) FILL(DT_BF16, 128, FILL16);
+    else if (a.dt == DT_BF16) FILL(DT_BF16, 64, FILL16);
+    else if (a.d == 128) FILL(DT_F32, 128, FILL32);
+    else FILL(DT_F32, 64, FILL32);
+#undef FILL_HP
 #undef FILL
     return hipGetLastError();
 }
 
-static void bwd_blocks(const NormRope &a, BwdArgs &f) {
-    f.hp = heads_a_run(a.n, a.d, a.q.heads + a.k.heads);
-    f.qc = (a.q.heads + f.hp - 1) / f.hp;
-    f.kc = (a.k.heads + f.hp - 1) / f.hp;
+static void bwd_blocks(const NormRope &a, BwdArgs &f, int hp) {
+    f.qc = (a.q.heads + hp - 1) / hp;
+    f.kc = (a.k.heads + hp - 1) / hp;
     const int per = 256 / lanes_of(a.d);
     const int64_t tb = (a.n + per - 1) / per, qi = tb * f.qc, ki = tb * f.kc;
     const int64_t all = qi + ki, most = std::min<int64_t>(all, BWD_BLOCKS);
@@ -541,12 +637,13 @@ hipError_t launch_norm_rope_bwd(const NormRope &a, const RopeGrads &g, float *ws
     f.a = a;
     f.g = g;
     f.part = a.norm && (g.dwq || g.dwk) ? ws : nullptr;
-    bwd_blocks(a, f);
+    const int hp = heads_a_run(a.n, a.d, a.q.heads + a.k.heads, a.dt == DT_BF16 ? BWD16 : BWD32);
+    bwd_blocks(a, f, hp);
     const dim3 grid((unsigned)(f.qb + f.kb));
-    ROPE_DISPATCH(k_norm_rope_bwd, f);
+    ROPE_DISPATCH(k_norm_rope_bwd, BWD16, BWD32, f);
     hipError_t e = hipGetLastError();
     if (f.part && e == hipSuccess) {
-        hipLaunchKernelGGL(k_rope_dw, dim3((unsigned)((a.d + 15) / 16), 2), dim3(256), 0, s, ws, f.qb, f.kb, a.d, g.dwq, g.dwk);
+        hipLaunchKernelGGL(k_rope_dw, dim3((unsigned)((a.d + 15) / 16), 2), dim3(1024), 0, s, ws, f.qb, f.kb, a.d, g.dwq, g.dwk);
         e = hipGetLastError();
     }
     return e;

@@ -46,6 +46,7 @@ struct NormRope {
     int rot;
     bool interleaved, norm;
     float eps;
+    double inv_d;            // 1 / d
 };
 
 hipError_t launch_rope_table(float *table, int64_t max_pos, int rot, double base, double factor, hipStream_t s);

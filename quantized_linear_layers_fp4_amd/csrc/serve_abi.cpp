@@ -67,6 +67,7 @@ NormRope rows_of(const void *q, int64_t q_ts, int64_t q_hs, int32_t hq, const vo
     a.interleaved = interleaved != 0;
     a.norm = eps >= 0.0f;
     a.eps = eps;
+    a.inv_d = 1.0 / d;
     return a;
 }
 
