@@ -709,45 +709,57 @@ def kv4_attention(q: torch.Tensor, cache: KV4Cache, pages: torch.Tensor, lens: t
             f, seen = L.fp4_kv4_attention_sinks, (min(window, most), min(sinks, most))
         else:
             f, seen = L.fp4_kv4_attention, (min(window, most),)
-        _on_device(q, lambda: _check(f(
-            _ptr(q), q.stride(0), q.stride(1), nq, hq, _ptr(q_start), _ptr(lens), b, max_q, _ptr(pages),
-            max(pages.stride(0), pages.shape[1]), pages.shape[1], _ptr(cache.data), cache.pages, cache.page, cache.heads, d,
-            *seen, d ** -0.5 if scale is None else float(scale), _ptr(o), _ptr(lse), _ptr(ws), ws.numel(), _stream(q))))
+        _on_device(q, f, _ptr(q), q.stride(0), q.stride(1), nq, hq, _ptr(q_start), _ptr(lens), b, max_q, _ptr(pages),
+                   max(pages.stride(0), pages.shape[1]), pages.shape[1], _ptr(cache.data), cache.pages, cache.page,
+                   cache.heads, d, *seen, d ** -0.5 if scale is None else float(scale), _ptr(o), _ptr(lse), _ptr(ws),
+                   ws.numel(), _stream(q))
     return (o, lse) if return_lse else o
 
 
 # --------------------------------------------------------------------------- page tables of the cache
-def _on_device(ref: torch.Tensor, call):
-    """call(), which enqueues on ref's device, with that device current."""
-    if not torch.cuda.is_initialized() or ref.get_device() == torch._C._cuda_getDevice():
-        return call()
-    with torch.cuda.device(ref.device):
-        return call()
+def _on_device(ref: torch.Tensor, call, *args):
+    """call(*args), which enqueues on ref's device, with that device current; raises its status."""
+    if torch.cuda.is_initialized() and ref.get_device() != torch._C._cuda_getDevice():
+        with torch.cuda.device(ref.device):
+            status = call(*args)
+    else:
+        status = call(*args)
+    if status:
+        _check(status)
 
 
 def _int32s(name: str, t: torch.Tensor, shape, ref: torch.Tensor | None = None):
-    if t.dtype != torch.int32 or not t.is_cuda or tuple(t.shape) != shape or not t.is_contiguous():
-        raise ValueError(f"expected {name} as {shape} contiguous int32 on a HIP device")
-    if ref is not None:
-        _same_device(ref, t)
+    if t.dtype is not torch.int32 or not t.is_cuda or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"expected {name} as {tuple(shape)} contiguous int32 on a HIP device")
+    if ref is not None and t.get_device() != ref.get_device():
+        raise ValueError("tensors must be on one device")
 
 
 class KV4Pages:
     """The page tables of b sequences of a cache and its free pages, all int32 on the device: table (b x width, -1
     where there is no page), lens (b, tokens of each), free (pages) and count (1): the first count entries of free
-    are the free pages, the last of them the next to be taken."""
-    __slots__ = ("table", "lens", "free", "count", "pages", "page")
+    are the free pages, the last of them the next to be taken.  The tensors are checked once and stay the object's;
+    their values may be written at any time."""
+    __slots__ = ("_table", "_lens", "_free", "_count", "_page", "_slots", "_args")
 
-    def __init__(self, table, lens, free, count, pages, page):
-        self.table, self.lens, self.free, self.count, self.pages, self.page = table, lens, free, count, pages, page
+    def __init__(self, table, lens, free, count, page):
+        if table.dim() != 2 or free.dim() != 1 or not table.numel() or not free.numel():
+            raise ValueError("expected a table (b, width) and a stack of free pages")
+        (b, width), pages = table.shape, free.shape[0]
+        _int32s("the table", table, (b, width))
+        _int32s("the lengths", lens, (b,), table)
+        _int32s("the free pages", free, (pages,), table)
+        _int32s("their count", count, (1,), table)
+        self._table, self._lens, self._free, self._count, self._page = table, lens, free, count, page
+        self._slots = torch.empty(0, dtype=torch.int64, device=table.device)
+        self._args = (_ptr(table), width, b, width, _ptr(lens), _ptr(free), _ptr(count), pages, page)
 
-    def _check(self):
-        b, width = self.table.shape
-        _int32s("the table", self.table, (b, width))
-        _int32s("the lengths", self.lens, (b,), self.table)
-        _int32s("the free pages", self.free, (self.pages,), self.table)
-        _int32s("their count", self.count, (1,), self.table)
-        return b, width
+    table = property(lambda self: self._table)
+    lens = property(lambda self: self._lens)
+    free = property(lambda self: self._free)
+    count = property(lambda self: self._count)
+    pages = property(lambda self: self._args[7])
+    page = property(lambda self: self._page)
 
 
 def kv4_page_tables(b: int, width: int, pages: int, page: int, device="cuda") -> KV4Pages:
@@ -757,7 +769,7 @@ def kv4_page_tables(b: int, width: int, pages: int, page: int, device="cuda") ->
         raise Fp4Error(f"no page tables of {b} sequences of {width} pages over {pages} pages of {page} tokens")
     i32 = dict(dtype=torch.int32, device=device)
     return KV4Pages(torch.full((b, width), -1, **i32), torch.zeros(b, **i32), torch.arange(pages - 1, -1, -1, **i32),
-                    torch.full((1,), pages, **i32), pages, page)
+                    torch.full((1,), pages, **i32), page)
 
 
 def kv4_extend(tables: KV4Pages, new: torch.Tensor | None = None, n: int | None = None):
@@ -766,23 +778,24 @@ def kv4_extend(tables: KV4Pages, new: torch.Tensor | None = None, n: int | None 
     int32 for n tokens (-1 behind the last), q_start int32 b + 1; q_start[i+1] - q_start[i] is what sequence i got:
     new[i], or 0 where its row, the free pages or n did not suffice.  Without n, token i is sequence i's only one:
     (slots, positions), -1 where it got none (new[i] = 0: none; above 1 counts as 1)."""
-    b, width = tables._check()
-    if new is None and n is not None:
-        raise ValueError("n tokens need new")
+    lens = tables._lens
+    b = lens.shape[0]
     if new is not None:
-        _int32s("the new tokens", new, (b,), tables.table)
-    if n is not None and n < 0:
-        raise ValueError(f"{n} tokens")
-    dev, L = tables.table.device, lib()
-    m = b if n is None else n
-    slots = torch.empty(m, dtype=torch.int64, device=dev)
-    pos = torch.empty(m, dtype=torch.int32, device=dev)
-    q_start = None if n is None else torch.empty(b + 1, dtype=torch.int32, device=dev)
-    need = 0 if n is None else L.fp4_kv4_extend_workspace_bytes(b, n)
-    ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-    _on_device(tables.table, lambda: _check(L.fp4_kv4_extend(
-        _ptr(tables.table), width, b, width, _ptr(tables.lens), _ptr(tables.free), _ptr(tables.count), tables.pages, tables.page,
-        _ptr(new), m, _ptr(slots), _ptr(pos), _ptr(q_start), _ptr(ws), need, _stream(tables.table))))
+        _int32s("the new tokens", new, (b,), lens)
+    elif n is not None:
+        raise ValueError("n tokens need new")
+    L = lib()
+    if n is None:
+        m, q_start, need, ws = b, None, 0, None
+    else:
+        if n < 0:
+            raise ValueError(f"{n} tokens")
+        m, q_start = n, lens.new_empty(b + 1)
+        need = L.fp4_kv4_extend_workspace_bytes(b, n)
+        ws = lens.new_empty(need // 4) if need else None
+    slots, pos = tables._slots.new_empty(m), lens.new_empty(m)
+    _on_device(lens, L.fp4_kv4_extend, *tables._args, _ptr(new), m, slots.data_ptr(), pos.data_ptr(), _ptr(q_start), _ptr(ws),
+               need, _stream(lens))
     return (slots, pos) if n is None else (slots, pos, q_start)
 
 
@@ -790,16 +803,14 @@ def kv4_release(tables: KV4Pages, keep: torch.Tensor | None = None, window: int 
     """Cut sequence i to its first keep[i] tokens (int32, b; None: all stay; 0 ends it) and give back the pages past them,
     and with a window those that no later query sees through it beside the first `sinks` tokens.  The first
     `shared` columns stay.  What is given back first is taken first by the next kv4_extend."""
-    b, width = tables._check()
+    lens = tables._lens
     if keep is not None:
-        _int32s("the lengths to keep", keep, (b,), tables.table)
-    L = lib()
-    need = L.fp4_kv4_release_workspace_bytes(b, width)
-    ws = torch.empty(need, dtype=torch.uint8, device=tables.table.device) if need else None
-    _on_device(tables.table, lambda: _check(L.fp4_kv4_release(
-        _ptr(tables.table), width, b, width, _ptr(tables.lens), _ptr(tables.free), _ptr(tables.count), tables.pages, tables.page,
-        _ptr(keep), min(window, 0x7FFFFFFF), min(sinks, 0x7FFFFFFF), min(shared, 0x7FFFFFFF), _ptr(ws), need,
-        _stream(tables.table))))
+        _int32s("the lengths to keep", keep, lens.shape, lens)
+    L, most = lib(), 0x7FFFFFFF
+    need = L.fp4_kv4_release_workspace_bytes(*tables._args[2:4])
+    ws = lens.new_empty(need // 4) if need else None
+    _on_device(lens, L.fp4_kv4_release, *tables._args, _ptr(keep), min(window, most), min(sinks, most), min(shared, most),
+               _ptr(ws), need, _stream(lens))
 
 
 # --------------------------------------------------------------------------- norm of queries and keys, rotation
@@ -808,56 +819,66 @@ def rope_table(max_pos: int, rot: int, base: float = 10000.0, factor: float = 1.
     t = torch.empty(max_pos, rot, dtype=torch.float32, device=device)
     if not t.is_cuda:
         raise ValueError("expected a HIP device")
-    _on_device(t, lambda: _check(lib().fp4_rope_table(_ptr(t), max_pos, rot, float(base), float(factor), _stream(t))))
+    _on_device(t, lib().fp4_rope_table, _ptr(t), max_pos, rot, float(base), float(factor), _stream(t))
     return t
 
 
-def _heads_like(name: str, t: torch.Tensor, n: int, d: int, ref: torch.Tensor):
-    if not t.is_cuda or t.dim() != 3 or t.shape[0] != n or t.shape[2] != d or (d > 1 and t.stride(2) != 1):
+def _head_args(name: str, t: torch.Tensor, ref: torch.Tensor, n: int, d: int):
+    """C arguments (pointer, token and head strides) of t as n x heads x d like ref, and the heads."""
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or shape[0] != n or shape[2] != d or stride[2] != 1 or not t.is_cuda:
         raise ValueError(f"expected {name} as ({n}, heads, {d}) on a HIP device, the last dimension contiguous")
-    if t.dtype != ref.dtype:
+    if t.dtype is not ref.dtype:
         raise TypeError(f"{name} is {t.dtype}, expected {ref.dtype}")
-    _same_device(ref, t)
+    if t.get_device() != ref.get_device():
+        raise ValueError("tensors must be on one device")
+    return (t.data_ptr(), stride[0], stride[1]), shape[1]
+
+
+_NO_HEADS = ((None, 0, 0), 0)
 
 
 def _rope_args(q, k, table, positions, q_weight, k_weight, eps):
-    """Checks what the calls over rows of heads share; (n, d, C arguments from the weights to rot)."""
+    """Checks what the calls over rows of heads share: (n, d, q's and k's arguments, those from the weights to rot)."""
     if q.dim() != 3:
         raise ValueError("expected queries (n, heads, d)")
     n, _, d = q.shape
-    _heads_like("q", q, n, d, q)
-    if k is not None:
-        _heads_like("k", k, n, d, q)
-    elif k_weight is not None:
-        raise ValueError("weights without keys")
-    w = [t for t in (q_weight, k_weight) if t is not None]
-    for t in w:
-        if not t.is_cuda or t.shape != (d,) or not t.is_contiguous():
-            raise ValueError(f"expected {d} contiguous weights on a HIP device")
-        if t.dtype != w[0].dtype:
+    qa = _head_args("q", q, q, n, d)
+    ka = _NO_HEADS if k is None else _head_args("k", k, q, n, d)
+    if qa[1] == 0:
+        raise ValueError("no query heads")
+    wdt = FP4_F32
+    if q_weight is not None or k_weight is not None:
+        if eps is None:
+            raise ValueError("weights without a norm")
+        if k is None and k_weight is not None:
+            raise ValueError("weights without keys")
+        for w in (q_weight, k_weight):
+            if w is None:
+                continue
+            if not w.is_cuda or w.shape != (d,) or not w.is_contiguous():
+                raise ValueError(f"expected {d} contiguous weights on a HIP device")
+            if w.get_device() != q.get_device():
+                raise ValueError("tensors must be on one device")
+            wdt = _dt(w)
+        if q_weight is not None and k_weight is not None and q_weight.dtype is not k_weight.dtype:
             raise TypeError("the weights must share a dtype")
-        _same_device(q, t)
-    if w and eps is None:
-        raise ValueError("weights without a norm")
     if eps is not None and not eps >= 0:
         raise ValueError(f"eps {eps}")
     rot = max_pos = 0
     if table is not None:
-        if table.dtype != torch.float32 or not table.is_cuda or table.dim() != 2 or not table.is_contiguous():
+        if table.dtype is not torch.float32 or not table.is_cuda or table.dim() != 2 or not table.is_contiguous():
             raise ValueError("expected an fp32 table (max_pos, rot) on a HIP device")
         if positions is None:
             raise ValueError("a table without positions")
         _int32s("the positions", positions, (n,), q)
-        _same_device(q, table)
+        if table.get_device() != q.get_device():
+            raise ValueError("tensors must be on one device")
         max_pos, rot = table.shape
         if rot < 16:
             raise ValueError(f"a rotation of {rot} columns")
-    return n, d, (_ptr(q_weight), _ptr(k_weight), _dt(w[0]) if w else FP4_F32, -1.0 if eps is None else float(eps),
-                  _ptr(positions) if rot else None, _ptr(table), max_pos, rot)
-
-
-def _head_args(t: torch.Tensor | None):
-    return (None, 0, 0) if t is None else (t.data_ptr(), t.stride(0), t.stride(1))
+    return n, d, qa, ka, (_ptr(q_weight), _ptr(k_weight), wdt, -1.0 if eps is None else float(eps),
+                          positions.data_ptr() if rot else None, _ptr(table), max_pos, rot)
 
 
 def qk_norm_rope(q: torch.Tensor, k: torch.Tensor | None, table: torch.Tensor | None = None,
@@ -867,15 +888,12 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor | None, table: torch.Tensor | 
     rotation of the first columns by table (rope_table's) at positions (int32, n): dense (q, k).  eps None: no norm; table
     None: no rotation.  Pairs are (i, i + rot / 2), or (2 i, 2 i + 1) if interleaved.  A negative position's rows
     are zeros; one past the table makes the rotated columns NaN."""
-    n, d, args = _rope_args(q, k, table, positions, q_weight, k_weight, eps)
-    qo = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    ko = None if k is None else torch.empty(k.shape, dtype=k.dtype, device=k.device)
-    if n and q.shape[1]:
-        _on_device(q, lambda: _check(lib().fp4_qk_norm_rope(
-            *_head_args(q), q.shape[1], *_head_args(k), 0 if k is None else k.shape[1], n, d, _dt(q), *args, int(interleaved),
-            _ptr(qo), _ptr(ko), _stream(q))))
-    elif n:
-        raise ValueError("no query heads")
+    n, d, (qp, hq), (kp, hkv), args = _rope_args(q, k, table, positions, q_weight, k_weight, eps)
+    qo = torch.empty_like(q, memory_format=torch.contiguous_format)
+    ko = None if k is None else torch.empty_like(k, memory_format=torch.contiguous_format)
+    if n:
+        _on_device(q, lib().fp4_qk_norm_rope, *qp, hq, *kp, hkv, n, d, _dt(q), *args, int(interleaved), qo.data_ptr(), _ptr(ko),
+                   _stream(q))
     return qo, ko
 
 
@@ -886,38 +904,34 @@ def qk_norm_rope_backward(dq: torch.Tensor, dk: torch.Tensor | None, q: torch.Te
     """Gradients (of q, of k, of q_weight, of k_weight) of qk_norm_rope from those of its outputs and its inputs; the weights'
     in fp32 (None where there is no weight).  out: (tensor or None, tensor or None) for the first two, views into the
     fused projection's gradient for one."""
-    n, d, args = _rope_args(q, k, table, positions, q_weight, k_weight, eps)
-    _heads_like("dq", dq, n, d, q)
+    n, d, (qp, hq), (kp, hkv), args = _rope_args(q, k, table, positions, q_weight, k_weight, eps)
     if (dk is None) != (k is None):
         raise ValueError("keys and their gradient go together")
-    if k is not None:
-        _heads_like("dk", dk, n, d, q)
-        if dk.shape != k.shape:
-            raise ValueError("dk is not like k")
-    if dq.shape != q.shape:
-        raise ValueError("dq is not like q")
     gq, gk = out if out is not None else (None, None)
     if gq is None:
-        gq = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        gq = torch.empty_like(q, memory_format=torch.contiguous_format)
     if gk is None and k is not None:
-        gk = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-    for x, g in ((q, gq), (k, gk)):
-        if g is not None:
-            _heads_like("out", g, n, d, q)
-            if x is None or g.shape != x.shape:
-                raise ValueError("out is not like the inputs")
-    wq, wk = (None if w is None else torch.empty(d, dtype=torch.float32, device=q.device) for w in (q_weight, k_weight))
-    if n == 0:
+        gk = torch.empty_like(k, memory_format=torch.contiguous_format)
+    elif k is None and gk is not None:
+        raise ValueError("a place for a gradient without keys")
+    (dqp, h0), (gqp, h1) = _head_args("dq", dq, q, n, d), _head_args("out", gq, q, n, d)
+    (dkp, h2), (gkp, h3) = (_NO_HEADS, _NO_HEADS) if k is None else (_head_args("dk", dk, q, n, d), _head_args("out", gk, q, n, d))
+    if h0 != hq or h1 != hq or h2 != hkv or h3 != hkv:
+        raise ValueError("gradients are not like the inputs")
+    wq = wk = ws = None
+    need = 0
+    if q_weight is not None or k_weight is not None:
+        wq, wk = torch.empty(2, d, dtype=torch.float32, device=q.device).unbind(0)
+        wq, wk = wq if q_weight is not None else None, wk if k_weight is not None else None
+        need = lib().fp4_qk_norm_rope_backward_workspace_bytes(d)
+        ws = torch.empty(need, dtype=torch.uint8, device=q.device)
+    if n:
+        _on_device(q, lib().fp4_qk_norm_rope_backward, *dqp, *dkp, *qp, hq, *kp, hkv, n, d, _dt(q), *args, int(interleaved), *gqp,
+                   *gkp, _ptr(wq), _ptr(wk), _ptr(ws), need, _stream(q))
+    else:
         for w in (wq, wk):
             if w is not None:
                 w.zero_()
-        return gq, gk, wq, wk
-    L = lib()
-    need = L.fp4_qk_norm_rope_backward_workspace_bytes(d) if wq is not None or wk is not None else 0
-    ws = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
-    _on_device(q, lambda: _check(L.fp4_qk_norm_rope_backward(
-        *_head_args(dq), *_head_args(dk), *_head_args(q), q.shape[1], *_head_args(k), 0 if k is None else k.shape[1], n, d,
-        _dt(q), *args, int(interleaved), *_head_args(gq), *_head_args(gk), _ptr(wq), _ptr(wk), _ptr(ws), need, _stream(q))))
     return gq, gk, wq, wk
 
 
@@ -927,15 +941,14 @@ def kv4_norm_rope(cache: KV4Cache, q: torch.Tensor, k: torch.Tensor, v: torch.Te
                   interleaved: bool = False) -> torch.Tensor:
     """qk_norm_rope, of which k goes with v (n x heads x d) to the cache's slots (as kv4_write takes them) in the same
     launch: returns q."""
-    n, d, args = _rope_args(q, k, table, positions, q_weight, k_weight, eps)
-    _heads_like("v", v, n, d, q)
-    if k.shape != v.shape or k.shape[1:] != (cache.heads, cache.d):
+    n, d, (qp, hq), (kp, hkv), args = _rope_args(q, k, table, positions, q_weight, k_weight, eps)
+    vp, hv = _head_args("v", v, q, n, d)
+    if hkv != cache.heads or hv != hkv or d != cache.d:
         raise ValueError(f"expected keys and values (n, {cache.heads}, {cache.d})")
     sb = _slot_bytes(slots, n)
     _same_device(q, cache.data, slots)
-    qo = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    qo = torch.empty_like(q, memory_format=torch.contiguous_format)
     if n:
-        _on_device(q, lambda: _check(lib().fp4_kv4_norm_rope(
-            _ptr(cache.data), cache.pages, cache.page, *_head_args(q), q.shape[1], *_head_args(k), *_head_args(v), cache.heads, n, d,
-            _dt(q), _ptr(slots), sb, *args, int(interleaved), _ptr(qo), _stream(q))))
+        _on_device(q, lib().fp4_kv4_norm_rope, cache.data.data_ptr(), cache.pages, cache.page, *qp, hq, *kp, *vp, hkv, n, d,
+                   _dt(q), slots.data_ptr(), sb, *args, int(interleaved), qo.data_ptr(), _stream(q))
     return qo
