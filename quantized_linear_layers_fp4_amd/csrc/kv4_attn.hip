@@ -692,9 +692,9 @@ __global__ __launch_bounds__(NT, 2) void k_kv4_chunk(DecArgs p) {
             pages_of(at + 4 * CT);
         };
         const int t0 = token_at<MODE>(sp, at);
-        const bool behind = t0 >= (MODE == SINKS ? sw.whi : sw.hi);
-        const bool ahead = MODE == SINKS ? t0 + CT <= sw.wlo && t0 >= a.sinks : t0 + CT <= sw.lo;
-        if (behind || ahead) {  // the wave's rows see nothing of it
+        // (named truth values here cost 20 registers and spills)
+        if (t0 >= (MODE == SINKS ? sw.whi : sw.hi) ||
+            (t0 + CT <= (MODE == SINKS ? sw.wlo : sw.lo) && (MODE != SINKS || t0 >= a.sinks))) {  // the wave's rows see nothing of it
             next();
             return;
         }
