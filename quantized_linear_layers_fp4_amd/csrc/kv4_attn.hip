@@ -44,7 +44,8 @@ constexpr float LOG2E = 1.44269504088896340736f;
 //   PREFIX  the first a.shared pages of row 0 of the table, for the queries of all sequences at once: rows are those of one
 //           long sequence, and more rows a tile read the bytes once
 //   OWN     a sequence's after those
-// PREFIX and OWN leave partial results, which one join brings together.
+// PREFIX leaves partial results; OWN takes them in at its end, or, where its own tokens are split too, leaves them to the
+// join, which brings both together.
 enum : int { PLAIN, SINKS, PREFIX, OWN };
 
 struct DecArgs {
@@ -58,7 +59,7 @@ struct DecArgs {
     int work, blanks; // workgroups that attend; those after them, for the queries of no row tile
     float c;          // scale * log2(e)
     float *part;      // partial results
-    // of the join of OWN: PREFIX's tile rows, rows a partial holds, splits and partial results
+    // of OWN: PREFIX's tile rows, rows a partial holds, splits and partial results
     int ptr_, ppr, psplits;
     const float *ppart;
 };
@@ -148,6 +149,11 @@ __device__ __forceinline__ int owner_of(const Kv4Attn &a, int query) {
     }
     if (lo == 0 || lo > a.b || query - query_at(a, lo - 1) >= a.max_q) return -1;
     return lo - 1;
+}
+
+// OWN: PREFIX's first partial result of a row of the call's; the next ones are ppr * (d + 4) floats on.
+__device__ __forceinline__ const float *prefix_part(const DecArgs &p, int head, int64_t row) {
+    return p.ppart + ((row / p.ptr_ * p.a.geo.hkv + head) * p.psplits * p.ppr + row % p.ptr_) * (p.a.geo.d + 4);
 }
 
 // PREFIX: whether some sequence has queries that do not see all shared tokens (all threads of the workgroup call it).
@@ -268,7 +274,7 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? 3 : 1) void k_kv4_decode(DecArgs
     Span sp = span_of<MODE>(a, p.g, seq, row0, 16);
     if (row0 >= sp.rows) return;
     const int beg = sp.lo + split * p.chunk, end = min(sp.hi, beg + p.chunk);
-    if ((p.splits > 1 || MODE >= PREFIX) && beg >= end) return;  // the joining kernel counts the splits the same way
+    if ((p.splits > 1 || MODE == PREFIX) && beg >= end) return;  // the joining kernel counts the splits the same way
 
     // this lane's row
     const int row = row0 + n;
@@ -440,6 +446,35 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? 3 : 1) void k_kv4_decode(DecArgs
         }
     }
 
+    if constexpr (MODE == OWN) {
+        // the shared tokens' partial results, by turns of the waves: columns (4 h + r) J .. + J - 1 of the row, as acc holds them
+        const float *w = prefix_part(p, head, (int64_t)sp.qbeg * p.g + row) + 4 * h * J;
+        if (p.splits == 1 && live) {
+#pragma unroll 2
+            for (int s = wave; s < p.psplits; s += NW) {
+                const float *ws = w + (int64_t)s * p.ppr * (D + 4);
+                const float2 ml = *reinterpret_cast<const float2 *>(ws + D - 4 * h * J);
+                float4 v[J];
+#pragma unroll
+                for (int i = 0; i < J; ++i) v[i] = *reinterpret_cast<const float4 *>(ws + 4 * i);
+                const float nm = fmaxf(m, ml.x), mu = nm == -INFINITY ? 0.0f : nm;
+                const float f0 = __builtin_amdgcn_exp2f(m - mu), f1 = __builtin_amdgcn_exp2f(ml.x - mu);
+                m = nm;
+                l = l * f0 + (h == 0 ? ml.y * f1 : 0.0f);
+                // column c of the lane's 4 J: element c / J of tile c % J
+#pragma unroll
+                for (int i = 0; i < J; ++i) {
+                    const float x[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        const int c = 4 * i + u;
+                        acc[c % J][c / J] = acc[c % J][c / J] * f0 + x[u] * f1;
+                    }
+                }
+            }
+        }
+    }
+
     // the waves join: maxima, then sums and outputs over the common maximum, in wave order
     __shared__ float sm[NW][16], sl_[NW][16];
     __shared__ __attribute__((aligned(16))) float so[NW][16][D + 4];
@@ -475,7 +510,7 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? 3 : 1) void k_kv4_decode(DecArgs
             o[2] += v.z * f;
             o[3] += v.w * f;
         }
-        if (p.splits == 1 && MODE < PREFIX) {
+        if (p.splits == 1 && MODE != PREFIX) {
             const int64_t out = (int64_t)(sp.qbeg + (row0 + r) / p.g) * a.hq + head * p.g + (row0 + r) % p.g;
             const float inv = L == 0.0f ? 0.0f : 1.0f / L;
             *reinterpret_cast<uint2 *>(a.o + out * D + col) =
@@ -527,7 +562,7 @@ __global__ __launch_bounds__(NT, 2) void k_kv4_chunk(DecArgs p) {
     const Span sp = span_of<MODE>(a, p.g, seq, row0, CR);
     if (row0 >= sp.rows) return;
     const int beg = sp.lo + split * p.chunk, end = min(sp.hi, beg + p.chunk);
-    if ((p.splits > 1 || MODE >= PREFIX) && beg >= end) return;  // the joining kernel counts the splits the same way
+    if ((p.splits > 1 || MODE == PREFIX) && beg >= end) return;  // the joining kernel counts the splits the same way
     const int stop = MODE == SINKS ? sp.whi : end;  // the first token that nobody sees
 
     // this lane's row, and what the wave's rows see
@@ -766,8 +801,30 @@ __global__ __launch_bounds__(NT, 2) void k_kv4_chunk(DecArgs p) {
     }
     l += __shfl_xor(l, 32, 64);
     if (!live) return;
+    float ms = m == -INFINITY ? m : m * c;  // of the scaled scores
+    if constexpr (MODE == OWN) {
+        const float *w = prefix_part(p, head, (int64_t)sp.qbeg * p.g + row);
+        if (p.splits == 1) {
+            for (int s = 0; s < p.psplits; ++s, w += (int64_t)p.ppr * (D + 4)) {
+                const float2 ml = *reinterpret_cast<const float2 *>(w + D);
+                const float nm = fmaxf(ms, ml.x), mu = nm == -INFINITY ? 0.0f : nm;
+                const float f0 = __builtin_amdgcn_exp2f(ms - mu), f1 = __builtin_amdgcn_exp2f(ml.x - mu);
+                ms = nm;
+                l = l * f0 + ml.y * f1;
+#pragma unroll
+                for (int j = 0; j < DT; ++j)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const float4 v = *reinterpret_cast<const float4 *>(w + 32 * j + 8 * q + 4 * h);
+                        const float x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) acc[j][4 * q + u] = acc[j][4 * q + u] * f0 + x[u] * f1;
+                    }
+            }
+        }
+    }
     // element r of tile j: column 32 j + 8 (r / 4) + 4 h + r % 4 of row n
-    if (p.splits == 1 && MODE < PREFIX) {
+    if (p.splits == 1 && MODE != PREFIX) {
         const int64_t out = (int64_t)(sp.qbeg + qi) * a.hq + qh;
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll
@@ -777,7 +834,7 @@ __global__ __launch_bounds__(NT, 2) void k_kv4_chunk(DecArgs p) {
                 *reinterpret_cast<uint2 *>(a.o + out * D + 32 * j + 8 * q + 4 * h) =
                     make_uint2(bf16_pack2(acc[j][4 * q] * inv, acc[j][4 * q + 1] * inv),
                                bf16_pack2(acc[j][4 * q + 2] * inv, acc[j][4 * q + 3] * inv));
-        if (a.lse && h == 0) a.lse[out] = l == 0.0f ? -INFINITY : (m * c + __builtin_amdgcn_logf(l)) * LN2;
+        if (a.lse && h == 0) a.lse[out] = l == 0.0f ? -INFINITY : (ms + __builtin_amdgcn_logf(l)) * LN2;
     } else {
         float *w = p.part +
                    (((((int64_t)seq * p.rt + rt) * a.geo.hkv + head) * p.splits + split) * p.pr + wave * 32 + n) * (D + 4);
@@ -788,7 +845,7 @@ __global__ __launch_bounds__(NT, 2) void k_kv4_chunk(DecArgs p) {
                 *reinterpret_cast<float4 *>(w + 32 * j + 8 * q + 4 * h) =
                     make_float4(acc[j][4 * q], acc[j][4 * q + 1], acc[j][4 * q + 2], acc[j][4 * q + 3]);
         if (h == 0) {
-            w[D] = m == -INFINITY ? m : m * c;
+            w[D] = ms;
             w[D + 1] = l;
         }
     }
@@ -817,8 +874,7 @@ __global__ __launch_bounds__(256) void k_kv4_join(DecArgs p) {
     const float *pw = nullptr;  // the shared tokens' partial results of the row
     const int64_t PS = (int64_t)p.ppr * (D + 4);
     if constexpr (MODE == OWN) {
-        const int64_t prow = (int64_t)sp.qbeg * p.g + row;
-        pw = p.ppart + ((prow / p.ptr_ * a.geo.hkv + head) * p.psplits * p.ppr + prow % p.ptr_) * (D + 4);
+        pw = prefix_part(p, head, (int64_t)sp.qbeg * p.g + row);
     }
     float M = -INFINITY, Lsum = 0.0f, o[4] = {0, 0, 0, 0};
     const int parts = MODE == OWN ? ns + p.psplits : ns;
@@ -900,9 +956,31 @@ int64_t splits_of(const DecArgs &p, int64_t groups, int64_t span) {
         splits = std::max(splits, std::min({(span + FAR - 1) / FAR, FAR_SPLITS, ((int64_t)1 << 22) / std::max<int64_t>(groups, 1)}));
     return std::max<int64_t>(1, std::min(splits, (span + unit - 1) / unit));
 }
+// The split of a many-rows call of SINKS, PREFIX or OWN, at most `most`: two workgroups of four waves a CU, or one of eight,
+// take turns of equal length, and a turn costs its tiles and about six more (the first loads, the last stores: 16 us
+// of 2.3 a tile at 256 rows of 128).  Each split writes and reads its partial results, about a tile's time for 8192 rows;
+// `join`: a launch more than one split costs, in tiles.  Against the rule above, splits and us: 1600 + 2000 queries of 20
+// heads of 64 behind 4000 shared tokens 4 -> 3; 2 x 1000 of them through a window of 1500 2 -> 1.
+int64_t turns_of(const DecArgs &p, int64_t groups, int64_t span, int64_t most, int64_t join) {
+    const int64_t tiles = (span + CT - 1) / CT, slots = p.tr == 256 ? 256 : 512;
+    int64_t best = 1, least = INT64_MAX;
+    for (int64_t n = 1; n <= std::min(most, tiles); ++n) {
+        const int64_t cost = (groups * n + slots - 1) / slots * ((tiles + n - 1) / n + 6) + n * groups * p.pr / 8192 + (n > 1 ? join : 0);
+        if (cost < least) {
+            least = cost;
+            best = n;
+        }
+    }
+    return best;
+}
+
 // The rest of a call's plan: `groups` of rows, each over `span` tokens at most.
-void split(DecArgs &p, int64_t groups, int64_t span) {
+void split(DecArgs &p, int64_t groups, int64_t span, int mode) {
     int64_t splits = splits_of(p, groups, span);
+    if (p.tr > 16 && mode == SINKS) splits = turns_of(p, groups, span, splits, 5);  // (PLAIN's workspace)
+    else if (p.tr > 16 && mode == PREFIX) splits = turns_of(p, groups, span, 64, 0);
+    else if (p.tr > 16 && mode == OWN) splits = turns_of(p, groups, span, 64, 10);
+    else if (mode == OWN && groups >= 256 && span <= 2 * FAR) splits = 1;  // then no join, 12 us for 64 sequences of 8 heads
     p.nw = p.tr == 16 && splits > 1 && wide(groups, span) ? WIDE : 4;
     if (p.nw == WIDE) splits = 1;
     const int64_t unit = p.tr > 16 ? CT : p.nw * TT;
@@ -921,12 +999,23 @@ DecArgs args_of(const Kv4Attn &a) {
     return p;
 }
 
-// Of PREFIX and OWN: the one's results lie behind the other's in the workspace.
-size_t own_ws_bytes(int b, int max_q, int hq, const Kv4Geom &g, int width, int shared) {
-    DecArgs p;
-    tiles_of(max_q, hq / g.hkv, g.d, p);
-    const int64_t groups = (int64_t)b * g.hkv * p.rt, span = (((int64_t)width - shared) << g.page_log2) + TT;
-    return ((size_t)(groups * splits_of(p, groups, span)) * p.pr * (g.d + 4) * 4 + 255) & ~(size_t)255;
+// The two parts of a call with a shared prefix, and the bytes of their partial results: OWN's, if it has more than one
+// split, then PREFIX's.
+size_t plan_shared(const Kv4Attn &a, DecArgs &pre, DecArgs &own) {
+    const int g = a.hq / a.geo.hkv, row = (a.geo.d + 4) * 4;
+    pre = own = args_of(a);
+    tiles_of(a.nq, g, a.geo.d, pre);
+    tiles_of(a.max_q, g, a.geo.d, own);
+    const int64_t pg = (int64_t)a.geo.hkv * pre.rt, og = (int64_t)a.b * a.geo.hkv * own.rt;
+    split(pre, pg, (int64_t)a.shared << a.geo.page_log2, PREFIX);
+    split(own, og, (((int64_t)a.width - a.shared) << a.geo.page_log2) + TT, OWN);
+    const size_t first = own.splits > 1 ? ((size_t)(og * own.splits) * own.pr * row + 255) & ~(size_t)255 : 0;
+    pre.part = reinterpret_cast<float *>(a.ws + first);
+    own.ptr_ = pre.tr;
+    own.ppr = pre.pr;
+    own.psplits = pre.splits;
+    own.ppart = pre.part;
+    return first + (size_t)(pg * pre.splits) * pre.pr * row;
 }
 
 template <int MODE>
@@ -993,34 +1082,31 @@ hipError_t launch_kv4_attn(const Kv4Attn &a, hipStream_t s) {
     // a window's span: that of the tile's first to its last query, and the start's rounding down; and the sinks'
     const bool sinks = a.window && a.sinks;
     if (a.window) span = std::min<int64_t>(span, (int64_t)a.window + p.tr / p.g + 1 + CT + (sinks ? (int64_t)a.sinks + CT : 0));
-    split(p, (int64_t)a.b * a.geo.hkv * p.rt, span);
+    split(p, (int64_t)a.b * a.geo.hkv * p.rt, span, sinks ? SINKS : PLAIN);
     p.blanks = blanks_of(a);
     return sinks ? attend_and_join<SINKS>(p, s) : attend_and_join<PLAIN>(p, s);
 }
 
 size_t kv4_attn_shared_ws_bytes(int64_t nq, int b, int max_q, int hq, const Kv4Geom &g, int width, int shared) {
-    DecArgs p;
-    tiles_of((int)nq, hq / g.hkv, g.d, p);
-    const int64_t groups = (int64_t)g.hkv * p.rt, splits = splits_of(p, groups, (int64_t)shared << g.page_log2);
-    return own_ws_bytes(b, max_q, hq, g, width, shared) + (size_t)(groups * splits) * p.pr * (g.d + 4) * 4;
+    Kv4Attn a{};
+    a.geo = g;
+    a.nq = (int)nq;
+    a.b = b;
+    a.max_q = max_q;
+    a.hq = hq;
+    a.width = width;
+    a.shared = shared;
+    DecArgs pre, own;
+    return plan_shared(a, pre, own);
 }
 
 hipError_t launch_kv4_attn_shared(const Kv4Attn &a, hipStream_t s) {
-    DecArgs pre = args_of(a), own = args_of(a);
-    tiles_of(a.nq, a.hq / a.geo.hkv, a.geo.d, pre);
-    split(pre, (int64_t)a.geo.hkv * pre.rt, (int64_t)a.shared << a.geo.page_log2);
-    pre.part = reinterpret_cast<float *>(a.ws + own_ws_bytes(a.b, a.max_q, a.hq, a.geo, a.width, a.shared));
-    hipError_t e = launch_attend<PREFIX>(pre, s);
-    if (e != hipSuccess) return e;
-    tiles_of(a.max_q, a.hq / a.geo.hkv, a.geo.d, own);
-    split(own, (int64_t)a.b * a.geo.hkv * own.rt, (((int64_t)a.width - a.shared) << a.geo.page_log2) + TT);
+    DecArgs pre, own;
+    plan_shared(a, pre, own);
     own.blanks = blanks_of(a);
-    own.ptr_ = pre.tr;
-    own.ppr = pre.pr;
-    own.psplits = pre.splits;
-    own.ppart = pre.part;
-    e = launch_attend<OWN>(own, s);
-    return e == hipSuccess ? launch_join<OWN>(own, s) : e;
+    hipError_t e = launch_attend<PREFIX>(pre, s);
+    if (e == hipSuccess) e = launch_attend<OWN>(own, s);
+    return e == hipSuccess && own.splits > 1 ? launch_join<OWN>(own, s) : e;
 }
 
 }  // namespace fp4
