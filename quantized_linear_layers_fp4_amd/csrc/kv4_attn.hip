@@ -434,20 +434,9 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? 3 : 1) void k_kv4_decode(DecArgs
         fetch(first, pk, pv, even);
         pages_of(first + NW * TT);
     }
-    if constexpr (ONE || NW == 4 || D == 64) {
-        for (int t0 = first; t0 < end; t0 += 2 * NW * TT) {
-            tile(even, odd, t0);
-            if (t0 + NW * TT < end) tile(odd, even, t0 + NW * TT);
-        }
-    } else {  // the 128 registers of 16 waves do not hold both tiles' addresses (9.2 | 14.8 us at 777 tokens)
-        for (int t0 = first; t0 < end; t0 += NW * TT) {
-            tile(even, odd, t0);
-            even = odd;
-        }
-    }
-
-    if constexpr (MODE == OWN) {
-        // the shared tokens' partial results, by turns of the waves: columns (4 h + r) J .. + J - 1 of the row, as acc holds them
+    // OWN: the shared tokens' partial results, by turns of the waves: columns (4 h + r) J .. + J - 1 of the row, as
+    // acc holds them
+    auto take_prefix = [&] {
         const float *w = prefix_part(p, head, (int64_t)sp.qbeg * p.g + row) + 4 * h * J;
         if (p.splits == 1 && live) {
 #pragma unroll 2
@@ -473,7 +462,22 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? 3 : 1) void k_kv4_decode(DecArgs
                 }
             }
         }
+    };
+    // while the first tile is on its way; the 128 registers of 16 waves have no room for both
+    if constexpr (MODE == OWN && NW == 4) take_prefix();
+    if constexpr (ONE || NW == 4 || D == 64) {
+        for (int t0 = first; t0 < end; t0 += 2 * NW * TT) {
+            tile(even, odd, t0);
+            if (t0 + NW * TT < end) tile(odd, even, t0 + NW * TT);
+        }
+    } else {  // the 128 registers of 16 waves do not hold both tiles' addresses (9.2 | 14.8 us at 777 tokens)
+        for (int t0 = first; t0 < end; t0 += NW * TT) {
+            tile(even, odd, t0);
+            even = odd;
+        }
     }
+
+    if constexpr (MODE == OWN && NW != 4) take_prefix();
 
     // the waves join: maxima, then sums and outputs over the common maximum, in wave order
     __shared__ float sm[NW][16], sl_[NW][16];
@@ -603,40 +607,42 @@ __global__ __launch_bounds__(NT, 2) void k_kv4_chunk(DecArgs p) {
     const int kt = tid / TPT, kq = tid % TPT;
     constexpr int VP = 8 / KD;
     const int vp = tid % VP, vn = tid / VP % (D / 8), vt = tid / VP / (D / 8);
-    const int vtok = vt * 8 + vp * KD;
+    // A wave's tokens, of K as of V, are WT consecutive ones, so they lie in one page, and page and address are scalars.
+    constexpr int WT = 64 * 64 / NT;
+    const int wt = wave * WT, ktok = kt - wt, vtok = vt * 8 + vp * KD - wt;
     // the bytes of two tiles on their way: an even tile's in set 0, an odd one's in set 1
     uint32_t kw[2][KD], vw[2][KD], ks[2], vs[2];
     const uint8_t *const headp = a.cache + (int64_t)head * region;
     const int64_t pstride = (int64_t)a.geo.hkv * region;
     auto page_at = [&](int t) { return fixed(table, min(t, stop - 1) >> lg); };
+    const uint32_t ko = ktok * (D / 2) + kq * (KD * 4), vo = ((vtok >> 3) * (D / 8) + vn) * 32 + (vtok & 7) * 4;
+    const uint32_t kso = (kq * KD / 4) * P + ktok, vso = (vn >> 2) * P + vtok;
     // pages outside the cache: their tokens' bytes are any page's, and their scores are masked
     bool okk[2];
-    auto fetch = [&](auto set, int at, int pk, int pv) {
+    auto fetch = [&](auto set, int at, int pg) {
         constexpr int z = decltype(set)::value;
-        const int t0 = token_at<MODE>(sp, at);
-        okk[z] = (uint32_t)pk < (uint64_t)a.geo.pages;
-        const bool okv = (uint32_t)pv < (uint64_t)a.geo.pages;
-        const uint8_t *kb = headp + (okk[z] ? pk : 0) * pstride, *vb = headp + (okv ? pv : 0) * pstride;
-        const int tk = (t0 + kt) & (P - 1), tv = (t0 + vtok) & (P - 1);
-        const uint8_t *ka = kb + tk * (D / 2) + kq * (KD * 4);
-        const uint8_t *va = vb + a.geo.v_off() + ((tv >> 3) * (D / 8) + vn) * 32 + (tv & 7) * 4;
+        okk[z] = (uint32_t)pg < (uint64_t)a.geo.pages;
+        const int in = (token_at<MODE>(sp, at) + wt) & (P - 1);  // a multiple of 8
+        const uint8_t *base = headp + (okk[z] ? pg : 0) * pstride;
+        const uint8_t *ka = base + in * (D / 2), *va = base + a.geo.v_off() + in * (D / 2);
+        const uint8_t *ksa = base + a.geo.ks_off() + in, *vsa = base + a.geo.vs_off() + in;
         if constexpr (KD == 4) {
-            const u32x4 x = *reinterpret_cast<const u32x4 *>(ka), y = *reinterpret_cast<const u32x4 *>(va);
+            const u32x4 x = *reinterpret_cast<const u32x4 *>(ka + ko), y = *reinterpret_cast<const u32x4 *>(va + vo);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 kw[z][i] = x[i];
                 vw[z][i] = y[i];
             }
-            vs[z] = *reinterpret_cast<const uint32_t *>(vb + a.geo.vs_off() + (vn >> 2) * P + tv);
+            vs[z] = *reinterpret_cast<const uint32_t *>(vsa + vso);
         } else {
-            const uint2 x = *reinterpret_cast<const uint2 *>(ka), y = *reinterpret_cast<const uint2 *>(va);
+            const uint2 x = *reinterpret_cast<const uint2 *>(ka + ko), y = *reinterpret_cast<const uint2 *>(va + vo);
             kw[z][0] = x.x;
             kw[z][1] = x.y;
             vw[z][0] = y.x;
             vw[z][1] = y.y;
-            vs[z] = *reinterpret_cast<const uint16_t *>(vb + a.geo.vs_off() + (vn >> 2) * P + tv);
+            vs[z] = *reinterpret_cast<const uint16_t *>(vsa + vso);
         }
-        ks[z] = kb[a.geo.ks_off() + (kq * KD / 4) * P + tk];
+        ks[z] = ksa[kso];
     };
     // K rows: KC pieces, turned so that 16 rows of one piece lie on 16 places; V rows (columns): 8
     // pieces of eight tokens, turned for the reads (32 consecutive columns) and the writes (every eighth)
@@ -690,27 +696,22 @@ __global__ __launch_bounds__(NT, 2) void k_kv4_chunk(DecArgs p) {
     float m = -INFINITY, l = 0.0f;  // m: of the unscaled scores
 
     // whether some page of a tile lies outside the cache, from the waves that unpacked it
-    __shared__ uint64_t bad[2][TPT];
+    __shared__ uint32_t bad[2][TPT];
     // tile t0 is multiplied while t0 + CT is unpacked, the bytes of the next two are on their way and the page
     // indices of t0 + 4 CT
     using I0 = std::integral_constant<int, 0>;
     using I1 = std::integral_constant<int, 1>;
-    int pk = 0, pv = 0;
-    auto pages_of = [&](int at) {
-        const int t0 = token_at<MODE>(sp, at);
-        pk = page_at(t0 + kt);
-        pv = page_at(t0 + vtok);
-    };
+    int pg = 0;
+    auto pages_of = [&](int at) { pg = page_at(token_at<MODE>(sp, at) + wt); };
     if (beg < end) {
         pages_of(beg);
-        fetch(I0{}, beg, pk, pv);
+        fetch(I0{}, beg, pg);
         pages_of(beg + CT);
-        fetch(I1{}, beg + CT, pk, pv);
+        fetch(I1{}, beg + CT, pg);
         pages_of(beg + 2 * CT);
-        const uint64_t bm = ~__builtin_amdgcn_ballot_w64(okk[0]);
-        if (lane == 0) bad[0][wave] = bm;
+        if (lane == 0) bad[0][wave] = !okk[0];
         unpack(I0{}, sk0, sv0);
-        fetch(I0{}, beg + 2 * CT, pk, pv);
+        fetch(I0{}, beg + 2 * CT, pg);
         pages_of(beg + 3 * CT);
     }
     auto tile = [&](auto buf, int at, const uint8_t *ck, const uint8_t *cv, uint8_t *nk, uint8_t *nv) {
@@ -720,10 +721,9 @@ __global__ __launch_bounds__(NT, 2) void k_kv4_chunk(DecArgs p) {
         // that it lies beside the products, which are matrix instructions
         auto next = [&] {
             using Set = std::integral_constant<int, b ^ 1>;
-            const uint64_t bm = ~__builtin_amdgcn_ballot_w64(okk[b ^ 1]);
-            if (lane == 0) bad[b ^ 1][wave] = bm;
+            if (lane == 0) bad[b ^ 1][wave] = !okk[b ^ 1];
             unpack(Set{}, nk, nv);
-            fetch(Set{}, at + 3 * CT, pk, pv);
+            fetch(Set{}, at + 3 * CT, pg);
             pages_of(at + 4 * CT);
         };
         const int t0 = token_at<MODE>(sp, at);
@@ -749,10 +749,10 @@ __global__ __launch_bounds__(NT, 2) void k_kv4_chunk(DecArgs p) {
             }
         __builtin_amdgcn_sched_barrier(0);
         // element r of block u: token t0 + 32 u + 16 (r / 8) + 8 h + r % 8 of row n
-        uint64_t any = 0;
+        uint32_t any = 0;
 #pragma unroll
         for (int w = 0; w < TPT; ++w) any |= bad[b][w];
-        const bool anybad = __builtin_amdgcn_readfirstlane((int)any | (int)(any >> 32)) != 0;
+        const bool anybad = __builtin_amdgcn_readfirstlane((int)any) != 0;
         const bool before = t0 < sw.full_lo && !(MODE == SINKS && t0 + CT <= a.sinks);
         if (anybad || before || t0 + CT > min(sw.full_hi, stop)) {
 #pragma unroll
@@ -760,8 +760,7 @@ __global__ __launch_bounds__(NT, 2) void k_kv4_chunk(DecArgs p) {
 #pragma unroll
                 for (int r = 0; r < 16; ++r) {
                     const int q = 32 * u + 16 * (r >> 3) + 8 * h + (r & 7), tok = t0 + q;
-                    // token q was unpacked by threads TPT q and on, 64 / TPT tokens a wave
-                    const bool ok = ((bad[b][q / (64 / TPT)] >> (TPT * (q % (64 / TPT)))) & 1) == 0;
+                    const bool ok = bad[b][q / WT] == 0;
                     s[u][r] = ok && tok < vhi && (tok >= vlo || (MODE == SINKS && tok < a.sinks)) ? s[u][r] : -INFINITY;
                 }
         }
@@ -974,12 +973,13 @@ int64_t turns_of(const DecArgs &p, int64_t groups, int64_t span, int64_t most, i
     return best;
 }
 
-// The rest of a call's plan: `groups` of rows, each over `span` tokens at most.
-void split(DecArgs &p, int64_t groups, int64_t span, int mode) {
+// The rest of a call's plan: `groups` of rows, each over `span` tokens at most, of the `full` that the table's rows hold.
+void split(DecArgs &p, int64_t groups, int64_t span, int64_t full, int mode) {
     int64_t splits = splits_of(p, groups, span);
     if (p.tr > 16 && mode == SINKS) splits = turns_of(p, groups, span, splits, 5);  // (PLAIN's workspace)
     else if (p.tr > 16 && mode == PREFIX) splits = turns_of(p, groups, span, 64, 0);
     else if (p.tr > 16 && mode == OWN) splits = turns_of(p, groups, span, 64, 10);
+    else if (mode == SINKS && groups >= 256 && 2 * span <= full) splits = 1;  // alike long, most of them: 45 -> 36 us, 64 x 2112 tokens
     else if (mode == OWN && groups >= 256 && span <= 2 * FAR) splits = 1;  // then no join, 12 us for 64 sequences of 8 heads
     p.nw = p.tr == 16 && splits > 1 && wide(groups, span) ? WIDE : 4;
     if (p.nw == WIDE) splits = 1;
@@ -1007,8 +1007,9 @@ size_t plan_shared(const Kv4Attn &a, DecArgs &pre, DecArgs &own) {
     tiles_of(a.nq, g, a.geo.d, pre);
     tiles_of(a.max_q, g, a.geo.d, own);
     const int64_t pg = (int64_t)a.geo.hkv * pre.rt, og = (int64_t)a.b * a.geo.hkv * own.rt;
-    split(pre, pg, (int64_t)a.shared << a.geo.page_log2, PREFIX);
-    split(own, og, (((int64_t)a.width - a.shared) << a.geo.page_log2) + TT, OWN);
+    const int64_t shared = (int64_t)a.shared << a.geo.page_log2, rest = (((int64_t)a.width - a.shared) << a.geo.page_log2) + TT;
+    split(pre, pg, shared, shared, PREFIX);
+    split(own, og, rest, rest, OWN);
     const size_t first = own.splits > 1 ? ((size_t)(og * own.splits) * own.pr * row + 255) & ~(size_t)255 : 0;
     pre.part = reinterpret_cast<float *>(a.ws + first);
     own.ptr_ = pre.tr;
@@ -1078,11 +1079,12 @@ size_t kv4_attn_ws_bytes(int b, int max_q, int hq, const Kv4Geom &g, int width) 
 hipError_t launch_kv4_attn(const Kv4Attn &a, hipStream_t s) {
     DecArgs p = args_of(a);
     tiles_of(a.max_q, a.hq / a.geo.hkv, a.geo.d, p);
-    int64_t span = (int64_t)a.width << a.geo.page_log2;
+    const int64_t full = (int64_t)a.width << a.geo.page_log2;
+    int64_t span = full;
     // a window's span: that of the tile's first to its last query, and the start's rounding down; and the sinks'
     const bool sinks = a.window && a.sinks;
     if (a.window) span = std::min<int64_t>(span, (int64_t)a.window + p.tr / p.g + 1 + CT + (sinks ? (int64_t)a.sinks + CT : 0));
-    split(p, (int64_t)a.b * a.geo.hkv * p.rt, span, sinks ? SINKS : PLAIN);
+    split(p, (int64_t)a.b * a.geo.hkv * p.rt, span, full, sinks ? SINKS : PLAIN);
     p.blanks = blanks_of(a);
     return sinks ? attend_and_join<SINKS>(p, s) : attend_and_join<PLAIN>(p, s);
 }
