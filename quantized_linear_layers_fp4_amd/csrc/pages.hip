@@ -45,6 +45,37 @@ __device__ __forceinline__ T block_scan(T x, T *sums, T &total) {
     return x + before;
 }
 
+// Two of them at once.
+__device__ __forceinline__ void block_scan2(int64_t &x, int64_t &y, int64_t *sums, int64_t &tx, int64_t &ty) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+        const int64_t u = __shfl_up(x, off, 64), v = __shfl_up(y, off, 64);
+        if (lane >= off) {
+            x += u;
+            y += v;
+        }
+    }
+    __syncthreads();
+    if (lane == 63) {
+        sums[wave] = x;
+        sums[NT / 64 + wave] = y;
+    }
+    __syncthreads();
+    tx = ty = 0;
+    int64_t bx = 0, by = 0;
+#pragma unroll
+    for (int w = 0; w < NT / 64; ++w) {
+        const int64_t u = sums[w], v = sums[NT / 64 + w];
+        bx += w < wave ? u : 0;
+        by += w < wave ? v : 0;
+        tx += u;
+        ty += v;
+    }
+    x += bx;
+    y += by;
+}
+
 // The number of entries of the ascending p[0 .. n) that are at most x.
 template <typename T>
 __device__ __forceinline__ int at_most(const T *p, int n, T x) {
@@ -81,7 +112,7 @@ template <bool PACKED>
 __global__ __launch_bounds__(NT) void k_pages_extend(PageTables t, const int32_t *__restrict__ add, int64_t n,
                                                      int64_t *__restrict__ slots, int32_t *__restrict__ positions,
                                                      int32_t *__restrict__ q_start, int32_t *__restrict__ ws, bool small) {
-    __shared__ int64_t sums[NT / 64];
+    __shared__ int64_t sums[2 * NT / 64];
     __shared__ int32_t s_start[NT + 1], s_old[NT], s_excl[NT];
     const int count = min(max(*t.count, 0), t.pages);
     int64_t pages = 0, asked = 0, given = 0, taken = 0;  // sums over the sequences before this turn's
@@ -93,27 +124,33 @@ __global__ __launch_bounds__(NT) void k_pages_extend(PageTables t, const int32_t
         if constexpr (!PACKED) a = min(a, (int64_t)1);
         bool ok = old + a <= ((int64_t)t.width << t.page_log2);
         const int have = pages_of(old, t.page_log2);
-        int64_t want = ok ? pages_of((int)(old + a), t.page_log2) - have : 0;
-        int64_t total;
-        const int64_t pi = pages + block_scan(want, sums, total);
-        pages += total;
-        ok = ok && (want == 0 || pi <= count);
-        a = ok ? a : 0;
-        int64_t ti = 0;
-        if constexpr (PACKED) {
-            ti = asked + block_scan(a, sums, total);
-            asked += total;
-            const bool fits = a == 0 || ti <= n;
-            if (__syncthreads_or(!fits) || asked - total != given) {  // offsets of those that got theirs
-                a = fits ? a : 0;
-                ok = ok && fits;
-                ti = given + block_scan(a, sums, total);
+        const int64_t need = ok ? pages_of((int)(old + a), t.page_log2) - have : 0;
+        int64_t pi = need, ti = ok ? a : 0, total, tokens;
+        block_scan2(pi, ti, sums, total, tokens);
+        pi += pages;
+        ti += asked;
+        bool short_ = in && a > 0 && (!ok || (need > 0 && pi > count) || (PACKED && ti > n));
+        if (__syncthreads_or(short_) || asked != given) {  // somebody gets nothing: who, and the sums of what the others get
+            ok = ok && (need == 0 || pi <= count);
+            a = ok ? a : 0;
+            if constexpr (PACKED) {
+                ti = asked + block_scan(a, sums, tokens);
+                ok = ok && (a == 0 || ti <= n);
+                asked += tokens;
+                a = ok ? a : 0;
+                ti = given + block_scan(a, sums, tokens);
+                given += tokens;
             }
-            given += total;
+            pages += total;
+            block_scan(ok ? need : 0, sums, total);
+            taken += total;
+        } else {
+            asked += tokens;
+            given += tokens;
+            pages += total;
+            taken += total;
         }
-        want = ok ? want : 0;
-        block_scan(want, sums, total);
-        taken += total;
+        const int64_t want = ok ? need : 0;
         const int excl = (int)(pi - want);
         if (in) {
             t.lens[i] = old + (int)a;
@@ -225,6 +262,20 @@ __global__ __launch_bounds__(NT) void k_pages_release(PageTables t, const int32_
             height = ws[G];
         } else {
             height = min(max(*t.count, 0), t.pages);
+        }
+    }
+    if constexpr (PHASE == 0) {
+        if (total <= NT) {  // the usual call: each entry is read once, and one scan says where it goes
+            int32_t *e = (int)threadIdx.x < total ? entry_of(threadIdx.x) : nullptr;
+            const int page = e ? *e : -1;
+            const bool good = (uint32_t)page < (uint32_t)t.pages;
+            const int rank = block_scan((int)good, sums, all) - 1;
+            const int64_t at = (int64_t)height + all - 1 - rank;
+            if (good && at < t.pages) t.free[at] = page;
+            if (e) *e = -1;
+            if ((int)threadIdx.x < mine) t.lens[first + threadIdx.x] = kept;
+            if (threadIdx.x == 0) *t.count = (int)min((int64_t)height + all, (int64_t)t.pages);
+            return;
         }
     }
     if constexpr (PHASE != 2) {
