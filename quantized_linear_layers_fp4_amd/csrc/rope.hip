@@ -224,7 +224,7 @@ __device__ __forceinline__ double row_scale64(const NormRope &a, const float (&x
     for (int i = 0; i < 8; ++i) ss = __builtin_fma((double)x[i], (double)x[i], ss);
     return rsqrt64(__builtin_fma(group_sum<L>(ss), a.inv_d, (double)a.eps));
 }
-// The same in fp32; false (for the whole wave) where some row's squares may have left fp32's range.
+// The same in fp32; false where the row's squares may have left fp32's range.
 template <int L>
 __device__ __forceinline__ bool row_scale32(const NormRope &a, const float (&x)[8], float &r) {
     float ss = 0.0f;
@@ -232,7 +232,7 @@ __device__ __forceinline__ bool row_scale32(const NormRope &a, const float (&x)[
     for (int i = 0; i < 8; ++i) ss = __builtin_fmaf(x[i], x[i], ss);
     const float v = __builtin_fmaf(group_sum<L>(ss), (float)a.inv_d, a.eps);
     r = __builtin_amdgcn_rsqf(v);
-    return __builtin_amdgcn_ballot_w64(!(v >= 0x1p-80f && v <= 0x1p120f)) == 0;
+    return v >= 0x1p-80f && v <= 0x1p120f;
 }
 
 template <int DT, int L, bool IL>
@@ -255,20 +255,19 @@ __device__ __forceinline__ void turn_row(const NormRope &a, const Raw<DT> &raw, 
     values<DT>(raw, x);
     partners<DT, IL>(raw, t.from, p);
     float r = 1.0f;
-    if (a.norm && !row_scale32<L>(a, x, r)) {
+    const bool fits = !a.norm || row_scale32<L>(a, x, r);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = r * __builtin_fmaf(p[i], v[i], x[i] * u[i]);
+    if (__builtin_amdgcn_ballot_w64(!fits) != 0) {  // the other rows of the wave keep what they have
         const double rd = row_scale64<L>(a, x);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const float f = (float)(rd * __builtin_fma((double)p[i], (double)v[i], (double)x[i] * (double)u[i]));
-            y[i] = t.zero ? 0.0f : f;
+            y[i] = fits ? y[i] : f;
         }
-        return;
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float f = r * __builtin_fmaf(p[i], v[i], x[i] * u[i]);
-        y[i] = t.zero ? 0.0f : f;
-    }
+    for (int i = 0; i < 8; ++i) y[i] = t.zero ? 0.0f : y[i];
 }
 
 struct FwdArgs {
@@ -455,14 +454,15 @@ __global__ __launch_bounds__(256) void k_norm_rope_bwd(BwdArgs f) {
             for (int i = 0; i < 8; ++i) g[i] = __builtin_fmaf(-turn.s[i], p[i], y[i] * turn.c[i]);
             if (a.norm) {
                 float r, dot = 0.0f;
-                if (row_scale32<L>(a, x, r)) {
+                const bool fits = row_scale32<L>(a, x, r);
+                if (__builtin_amdgcn_ballot_w64(!fits) != 0) {
+                    const double rd = row_scale64<L>(a, x);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) x[i] = fits ? x[i] * r : (float)(x[i] * rd);
+                    r = fits ? r : (float)rd;
+                } else {
 #pragma unroll
                     for (int i = 0; i < 8; ++i) x[i] *= r;
-                } else {
-                    const double rd = row_scale64<L>(a, x);
-                    r = (float)rd;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) x[i] = (float)(x[i] * rd);
                 }
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
