@@ -666,26 +666,31 @@ def kv4_attention(q: torch.Tensor, cache: KV4Cache, pages: torch.Tensor, lens: t
     shared: the first pages of every row that are taken to be row 0's and read once for all sequences (not with
     a window; ws of kv4_attention_workspace with the same shared).  A query that sees nothing gets 0 and lse -inf, and so does one past its
     sequence's first max_q, before q_start[0] or from q_start[b] on."""
-    if q.dtype != torch.bfloat16:
+    if q.dtype is not torch.bfloat16:
         raise TypeError(f"expected bfloat16 queries, got {q.dtype}")
-    if not q.is_cuda or q.dim() != 3 or q.shape[2] != cache.d or q.stride(2) != 1:
+    # (each attribute of a tensor costs about 0.1 us: they are read once)
+    dev, qs, qst, ps, pst = q.get_device(), q.shape, q.stride(), pages.shape, pages.stride()
+    if dev < 0 or len(qs) != 3 or qs[2] != cache.d or qst[2] != 1:
         raise ValueError(f"expected queries (nq, hq, {cache.d}) on a HIP device, the last dimension contiguous")
-    nq, hq, d = q.shape
+    nq, hq, d = qs
     if hq == 0 or hq % cache.heads:
         raise ValueError(f"{hq} query heads over {cache.heads} key/value heads")
-    b = pages.shape[0]
-    if lens.dtype != torch.int32 or not lens.is_cuda or lens.shape != (b,) or not lens.is_contiguous():
-        raise ValueError(f"expected {b} int32 lengths on a HIP device")
-    if q_start is not None and (q_start.dtype != torch.int32 or not q_start.is_cuda or q_start.shape != (b + 1,) or
-                                not q_start.is_contiguous()):
-        raise ValueError(f"expected {b + 1} int32 offsets on a HIP device")
-    if pages.dtype != torch.int32 or not pages.is_cuda or pages.dim() != 2 or \
-            (pages.shape[1] > 1 and pages.stride(1) != 1) or (b > 1 and pages.stride(0) < pages.shape[1]):
+    if pages.dtype is not torch.int32 or pages.get_device() < 0 or len(ps) != 2 or (ps[1] > 1 and pst[1] != 1) or \
+            (ps[0] > 1 and pst[0] < ps[1]):
         raise ValueError("expected an int32 page table (b, width) on a HIP device, rows contiguous")
-    if q_start is None and nq != b:
-        raise ValueError(f"{nq} queries for {b} sequences without q_start")
-    if max_q is None:
-        max_q = 1 if q_start is None else nq
+    b, width = ps
+    if lens.dtype is not torch.int32 or lens.get_device() < 0 or lens.shape != (b,) or not lens.is_contiguous():
+        raise ValueError(f"expected {b} int32 lengths on a HIP device")
+    if q_start is None:
+        if nq != b:
+            raise ValueError(f"{nq} queries for {b} sequences without q_start")
+        if max_q is None:
+            max_q = 1
+    else:
+        if q_start.dtype is not torch.int32 or q_start.get_device() < 0 or q_start.shape != (b + 1,) or not q_start.is_contiguous():
+            raise ValueError(f"expected {b + 1} int32 offsets on a HIP device")
+        if max_q is None:
+            max_q = nq
     if sinks < 0 or shared < 0:
         raise ValueError(f"sinks {sinks}, shared {shared}")
     if shared and window:
@@ -709,10 +714,9 @@ def kv4_attention(q: torch.Tensor, cache: KV4Cache, pages: torch.Tensor, lens: t
             f, seen = L.fp4_kv4_attention_sinks, (min(window, most), min(sinks, most))
         else:
             f, seen = L.fp4_kv4_attention, (min(window, most),)
-        _on_device(q, f, _ptr(q), q.stride(0), q.stride(1), nq, hq, _ptr(q_start), _ptr(lens), b, max_q, _ptr(pages),
-                   max(pages.stride(0), pages.shape[1]), pages.shape[1], _ptr(cache.data), cache.pages, cache.page,
-                   cache.heads, d, *seen, d ** -0.5 if scale is None else float(scale), _ptr(o), _ptr(lse), _ptr(ws),
-                   ws.numel(), _stream(q))
+        _on_device(q, f, q.data_ptr(), qst[0], qst[1], nq, hq, _ptr(q_start), lens.data_ptr(), b, max_q, pages.data_ptr(),
+                   max(pst[0], width), width, cache.data.data_ptr(), cache.pages, cache.page, cache.heads, d, *seen,
+                   d ** -0.5 if scale is None else float(scale), o.data_ptr(), _ptr(lse), ws.data_ptr(), ws.numel(), _stream(q))
     return (o, lse) if return_lse else o
 
 
