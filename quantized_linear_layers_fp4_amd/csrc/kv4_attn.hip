@@ -44,8 +44,8 @@ constexpr float LOG2E = 1.44269504088896340736f;
 //   PREFIX  the first a.shared pages of row 0 of the table, for the queries of all sequences at once: rows are those of one
 //           long sequence, and more rows a tile read the bytes once
 //   OWN     a sequence's after those
-// PREFIX leaves partial results; OWN takes them in at its end, or, where its own tokens are split too, leaves them to the
-// join, which brings both together.
+// PREFIX leaves partial results; OWN takes them in itself, or, where its own tokens are split too or PREFIX's splits are many,
+// leaves partial results as well, and the join brings both together.
 enum : int { PLAIN, SINKS, PREFIX, OWN };
 
 struct DecArgs {
@@ -62,6 +62,7 @@ struct DecArgs {
     // of OWN: PREFIX's tile rows, rows a partial holds, splits and partial results
     int ptr_, ppr, psplits;
     const float *ppart;
+    bool takes;       // it takes PREFIX's results in itself: it has one split, and they are few for a wave
 };
 
 // Entry i of a table that no kernel here writes: a scalar load where i is uniform, though other code of the kernel
@@ -274,7 +275,7 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? 3 : 1) void k_kv4_decode(DecArgs
     Span sp = span_of<MODE>(a, p.g, seq, row0, 16);
     if (row0 >= sp.rows) return;
     const int beg = sp.lo + split * p.chunk, end = min(sp.hi, beg + p.chunk);
-    if ((p.splits > 1 || MODE == PREFIX) && beg >= end) return;  // the joining kernel counts the splits the same way
+    if ((MODE == OWN ? !p.takes : p.splits > 1 || MODE == PREFIX) && beg >= end) return;  // the join counts the splits the same way
 
     // this lane's row
     const int row = row0 + n;
@@ -438,7 +439,7 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? 3 : 1) void k_kv4_decode(DecArgs
     // acc holds them
     auto take_prefix = [&] {
         const float *w = prefix_part(p, head, (int64_t)sp.qbeg * p.g + row) + 4 * h * J;
-        if (p.splits == 1 && live) {
+        if (p.takes && live) {
 #pragma unroll 2
             for (int s = wave; s < p.psplits; s += NW) {
                 const float *ws = w + (int64_t)s * p.ppr * (D + 4);
@@ -514,7 +515,7 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? 3 : 1) void k_kv4_decode(DecArgs
             o[2] += v.z * f;
             o[3] += v.w * f;
         }
-        if (p.splits == 1 && MODE != PREFIX) {
+        if (MODE == OWN ? p.takes : p.splits == 1 && MODE != PREFIX) {
             const int64_t out = (int64_t)(sp.qbeg + (row0 + r) / p.g) * a.hq + head * p.g + (row0 + r) % p.g;
             const float inv = L == 0.0f ? 0.0f : 1.0f / L;
             *reinterpret_cast<uint2 *>(a.o + out * D + col) =
@@ -566,7 +567,7 @@ __global__ __launch_bounds__(NT, 2) void k_kv4_chunk(DecArgs p) {
     const Span sp = span_of<MODE>(a, p.g, seq, row0, CR);
     if (row0 >= sp.rows) return;
     const int beg = sp.lo + split * p.chunk, end = min(sp.hi, beg + p.chunk);
-    if ((p.splits > 1 || MODE == PREFIX) && beg >= end) return;  // the joining kernel counts the splits the same way
+    if ((MODE == OWN ? !p.takes : p.splits > 1 || MODE == PREFIX) && beg >= end) return;  // the join counts the splits the same way
     const int stop = MODE == SINKS ? sp.whi : end;  // the first token that nobody sees
 
     // this lane's row, and what the wave's rows see
@@ -803,7 +804,7 @@ __global__ __launch_bounds__(NT, 2) void k_kv4_chunk(DecArgs p) {
     float ms = m == -INFINITY ? m : m * c;  // of the scaled scores
     if constexpr (MODE == OWN) {
         const float *w = prefix_part(p, head, (int64_t)sp.qbeg * p.g + row);
-        if (p.splits == 1) {
+        if (p.takes) {
             for (int s = 0; s < p.psplits; ++s, w += (int64_t)p.ppr * (D + 4)) {
                 const float2 ml = *reinterpret_cast<const float2 *>(w + D);
                 const float nm = fmaxf(ms, ml.x), mu = nm == -INFINITY ? 0.0f : nm;
@@ -823,7 +824,7 @@ __global__ __launch_bounds__(NT, 2) void k_kv4_chunk(DecArgs p) {
         }
     }
     // element r of tile j: column 32 j + 8 (r / 4) + 4 h + r % 4 of row n
-    if (p.splits == 1 && MODE != PREFIX) {
+    if (MODE == OWN ? p.takes : p.splits == 1 && MODE != PREFIX) {
         const int64_t out = (int64_t)(sp.qbeg + qi) * a.hq + qh;
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll
@@ -1009,8 +1010,11 @@ size_t plan_shared(const Kv4Attn &a, DecArgs &pre, DecArgs &own) {
     const int64_t pg = (int64_t)a.geo.hkv * pre.rt, og = (int64_t)a.b * a.geo.hkv * own.rt;
     const int64_t shared = (int64_t)a.shared << a.geo.page_log2, rest = (((int64_t)a.width - a.shared) << a.geo.page_log2) + TT;
     split(pre, pg, shared, shared, PREFIX);
-    split(own, og, rest, rest, OWN);
-    const size_t first = own.splits > 1 ? ((size_t)(og * own.splits) * own.pr * row + 255) & ~(size_t)255 : 0;
+    // A wave of the many-rows kernel reads its rows' results one split after the other, about 1 us each, and the decode
+    // kernel's waves take turns: 32 splits of 912 rows a head were 60 us where a join takes 8, 183 of 25 rows 25.
+    split(own, og, rest, rest, own.tr == 16 || pre.splits <= 8 ? OWN : PREFIX);
+    own.takes = own.splits == 1 && pre.splits <= 8 * (own.tr == 16 ? own.nw : 1);
+    const size_t first = !own.takes ? ((size_t)(og * own.splits) * own.pr * row + 255) & ~(size_t)255 : 0;
     pre.part = reinterpret_cast<float *>(a.ws + first);
     own.ptr_ = pre.tr;
     own.ppr = pre.pr;
@@ -1108,7 +1112,7 @@ hipError_t launch_kv4_attn_shared(const Kv4Attn &a, hipStream_t s) {
     own.blanks = blanks_of(a);
     hipError_t e = launch_attend<PREFIX>(pre, s);
     if (e == hipSuccess) e = launch_attend<OWN>(own, s);
-    return e == hipSuccess && own.splits > 1 ? launch_join<OWN>(own, s) : e;
+    return e == hipSuccess && !own.takes ? launch_join<OWN>(own, s) : e;
 }
 
 }  // namespace fp4
