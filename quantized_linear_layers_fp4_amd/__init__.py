@@ -827,14 +827,14 @@ def rope_table(max_pos: int, rot: int, base: float = 10000.0, factor: float = 1.
     return t
 
 
-def _head_args(name: str, t: torch.Tensor, ref: torch.Tensor, n: int, d: int):
-    """C arguments (pointer, token and head strides) of t as n x heads x d like ref, and the heads."""
+def _head_args(name: str, t: torch.Tensor, dtype: torch.dtype, dev: int, n: int, d: int):
+    """C arguments (pointer, token and head strides) of t as n x heads x d on device dev, and the heads."""
     shape, stride = t.shape, t.stride()
-    if len(shape) != 3 or shape[0] != n or shape[2] != d or stride[2] != 1 or not t.is_cuda:
-        raise ValueError(f"expected {name} as ({n}, heads, {d}) on a HIP device, the last dimension contiguous")
-    if t.dtype is not ref.dtype:
-        raise TypeError(f"{name} is {t.dtype}, expected {ref.dtype}")
-    if t.get_device() != ref.get_device():
+    if len(shape) != 3 or shape[0] != n or shape[2] != d or stride[2] != 1:
+        raise ValueError(f"expected {name} as ({n}, heads, {d}), the last dimension contiguous")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} is {t.dtype}, expected {dtype}")
+    if t.get_device() != dev:
         raise ValueError("tensors must be on one device")
     return (t.data_ptr(), stride[0], stride[1]), shape[1]
 
@@ -842,13 +842,21 @@ def _head_args(name: str, t: torch.Tensor, ref: torch.Tensor, n: int, d: int):
 _NO_HEADS = ((None, 0, 0), 0)
 
 
+def _weight_args(w: torch.Tensor, dev: int, d: int) -> int:
+    """w's type code, after its checks."""
+    if w.get_device() != dev or w.dim() != 1 or w.numel() != d or not w.is_contiguous():
+        raise ValueError(f"expected {d} contiguous weights on the rows' device")
+    return _dt(w)
+
+
 def _rope_args(q, k, table, positions, q_weight, k_weight, eps):
-    """Checks what the calls over rows of heads share: (n, d, q's and k's arguments, those from the weights to rot)."""
-    if q.dim() != 3:
-        raise ValueError("expected queries (n, heads, d)")
+    """Checks what the calls over rows of heads share: (n, d, device, q's and k's arguments, those from the weights to rot)."""
+    dev, dtype = q.get_device(), q.dtype
+    if dev < 0 or q.dim() != 3:
+        raise ValueError("expected queries (n, heads, d) on a HIP device")
     n, _, d = q.shape
-    qa = _head_args("q", q, q, n, d)
-    ka = _NO_HEADS if k is None else _head_args("k", k, q, n, d)
+    qa = _head_args("q", q, dtype, dev, n, d)
+    ka = _NO_HEADS if k is None else _head_args("k", k, dtype, dev, n, d)
     if qa[1] == 0:
         raise ValueError("no query heads")
     wdt = FP4_F32
@@ -857,32 +865,27 @@ def _rope_args(q, k, table, positions, q_weight, k_weight, eps):
             raise ValueError("weights without a norm")
         if k is None and k_weight is not None:
             raise ValueError("weights without keys")
-        for w in (q_weight, k_weight):
-            if w is None:
-                continue
-            if not w.is_cuda or w.shape != (d,) or not w.is_contiguous():
-                raise ValueError(f"expected {d} contiguous weights on a HIP device")
-            if w.get_device() != q.get_device():
-                raise ValueError("tensors must be on one device")
-            wdt = _dt(w)
-        if q_weight is not None and k_weight is not None and q_weight.dtype is not k_weight.dtype:
+        wdt = _weight_args(q_weight if q_weight is not None else k_weight, dev, d)
+        if q_weight is not None and k_weight is not None and _weight_args(k_weight, dev, d) != wdt:
             raise TypeError("the weights must share a dtype")
     if eps is not None and not eps >= 0:
         raise ValueError(f"eps {eps}")
-    rot = max_pos = 0
-    if table is not None:
-        if table.dtype is not torch.float32 or not table.is_cuda or table.dim() != 2 or not table.is_contiguous():
-            raise ValueError("expected an fp32 table (max_pos, rot) on a HIP device")
+    if table is None:
+        pos = tab = None
+        max_pos = rot = 0
+    else:
+        if table.dtype is not torch.float32 or table.get_device() != dev or table.dim() != 2 or not table.is_contiguous():
+            raise ValueError("expected an fp32 table (max_pos, rot) on the rows' device")
         if positions is None:
             raise ValueError("a table without positions")
-        _int32s("the positions", positions, (n,), q)
-        if table.get_device() != q.get_device():
-            raise ValueError("tensors must be on one device")
+        if positions.dtype is not torch.int32 or positions.get_device() != dev or positions.dim() != 1 or \
+                positions.numel() != n or not positions.is_contiguous():
+            raise ValueError(f"expected {n} contiguous int32 positions on the rows' device")
         max_pos, rot = table.shape
         if rot < 16:
             raise ValueError(f"a rotation of {rot} columns")
-    return n, d, qa, ka, (_ptr(q_weight), _ptr(k_weight), wdt, -1.0 if eps is None else float(eps),
-                          positions.data_ptr() if rot else None, _ptr(table), max_pos, rot)
+        pos, tab = positions.data_ptr(), table.data_ptr()
+    return n, d, dev, qa, ka, (_ptr(q_weight), _ptr(k_weight), wdt, -1.0 if eps is None else float(eps), pos, tab, max_pos, rot)
 
 
 def qk_norm_rope(q: torch.Tensor, k: torch.Tensor | None, table: torch.Tensor | None = None,
@@ -892,7 +895,7 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor | None, table: torch.Tensor | 
     rotation of the first columns by table (rope_table's) at positions (int32, n): dense (q, k).  eps None: no norm; table
     None: no rotation.  Pairs are (i, i + rot / 2), or (2 i, 2 i + 1) if interleaved.  A negative position's rows
     are zeros; one past the table makes the rotated columns NaN."""
-    n, d, (qp, hq), (kp, hkv), args = _rope_args(q, k, table, positions, q_weight, k_weight, eps)
+    n, d, dev, (qp, hq), (kp, hkv), args = _rope_args(q, k, table, positions, q_weight, k_weight, eps)
     qo = torch.empty_like(q, memory_format=torch.contiguous_format)
     ko = None if k is None else torch.empty_like(k, memory_format=torch.contiguous_format)
     if n:
@@ -908,7 +911,7 @@ def qk_norm_rope_backward(dq: torch.Tensor, dk: torch.Tensor | None, q: torch.Te
     """Gradients (of q, of k, of q_weight, of k_weight) of qk_norm_rope from those of its outputs and its inputs; the weights'
     in fp32 (None where there is no weight).  out: (tensor or None, tensor or None) for the first two, views into the
     fused projection's gradient for one."""
-    n, d, (qp, hq), (kp, hkv), args = _rope_args(q, k, table, positions, q_weight, k_weight, eps)
+    n, d, dev, (qp, hq), (kp, hkv), args = _rope_args(q, k, table, positions, q_weight, k_weight, eps)
     if (dk is None) != (k is None):
         raise ValueError("keys and their gradient go together")
     gq, gk = out if out is not None else (None, None)
@@ -918,8 +921,10 @@ def qk_norm_rope_backward(dq: torch.Tensor, dk: torch.Tensor | None, q: torch.Te
         gk = torch.empty_like(k, memory_format=torch.contiguous_format)
     elif k is None and gk is not None:
         raise ValueError("a place for a gradient without keys")
-    (dqp, h0), (gqp, h1) = _head_args("dq", dq, q, n, d), _head_args("out", gq, q, n, d)
-    (dkp, h2), (gkp, h3) = (_NO_HEADS, _NO_HEADS) if k is None else (_head_args("dk", dk, q, n, d), _head_args("out", gk, q, n, d))
+    dt = q.dtype
+    (dqp, h0), (gqp, h1) = _head_args("dq", dq, dt, dev, n, d), _head_args("out", gq, dt, dev, n, d)
+    (dkp, h2), (gkp, h3) = (_NO_HEADS, _NO_HEADS) if k is None else (_head_args("dk", dk, dt, dev, n, d),
+                                                                     _head_args("out", gk, dt, dev, n, d))
     if h0 != hq or h1 != hq or h2 != hkv or h3 != hkv:
         raise ValueError("gradients are not like the inputs")
     wq = wk = ws = None
@@ -945,8 +950,8 @@ def kv4_norm_rope(cache: KV4Cache, q: torch.Tensor, k: torch.Tensor, v: torch.Te
                   interleaved: bool = False) -> torch.Tensor:
     """qk_norm_rope, of which k goes with v (n x heads x d) to the cache's slots (as kv4_write takes them) in the same
     launch: returns q."""
-    n, d, (qp, hq), (kp, hkv), args = _rope_args(q, k, table, positions, q_weight, k_weight, eps)
-    vp, hv = _head_args("v", v, q, n, d)
+    n, d, dev, (qp, hq), (kp, hkv), args = _rope_args(q, k, table, positions, q_weight, k_weight, eps)
+    vp, hv = _head_args("v", v, q.dtype, dev, n, d)
     if hkv != cache.heads or hv != hkv or d != cache.d:
         raise ValueError(f"expected keys and values (n, {cache.heads}, {cache.d})")
     sb = _slot_bytes(slots, n)
