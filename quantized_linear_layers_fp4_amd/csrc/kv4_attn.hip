@@ -117,11 +117,15 @@ __device__ __forceinline__ Span span_of(const Kv4Attn &a, int g, int seq, int ro
         s.whi = hi;
         if (hi <= 0) return s;
         const int turn = (int)(((int64_t)min(a.sinks, hi) + CT - 1) & ~(int64_t)(CT - 1));
-        if (turn < lo) {
+        if (lo >= hi) {  // the table's row ends before the window: the first tokens alone
+            s.hi = min(turn, hi);
+        } else if (turn < lo) {
             s.turn = turn;
-            s.gap = lo - turn;  // a window that the table's row ends before leaves the first tokens alone
+            s.gap = lo - turn;
+            s.hi = turn + hi - lo;
+        } else {
+            s.hi = hi;
         }
-        s.hi = turn < lo ? turn + max(hi - lo, 0) : hi;
     } else {
         if (lo >= hi) return s;
         s.lo = lo;
@@ -172,7 +176,7 @@ __device__ __forceinline__ int prefix_seen(const Kv4Attn &a, int g, int row) {
     const int query = row / g, seq = owner_of(a, query);
     if (seq < 0) return prefix_of(a);  // of a row that nothing is made of
     const int beg = a.q_start ? query_at(a, seq) : query, ql = a.q_start ? query_at(a, seq + 1) - beg : 1;
-    return min(max(max(a.lens[seq], 0) - ql + (query - beg) + 1, 0), prefix_of(a));
+    return (int)min(max((int64_t)max(a.lens[seq], 0) - ql + (query - beg) + 1, (int64_t)0), (int64_t)prefix_of(a));
 }
 
 // Queries that no sequence's row tiles cover get zeros and lse = -inf: those past a sequence's first max_q, before

@@ -167,6 +167,20 @@ def test_sinks_where_the_table_ends(qlens):
     c.check(5, 96)
 
 
+@pytest.mark.parametrize("qlens", [[1, 2], [40, 3], [300, 200]])
+def test_lengths_and_windows_of_any_value(qlens):
+    """Lengths far past the table and negative ones, windows and sinks of any size: nothing is read outside, and rows see
+    what the table holds of what is theirs."""
+    for lens in ([2 ** 31 - 1, 2 ** 31 - 1], [2 ** 30, -2 ** 31], [150, 2 ** 31 - 5]):
+        c = Case([96, 96], qlens, 8, 2, 64, 32, width=3)
+        c.lens = lens
+        for window, sinks in ((1, 1), (50, 40), (2 ** 31 - 1, 2 ** 31 - 1), (2 ** 31 - 40, 3), (2 ** 30, 2 ** 30), (100, 96)):
+            c.check(window, sinks)
+        c = Case([96, 96], qlens, 8, 2, 64, 32, width=3, shared=2)
+        c.lens = lens
+        c.check()
+
+
 def test_sinks_without_a_window_and_a_window_without_sinks():
     c = Case([300, 77], [40, 1], 4, 2, 128, 32)
     base = c.run()
