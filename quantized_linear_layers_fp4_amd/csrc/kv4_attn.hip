@@ -604,6 +604,9 @@ __global__ __launch_bounds__(NT, 2) void k_kv4_chunk(DecArgs p) {
         qf[i] = __builtin_bit_cast(v8bf, x);
     }
 
+    // SINKS: tokens vlo .. vlo + vcount - 1 and those below vsinks (three comparisons instead cost 30 registers, a wave)
+    const uint32_t vcount = max(vhi - vlo, 0);
+    const int vsinks = min(a.sinks, vhi);
     // What a thread unpacks: KD dwords of one token's K (of one group of 32), and eight columns of KD
     // consecutive tokens' V.
     const int lg = a.geo.page_log2, P = 1 << lg;
@@ -766,7 +769,8 @@ __global__ __launch_bounds__(NT, 2) void k_kv4_chunk(DecArgs p) {
                 for (int r = 0; r < 16; ++r) {
                     const int q = 32 * u + 16 * (r >> 3) + 8 * h + (r & 7), tok = t0 + q;
                     const bool ok = bad[b][q / WT] == 0;
-                    s[u][r] = ok && tok < vhi && (tok >= vlo || (MODE == SINKS && tok < a.sinks)) ? s[u][r] : -INFINITY;
+                    const bool see = MODE == SINKS ? (uint32_t)(tok - vlo) < vcount || tok < vsinks : tok < vhi && tok >= vlo;
+                    s[u][r] = ok && see ? s[u][r] : -INFINITY;
                 }
         }
         float mx = m;
@@ -960,18 +964,27 @@ int64_t splits_of(const DecArgs &p, int64_t groups, int64_t span) {
         splits = std::max(splits, std::min({(span + FAR - 1) / FAR, FAR_SPLITS, ((int64_t)1 << 22) / std::max<int64_t>(groups, 1)}));
     return std::max<int64_t>(1, std::min(splits, (span + unit - 1) / unit));
 }
-// The split of a many-rows call of SINKS, PREFIX or OWN, at most `most`: two workgroups of four waves a CU, or one of eight,
-// take turns of equal length, and a turn costs its tiles and about six more (the first loads, the last stores: 16 us
-// of 2.3 a tile at 256 rows of 128).  Each split writes and reads its partial results, about a tile's time for 8192 rows;
-// `join`: a launch more than one split costs, in tiles.  Against the rule above, splits and us: 1600 + 2000 queries of 20
-// heads of 64 behind 4000 shared tokens 4 -> 3; 2 x 1000 of them through a window of 1500 2 -> 1.
-int64_t turns_of(const DecArgs &p, int64_t groups, int64_t span, int64_t most, int64_t join) {
-    const int64_t tiles = (span + CT - 1) / CT, slots = p.tr == 256 ? 256 : 512;
-    int64_t best = 1, least = INT64_MAX;
-    for (int64_t n = 1; n <= std::min(most, tiles); ++n) {
-        const int64_t cost = (groups * n + slots - 1) / slots * ((tiles + n - 1) / n + 6) + n * groups * p.pr / 8192 + (n > 1 ? join : 0);
-        if (cost < least) {
-            least = cost;
+// The split of a many-rows call of SINKS, PREFIX or OWN, at most `most`, by the time that it would take.  A tile takes
+// 2.3 us of a workgroup of eight waves; one of four has company on its CU: 1.1, 1.6 and 2.0 us with one to three of them
+// at heads of 64, 1.6 and 2.4 with two at 128.  A turn of workgroups costs 5 us besides; partial results are written and
+// read at 4.8 TB/s; `always`: one split leaves them too, and otherwise more than one costs the join's launch.
+// Against the rule above, splits and us: 17 x 75 queries of 20 heads of 64 behind 4000 shared tokens 4 -> 5 and 101 -> 53 with
+// its join gone, 2 x 1000 of them through a window of 1500 2 -> 1 and 65 -> 55.
+int64_t turns_of(const DecArgs &p, int64_t groups, int64_t span, int64_t most, bool always) {
+    const int64_t tiles = (span + CT - 1) / CT;
+    const bool wide_tile = p.tr == 256, small_head = p.a.geo.d == 64;
+    const int64_t company = wide_tile ? 1 : small_head ? 3 : 2;
+    const float one = wide_tile ? 2.3f : small_head ? 1.13f : 1.6f, more = small_head ? 0.43f : 0.8f;
+    const float parts = (float)groups * p.pr * (p.a.geo.d + 4) * (8.0f / 4.8e6f);
+    int64_t best = 1;
+    float least = 0.0f;
+    for (int64_t n = 1; n <= std::min({most, tiles, (int64_t)64}); ++n) {
+        const int64_t on_cu = (groups * n + 255) / 256, full = on_cu / company, rest = on_cu % company;
+        const float tile = full * (one + (company - 1) * more) + (rest ? one + (rest - 1) * more : 0.0f);
+        const float t = tile * ((tiles + n - 1) / n) + 5.0f * (full + (rest != 0)) + (always || n > 1 ? parts * n : 0.0f) +
+                        (!always && n > 1 ? 4.0f : 0.0f);
+        if (n == 1 || t < least) {
+            least = t;
             best = n;
         }
     }
@@ -981,9 +994,9 @@ int64_t turns_of(const DecArgs &p, int64_t groups, int64_t span, int64_t most, i
 // The rest of a call's plan: `groups` of rows, each over `span` tokens at most, of the `full` that the table's rows hold.
 void split(DecArgs &p, int64_t groups, int64_t span, int64_t full, int mode) {
     int64_t splits = splits_of(p, groups, span);
-    if (p.tr > 16 && mode == SINKS) splits = turns_of(p, groups, span, splits, 5);  // (PLAIN's workspace)
-    else if (p.tr > 16 && mode == PREFIX) splits = turns_of(p, groups, span, 64, 0);
-    else if (p.tr > 16 && mode == OWN) splits = turns_of(p, groups, span, 64, 10);
+    if (p.tr > 16 && mode == SINKS) splits = turns_of(p, groups, span, splits, false);  // (PLAIN's workspace)
+    else if (p.tr > 16 && mode == PREFIX) splits = turns_of(p, groups, span, 64, true);
+    else if (p.tr > 16 && mode == OWN) splits = turns_of(p, groups, span, 64, false);
     else if (mode == SINKS && groups >= 256 && 2 * span <= full) splits = 1;  // alike long, most of them: 45 -> 36 us, 64 x 2112 tokens
     else if (mode == OWN && groups >= 256 && span <= 2 * FAR) splits = 1;  // then no join, 12 us for 64 sequences of 8 heads
     p.nw = p.tr == 16 && splits > 1 && wide(groups, span) ? WIDE : 4;
