@@ -456,11 +456,15 @@ fp4_status fp4_kv4_attention_sinks(const void *q, int64_t q_token_stride, int64_
                                    float scale, void *o, float *lse, void *workspace, size_t ws_bytes, void *stream);
 
 /* The same (without a window) for sequences whose first pages are shared: the first `shared` (1 .. width) pages of
- * every row are taken to be those of row 0, whose bytes are read once for the queries of all sequences, not once for each
- * sequence.  lens count the shared tokens; a sequence may be shorter than they are.  Results are those of
- * fp4_kv4_attention within the roundings of its sums.
+ * every row are taken to be those of row 0.  Where that is quicker, their bytes are read once for the queries of all
+ * sequences and each sequence's own tokens beside them (two parts), else once for each sequence (one part).  lens count the
+ * shared tokens; a sequence may be shorter than they are.  Results are those of fp4_kv4_attention within the
+ * roundings of its sums.
  * Further limit: nq * (hq / hkv) < 2^24.
- *   workspace: at least fp4_kv4_attention_shared_workspace_bytes(...) bytes (0: invalid arguments). */
+ *   workspace: at least fp4_kv4_attention_shared_workspace_bytes(...) bytes (0 for invalid arguments, or if none is needed).
+ * fp4_kv4_attention_shared_parts (host-only): 1 or 2, as a call of these sizes is done; 0 for invalid arguments. */
+int32_t fp4_kv4_attention_shared_parts(int64_t nq, int32_t b, int32_t max_q, int32_t hq, int32_t hkv, int32_t d, int32_t page,
+                                       int32_t width, int32_t shared);
 size_t fp4_kv4_attention_shared_workspace_bytes(int64_t nq, int32_t b, int32_t max_q, int32_t hq, int32_t hkv, int32_t d,
                                                 int32_t page, int32_t width, int32_t shared);
 fp4_status fp4_kv4_attention_shared(const void *q, int64_t q_token_stride, int64_t q_head_stride, int64_t nq, int32_t hq,

@@ -38,7 +38,7 @@ EXPORTS = (
     "fp4_block8_gemm", "fp4_block8_linear_workspace_bytes", "fp4_block8_linear",
     "fp4_block8_backward_workspace_bytes", "fp4_block8_backward",
     "fp4_kv4_cache_bytes", "fp4_kv4_write", "fp4_kv4_read", "fp4_kv4_attention_workspace_bytes", "fp4_kv4_attention",
-    "fp4_kv4_attention_sinks", "fp4_kv4_attention_shared_workspace_bytes", "fp4_kv4_attention_shared",
+    "fp4_kv4_attention_sinks", "fp4_kv4_attention_shared_parts", "fp4_kv4_attention_shared_workspace_bytes", "fp4_kv4_attention_shared",
     "fp4_kv4_extend_workspace_bytes", "fp4_kv4_extend", "fp4_kv4_release_workspace_bytes", "fp4_kv4_release",
     "fp4_rope_table", "fp4_qk_norm_rope", "fp4_kv4_norm_rope", "fp4_qk_norm_rope_backward_workspace_bytes",
     "fp4_qk_norm_rope_backward",
@@ -110,6 +110,7 @@ def lib():
                                     i32, C.c_float, vp, vp, vp, sz, vp]),
         "fp4_kv4_attention_sinks": (i32, [vp, i64, i64, i64, i32, vp, vp, i32, i32, vp, i64, i32, vp, i64, i32, i32, i32,
                                           i32, i32, C.c_float, vp, vp, vp, sz, vp]),
+        "fp4_kv4_attention_shared_parts": (i32, [i64, i32, i32, i32, i32, i32, i32, i32, i32]),
         "fp4_kv4_attention_shared_workspace_bytes": (sz, [i64, i32, i32, i32, i32, i32, i32, i32, i32]),
         "fp4_kv4_attention_shared": (i32, [vp, i64, i64, i64, i32, vp, vp, i32, i32, vp, i64, i32, vp, i64, i32, i32, i32,
                                            i32, C.c_float, vp, vp, vp, sz, vp]),
@@ -663,8 +664,8 @@ def kv4_attention(q: torch.Tensor, cache: KV4Cache, pages: torch.Tensor, lens: t
     sequence (None: as many as q has, or 1 without q_start; a close bound is faster, needs less workspace, and is
     needed where b times q's rows pass what a call may have);
     window: tokens a query sees (0: all); sinks: with a window, the first tokens of a sequence that stay visible;
-    shared: the first pages of every row that are taken to be row 0's and read once for all sequences (not with
-    a window; ws of kv4_attention_workspace with the same shared).  A query that sees nothing gets 0 and lse -inf, and so does one past its
+    shared: the first pages of every row that are taken to be row 0's, and read once for all sequences where that is
+    quicker (not with a window; ws of kv4_attention_workspace with the same shared).  A query that sees nothing gets 0 and lse -inf, and so does one past its
     sequence's first max_q, before q_start[0] or from q_start[b] on."""
     if q.dtype is not torch.bfloat16:
         raise TypeError(f"expected bfloat16 queries, got {q.dtype}")

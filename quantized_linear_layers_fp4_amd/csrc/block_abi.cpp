@@ -296,6 +296,13 @@ static bool shared_shape(int64_t nq, int32_t b, int32_t max_q, int32_t hq, int32
            attn_shape(1, (int32_t)nq, hq, hkv, width, page, 0);
 }
 
+int32_t fp4_kv4_attention_shared_parts(int64_t nq, int32_t b, int32_t max_q, int32_t hq, int32_t hkv, int32_t d, int32_t page,
+                                       int32_t width, int32_t shared) {
+    Kv4Geom g;
+    if (!geom(1, page, hkv, d, g) || !shared_shape(nq, b, max_q, hq, hkv, width, page, shared)) return 0;
+    return kv4_attn_shared_parts(nq, b, max_q, hq, g, width, shared);
+}
+
 size_t fp4_kv4_attention_shared_workspace_bytes(int64_t nq, int32_t b, int32_t max_q, int32_t hq, int32_t hkv, int32_t d,
                                                 int32_t page, int32_t width, int32_t shared) {
     Kv4Geom g;

@@ -56,6 +56,7 @@ hipError_t launch_kv4_read(const uint8_t *cache, const Kv4Geom &g, const void *s
                            void *V, int dt, hipStream_t s);
 size_t kv4_attn_ws_bytes(int b, int max_q, int hq, const Kv4Geom &g, int width);
 hipError_t launch_kv4_attn(const Kv4Attn &a, hipStream_t s);
+int kv4_attn_shared_parts(int64_t nq, int b, int max_q, int hq, const Kv4Geom &g, int width, int shared);
 size_t kv4_attn_shared_ws_bytes(int64_t nq, int b, int max_q, int hq, const Kv4Geom &g, int width, int shared);
 hipError_t launch_kv4_attn_shared(const Kv4Attn &a, hipStream_t s);
 

@@ -44,9 +44,10 @@ constexpr float LOG2E = 1.44269504088896340736f;
 //   PREFIX  the first a.shared pages of row 0 of the table, for the queries of all sequences at once: rows are those of one
 //           long sequence, and more rows a tile read the bytes once
 //   OWN     a sequence's after those
+//   WHOLE   PLAIN's, their first a.shared pages looked up in row 0: where sharing their bytes would cost more than it saves
 // PREFIX leaves partial results; OWN takes them in itself, or, where its own tokens are split too or PREFIX's splits are many,
 // leaves partial results as well, and the join brings both together.
-enum : int { PLAIN, SINKS, PREFIX, OWN };
+enum : int { PLAIN, SINKS, PREFIX, OWN, WHOLE };
 
 struct DecArgs {
     Kv4Attn a;
@@ -324,7 +325,10 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? 3 : 1) void k_kv4_decode(DecArgs
         uint2 vs;
         bool okk;  // the page is one of the cache's (K's lane; V's tokens are the same pages)
     };
-    auto page_at = [&](int t) { return fixed(table, min(t, stop - 1) >> lg); };
+    auto page_at = [&](int t) {
+        const int c = min(t, stop - 1) >> lg;
+        return fixed(MODE == WHOLE && c < a.shared ? a.pages : table, c);
+    };
     auto fetch = [&](int at, int pk, int pv, Tile &x) {
         const int t0 = token_at<MODE>(sp, at);
         x.okk = (uint32_t)pk < (uint64_t)a.geo.pages;
@@ -622,7 +626,10 @@ __global__ __launch_bounds__(NT, 2) void k_kv4_chunk(DecArgs p) {
     uint32_t kw[2][KD], vw[2][KD], ks[2], vs[2];
     const uint8_t *const headp = a.cache + (int64_t)head * region;
     const int64_t pstride = (int64_t)a.geo.hkv * region;
-    auto page_at = [&](int t) { return fixed(table, min(t, stop - 1) >> lg); };
+    auto page_at = [&](int t) {
+        const int c = min(t, stop - 1) >> lg;
+        return fixed(MODE == WHOLE && c < a.shared ? a.pages : table, c);
+    };
     const uint32_t ko = ktok * (D / 2) + kq * (KD * 4), vo = ((vtok >> 3) * (D / 8) + vn) * 32 + (vtok & 7) * 4;
     const uint32_t kso = (kq * KD / 4) * P + ktok, vso = (vn >> 2) * P + vtok;
     // pages outside the cache: their tokens' bytes are any page's, and their scores are masked
@@ -970,21 +977,20 @@ int64_t splits_of(const DecArgs &p, int64_t groups, int64_t span) {
 // read at 4.8 TB/s; `always`: one split leaves them too, and otherwise more than one costs the join's launch.
 // Against the rule above, splits and us: 17 x 75 queries of 20 heads of 64 behind 4000 shared tokens 4 -> 5 and 101 -> 53 with
 // its join gone, 2 x 1000 of them through a window of 1500 2 -> 1 and 65 -> 55.
-int64_t turns_of(const DecArgs &p, int64_t groups, int64_t span, int64_t most, bool always) {
+int64_t turns_of(const DecArgs &p, int64_t groups, int64_t span, int64_t most, bool always, float &us) {
     const int64_t tiles = (span + CT - 1) / CT;
     const bool wide_tile = p.tr == 256, small_head = p.a.geo.d == 64;
     const int64_t company = wide_tile ? 1 : small_head ? 3 : 2;
     const float one = wide_tile ? 2.3f : small_head ? 1.13f : 1.6f, more = small_head ? 0.43f : 0.8f;
     const float parts = (float)groups * p.pr * (p.a.geo.d + 4) * (8.0f / 4.8e6f);
     int64_t best = 1;
-    float least = 0.0f;
     for (int64_t n = 1; n <= std::min({most, tiles, (int64_t)64}); ++n) {
         const int64_t on_cu = (groups * n + 255) / 256, full = on_cu / company, rest = on_cu % company;
         const float tile = full * (one + (company - 1) * more) + (rest ? one + (rest - 1) * more : 0.0f);
         const float t = tile * ((tiles + n - 1) / n) + 5.0f * (full + (rest != 0)) + (always || n > 1 ? parts * n : 0.0f) +
                         (!always && n > 1 ? 4.0f : 0.0f);
-        if (n == 1 || t < least) {
-            least = t;
+        if (n == 1 || t < us) {
+            us = t;
             best = n;
         }
     }
@@ -992,21 +998,31 @@ int64_t turns_of(const DecArgs &p, int64_t groups, int64_t span, int64_t most, b
 }
 
 // The rest of a call's plan: `groups` of rows, each over `span` tokens at most, of the `full` that the table's rows hold.
-void split(DecArgs &p, int64_t groups, int64_t span, int64_t full, int mode) {
+// Returns about how many us it takes, launch and all (not of PLAIN's many-rows kernels): the decode kernel 6 and what
+// the bytes take, of the last-level cache where they are shared, 7.9 TB/s at heads of 128 and 5.8 at 64.
+float split(DecArgs &p, int64_t groups, int64_t span, int64_t full, int mode) {
     int64_t splits = splits_of(p, groups, span);
-    if (p.tr > 16 && mode == SINKS) splits = turns_of(p, groups, span, splits, false);  // (PLAIN's workspace)
-    else if (p.tr > 16 && mode == PREFIX) splits = turns_of(p, groups, span, 64, true);
-    else if (p.tr > 16 && mode == OWN) splits = turns_of(p, groups, span, 64, false);
-    else if (mode == SINKS && groups >= 256 && 2 * span <= full) splits = 1;  // alike long, most of them: 45 -> 36 us, 64 x 2112 tokens
-    else if (mode == OWN && groups >= 256 && span <= 2 * FAR) splits = 1;  // then no join, 12 us for 64 sequences of 8 heads
+    float us = 0.0f;
+    if (p.tr > 16) {
+        if (mode == SINKS) splits = turns_of(p, groups, span, splits, false, us);  // (PLAIN's workspace)
+        else if (mode != PLAIN) splits = turns_of(p, groups, span, 64, mode == PREFIX, us);
+        us += 4.0f;
+    } else {
+        if (mode == SINKS && groups >= 256 && 2 * span <= full) splits = 1;  // alike long, most of them: 45 -> 36 us, 64 x 2112 tokens
+        if (mode == OWN && groups >= 256 && span <= 2 * FAR) splits = 1;     // then no join, 12 us for 64 sequences of 8 heads
+    }
     p.nw = p.tr == 16 && splits > 1 && wide(groups, span) ? WIDE : 4;
     if (p.nw == WIDE) splits = 1;
+    if (p.tr == 16)
+        us = 6.0f + (float)groups * span * p.a.geo.d * (17.0f / 16.0f) / (p.a.geo.d == 128 ? 7.9e6f : 5.8e6f) +
+             (mode == WHOLE && splits > 1 ? 4.0f : 0.0f);
     const int64_t unit = p.tr > 16 ? CT : p.nw * TT;
     const int64_t chunk = ((span + splits - 1) / splits + unit - 1) / unit * unit;
     p.chunk = (int)chunk;
     p.splits = (int)((span + chunk - 1) / chunk);
     p.work = (int)(groups * p.splits);  // below 2^23
     p.blanks = 0;
+    return us;
 }
 
 DecArgs args_of(const Kv4Attn &a) {
@@ -1017,27 +1033,48 @@ DecArgs args_of(const Kv4Attn &a) {
     return p;
 }
 
-// The two parts of a call with a shared prefix, and the bytes of their partial results: OWN's, if it has more than one
-// split, then PREFIX's.
-size_t plan_shared(const Kv4Attn &a, DecArgs &pre, DecArgs &own) {
+// A call with shared pages: in two parts, or (`whole`) as one; and the bytes of its partial results, OWN's or WHOLE's,
+// if they leave any, then PREFIX's.
+struct SharedPlan {
+    DecArgs pre, own;
+    bool whole;
+    size_t bytes;
+};
+SharedPlan plan_shared(const Kv4Attn &a) {
+    SharedPlan s;
     const int g = a.hq / a.geo.hkv, row = (a.geo.d + 4) * 4;
-    pre = own = args_of(a);
-    tiles_of(a.nq, g, a.geo.d, pre);
-    tiles_of(a.max_q, g, a.geo.d, own);
-    const int64_t pg = (int64_t)a.geo.hkv * pre.rt, og = (int64_t)a.b * a.geo.hkv * own.rt;
-    const int64_t shared = (int64_t)a.shared << a.geo.page_log2, rest = (((int64_t)a.width - a.shared) << a.geo.page_log2) + TT;
-    split(pre, pg, shared, shared, PREFIX);
-    // A wave of the many-rows kernel reads its rows' results one split after the other, about 1 us each, and the decode
-    // kernel's waves take turns: 32 splits of 912 rows a head were 60 us where a join takes 8, 183 of 25 rows 25.
-    split(own, og, rest, rest, own.tr == 16 || pre.splits <= 8 ? OWN : PREFIX);
-    own.takes = own.splits == 1 && pre.splits <= 8 * (own.tr == 16 ? own.nw : 1);
-    const size_t first = !own.takes ? ((size_t)(og * own.splits) * own.pr * row + 255) & ~(size_t)255 : 0;
-    pre.part = reinterpret_cast<float *>(a.ws + first);
-    own.ptr_ = pre.tr;
-    own.ppr = pre.pr;
-    own.psplits = pre.splits;
-    own.ppart = pre.part;
-    return first + (size_t)(pg * pre.splits) * pre.pr * row;
+    s.pre = s.own = args_of(a);
+    tiles_of(a.nq, g, a.geo.d, s.pre);
+    tiles_of(a.max_q, g, a.geo.d, s.own);
+    const int64_t pg = (int64_t)a.geo.hkv * s.pre.rt, og = (int64_t)a.b * a.geo.hkv * s.own.rt;
+    const int64_t shared = (int64_t)a.shared << a.geo.page_log2, all = (int64_t)a.width << a.geo.page_log2, rest = all - shared + TT;
+    // OWN takes PREFIX's results in, one split after the other in a wave, about 1 us each; or a join does, 6 us and their bytes
+    float two = split(s.pre, pg, shared, shared, PREFIX);
+    DecArgs joined = s.own, one = s.own;
+    const float taken = split(s.own, og, rest, rest, OWN) +
+                        (s.own.tr == 16 ? 1.2f * ((s.pre.splits + s.own.nw - 1) / s.own.nw) : 1.0f * s.pre.splits);
+    const float left = split(joined, og, rest, rest, PREFIX) + 6.0f +
+                       (float)a.nq * a.hq * (s.pre.splits + joined.splits) * row / 4.8e6f;
+    s.own.takes = s.own.splits == 1 && taken <= left;
+    if (!s.own.takes) s.own = joined;
+    two += s.own.takes ? taken : left;
+    // Two parts | one, us, heads of 128 in groups of four over 8, 16384 shared tokens: 28 | 15 for one single token, 27 | 29
+    // for 8, 30 | 47 for 16, 47 | 146 for 64; 2048: 14 | 13 for 8, 27 | 33 for 64; 8 x 40 tokens 44 | 40 behind 2048, 107 | 153
+    // behind 16384.
+    s.whole = split(one, og, all, all, WHOLE) <= two;
+    if (s.whole) {
+        s.own = one;
+        s.bytes = one.splits > 1 ? (size_t)(og * one.splits) * one.pr * row : 0;
+        return s;
+    }
+    const size_t first = !s.own.takes ? ((size_t)(og * s.own.splits) * s.own.pr * row + 255) & ~(size_t)255 : 0;
+    s.pre.part = reinterpret_cast<float *>(a.ws + first);
+    s.own.ptr_ = s.pre.tr;
+    s.own.ppr = s.pre.pr;
+    s.own.psplits = s.pre.splits;
+    s.own.ppart = s.pre.part;
+    s.bytes = first + (size_t)(pg * s.pre.splits) * s.pre.pr * row;
+    return s;
 }
 
 template <int MODE>
@@ -1110,7 +1147,7 @@ hipError_t launch_kv4_attn(const Kv4Attn &a, hipStream_t s) {
     return sinks ? attend_and_join<SINKS>(p, s) : attend_and_join<PLAIN>(p, s);
 }
 
-size_t kv4_attn_shared_ws_bytes(int64_t nq, int b, int max_q, int hq, const Kv4Geom &g, int width, int shared) {
+static SharedPlan plan_shared(int64_t nq, int b, int max_q, int hq, const Kv4Geom &g, int width, int shared) {
     Kv4Attn a{};
     a.geo = g;
     a.nq = (int)nq;
@@ -1119,17 +1156,25 @@ size_t kv4_attn_shared_ws_bytes(int64_t nq, int b, int max_q, int hq, const Kv4G
     a.hq = hq;
     a.width = width;
     a.shared = shared;
-    DecArgs pre, own;
-    return plan_shared(a, pre, own);
+    return plan_shared(a);
+}
+int kv4_attn_shared_parts(int64_t nq, int b, int max_q, int hq, const Kv4Geom &g, int width, int shared) {
+    return plan_shared(nq, b, max_q, hq, g, width, shared).whole ? 1 : 2;
+}
+size_t kv4_attn_shared_ws_bytes(int64_t nq, int b, int max_q, int hq, const Kv4Geom &g, int width, int shared) {
+    return plan_shared(nq, b, max_q, hq, g, width, shared).bytes;
 }
 
 hipError_t launch_kv4_attn_shared(const Kv4Attn &a, hipStream_t s) {
-    DecArgs pre, own;
-    plan_shared(a, pre, own);
-    own.blanks = blanks_of(a);
-    hipError_t e = launch_attend<PREFIX>(pre, s);
-    if (e == hipSuccess) e = launch_attend<OWN>(own, s);
-    return e == hipSuccess && !own.takes ? launch_join<OWN>(own, s) : e;
+    SharedPlan p = plan_shared(a);
+    p.own.blanks = blanks_of(a);
+    if (p.whole) {
+        const hipError_t e = launch_attend<WHOLE>(p.own, s);
+        return e == hipSuccess && p.own.splits > 1 ? launch_join<PLAIN>(p.own, s) : e;
+    }
+    hipError_t e = launch_attend<PREFIX>(p.pre, s);
+    if (e == hipSuccess) e = launch_attend<OWN>(p.own, s);
+    return e == hipSuccess && !p.own.takes ? launch_join<OWN>(p.own, s) : e;
 }
 
 }  // namespace fp4

@@ -41,7 +41,7 @@ class Case:
         k, v = kv(self.pages * page, hkv, d, seed + 1)
         k = k * kmul
         fp4.kv4_write(self.cache, k.to(DEV), v.to(DEV), torch.arange(self.pages * page, device=DEV))
-        self.kc, self.vc = ref.cache_values(f64(k)), ref.cache_values(f64(v))
+        self.kc, self.vc = (torch.from_numpy(ref.cache_values(f64(x))).to(DEV) for x in (k, v))
         self.lens, self.starts = list(lens), [0]
         for q in qlens:
             self.starts.append(self.starts[-1] + q)
@@ -58,33 +58,37 @@ class Case:
     def want(self, window=0, sinks=0, scale=None, max_q=None):
         """o, lse and the magnitudes behind them."""
         nq, hq, d = self.q.shape
-        q, table = f64(self.q), self.table.numpy()
+        q, table = self.q.to(DEV).double(), self.table.to(DEV).long()
         scale = d ** -0.5 if scale is None else scale
-        o, lse = np.zeros(q.shape), np.full((nq, hq), -np.inf)
-        omag, smag = np.zeros(q.shape), np.zeros((nq, hq))
+        z = lambda *n: torch.zeros(*n, dtype=torch.float64, device=DEV)  # noqa: E731
+        o, lse, omag, smag = z(nq, hq, d), z(nq, hq) - np.inf, z(nq, hq, d), z(nq, hq)
+        g = hq // self.hkv
         for i, n in enumerate(self.lens):
-            cap = min(max(n, 0), self.width * self.page)
-            t = np.arange(cap)
-            pg = np.where(t // self.page < self.shared, table[0, t // self.page], table[i, t // self.page]) if cap else t
+            t = torch.arange(min(max(n, 0), self.width * self.page), device=DEV)
+            pg = table[i, t // self.page]
+            pg = torch.where(t < self.shared * self.page, table[0, t // self.page], pg)
             ql = self.starts[i + 1] - self.starts[i]
-            for j in range(min(ql, max_q or self.max_q)):
-                pos = max(n, 0) - ql + j
-                see = (t <= pos) & (pg >= 0) & (pg < self.pages)
-                if window:
-                    see &= (t > pos - window) | (t < sinks)
-                if not see.any():
-                    continue
-                slot, row = pg[see] * self.page + t[see] % self.page, self.starts[i] + j
-                kk, vv = self.kc[slot], self.vc[slot]
-                for h in range(hq):
-                    g = h // (hq // self.hkv)
-                    s = kk[:, g] @ q[row, h] * scale
-                    m = s.max()
-                    p = np.exp(s - m)
-                    lse[row, h] = m + np.log(p.sum())
-                    o[row, h], omag[row, h] = p @ vv[:, g] / p.sum(), p @ np.abs(vv[:, g]) / p.sum()
-                    smag[row, h] = (np.abs(kk[:, g]) @ np.abs(q[row, h])).max() * abs(scale)
-        return o, lse, omag, smag
+            m = min(ql, max_q or self.max_q)
+            rows = slice(self.starts[i], self.starts[i] + m)
+            pos = max(n, 0) - ql + torch.arange(m, device=DEV)
+            see = (t <= pos[:, None]) & (pg >= 0) & (pg < self.pages)
+            if window:
+                see &= (t > pos[:, None] - window) | (t < sinks)
+            slot = pg.clamp(0, self.pages - 1) * self.page + t % self.page
+            some = see.any(1)
+            if m == 0 or t.numel() == 0:
+                continue
+            for h in range(self.hkv):
+                hs = slice(h * g, h * g + g)
+                kk, vv, qq = self.kc[slot, h], self.vc[slot, h], q[rows, hs].reshape(-1, d)
+                hide = ~see.repeat_interleave(g, 0)
+                s = (qq @ kk.t() * scale).masked_fill(hide, -np.inf)
+                zz = torch.logsumexp(s, 1)
+                p = torch.exp(s - torch.where(zz == -np.inf, torch.zeros_like(zz), zz)[:, None])
+                lse[rows, hs] = torch.where(some[:, None], zz.view(m, g), lse[rows, hs])
+                o[rows, hs], omag[rows, hs] = (p @ vv).view(m, g, d), (p @ vv.abs()).view(m, g, d)
+                smag[rows, hs] = (qq.abs() @ kk.abs().t() * abs(scale)).masked_fill(hide, 0).amax(1).view(m, g)
+        return tuple(x.cpu().numpy() for x in (o, lse, omag, smag))
 
     def check(self, window=0, sinks=0, scale=None, max_q=None, **kw):
         if window or sinks:
@@ -217,6 +221,29 @@ def test_shared_sizes(d):
     Case([300, 256, 280], [60, 60, 60], 8, 2, d, 64, shared=4, width=4).check()
 
 
+def parts(c):
+    nq, hq, d = c.q.shape
+    return fp4.lib().fp4_kv4_attention_shared_parts(nq, len(c.lens), c.max_q, hq, c.hkv, d, c.page, c.width, c.shared)
+
+
+@pytest.mark.parametrize("b,t,hq,hkv,d,page,shared,own", [
+    (8, 1, 8, 8, 128, 64, 256, 100), (30, 1, 8, 8, 64, 32, 256, 60), (16, 1, 16, 8, 128, 16, 512, 60), (64, 1, 32, 8, 128, 64, 64, 100),
+    (70, 1, 8, 4, 64, 32, 200, 300), (32, 1, 8, 8, 64, 16, 301, 200), (5, 1, 8, 8, 128, 64, 512, 30), (40, 1, 24, 8, 64, 32, 512, 3000),
+    (24, 40, 8, 8, 64, 64, 128, 100), (16, 40, 16, 4, 128, 32, 513, 1000), (64, 5, 12, 4, 64, 64, 256, 50), (64, 8, 32, 8, 128, 128, 16, 20)])
+def test_shared_in_two_parts(b, t, hq, hkv, d, page, shared, own):
+    """Sizes at which the shared bytes are read once: few and many rows of either part, splits joined and taken in;
+    sequences that end inside the shared pages or hold nothing, and unlike numbers of queries."""
+    p = shared * page
+    lens = [p + t + own * (i * 7 % b) // b for i in range(b)]
+    c = Case(lens, [t - i * 3 % t for i in range(b)], hq, hkv, d, page, shared, seed=b)
+    assert parts(c) == 2
+    c.check()
+    c.lens[1], c.lens[2], c.lens[3], c.lens[b - 1] = p - page - 3, 0, p, 7
+    c.check()
+    c.table[:, 1], c.table[0, shared - 1], c.table[b // 2, shared] = -1, c.pages, -5
+    c.check(scale=-0.05)
+
+
 def test_shared_is_row_0s():
     """The other rows' first entries are not those that count; results are the plain call's within the roundings."""
     for qlens in ([1] * 5, [30, 1, 64, 5, 17]):
@@ -233,27 +260,33 @@ def test_shared_is_row_0s():
 
 def test_shared_rows_of_no_sequence():
     """A padded batch: rows before, between (past max_q) and behind the sequences get zeros and lse -inf."""
-    for qlens, mq in (([3, 1, 6], 3), ([70, 30, 50], 40)):
-        c = Case([200, 180, 170], qlens, 4, 2, 64, 16, shared=5, tail=9)
+    for qlens, mq, b in (([3, 1, 6], 3, 3), ([70, 30, 50], 40, 3), ([2, 1, 3], 2, 60), ([30, 1, 17], 20, 48)):
+        c = Case(([200, 180, 170] if b == 3 else [8200, 8260, 8230]) * (b // 3), qlens * (b // 3), 8, 4, 64, 16,
+                 shared=5 if b == 3 else 512, tail=9)
+        assert parts(c) == (1 if b == 3 else 2)
         c.check(max_q=mq)
         starts = i32([s + 4 for s in c.starts])
         o, lse = c.run(q_start=starts, max_q=max(qlens), q=torch.cat([c.q[-4:], c.q[:-4]]).to(DEV))
         want = c.run(max_q=max(qlens))
         n = c.starts[-1]
         assert torch.equal(o[4:4 + n], want[0][:n]) and torch.equal(lse[4:4 + n], want[1][:n])
-        assert float(o[:4].abs().sum()) == 0 and bool((lse[4 + n:] == -float("inf")).all())
+        assert float(o[:4].abs().sum()) == 0 and float(o[4 + n:].abs().sum()) == 0
+        assert bool((lse[:4] == -float("inf")).all()) and bool((lse[4 + n:] == -float("inf")).all())
 
 
 def test_shared_bad_pages_and_nonfinite_tokens():
-    for qlens in ([1, 2], [50, 64]):
-        c = Case([300, 222], qlens, 4, 2, 128, 32, shared=4)
-        c.table[:, 1], c.table[1, 5] = -1, c.pages
+    for qlens, pre in (([1, 2], 4), ([50, 64], 4), ([1, 2] * 16, 400), ([30, 20] * 24, 300)):
+        c = Case([32 * pre + 172, 32 * pre + 94] * (len(qlens) // 2), qlens, 4 if pre == 4 else 16, 2 if pre == 4 else 4, 128, 32,
+                 shared=pre)
+        assert parts(c) == (1 if pre == 4 else 2)
+        c.table[:, 1], c.table[1, pre + 1] = -1, c.pages
         c.check()
-        bad = torch.full((1, 2, 128), float("inf"), device=DEV)
-        bad[:, 0] = 1
+        bad = torch.full((1, c.hkv, 128), float("inf"), device=DEV)
+        bad[:, :c.hkv // 2] = 1
         fp4.kv4_write(c.cache, bad, bad, torch.tensor([int(c.table[0, 0]) * 32 + 7], device=DEV))
         o, _ = c.run()
-        assert bool(o[:, 2:].isnan().all()) and bool(o[:, :2].isfinite().all())
+        half = o.shape[1] // 2
+        assert bool(o[:, half:].isnan().all()) and bool(o[:, :half].isfinite().all())
 
 
 @pytest.mark.parametrize("qlens", [[1, 1], [40, 70]])
@@ -275,23 +308,28 @@ def test_shared_scales_and_strides(qlens):
 def test_workspaces_are_enough():
     """The stated bytes suffice (nothing behind them is written), for splits of either part."""
     for lens, qlens, shared, page in (([5000, 4000], [1, 1], 60, 32), ([700] * 30, [3] * 30, 20, 32), ([9000], [2], 1, 64),
-                                      ([400, 333], [100, 90], 3, 64)):
-        c = Case(lens, qlens, 8, 2, 64, page, shared=shared)
+                                      ([400, 333], [100, 90], 3, 64), ([8200 + 9 * i for i in range(40)], [1] * 40, 128, 64),
+                                      ([5200 + 30 * i for i in range(40)], [5] * 40, 80, 64)):
+        c = Case(lens, qlens, 32 if len(lens) == 40 else 8, 8 if len(lens) == 40 else 2, 64, page, shared=shared)
+        assert parts(c) == (2 if len(lens) == 40 else 1)
         n = fp4.kv4_attention_workspace(c.q.to(DEV), c.cache, c.table.to(DEV), c.max_q, shared).numel()
         ws = torch.full((n + 4096,), 77, dtype=torch.uint8, device=DEV)
         got = c.run(ws=ws[:n])
         assert bool((ws[n:] == 77).all()) and torch.equal(got[0], c.run()[0])
-        with pytest.raises(fp4.Fp4Error):
-            c.run(ws=ws[:n - 16] if n > 16 else ws[:0])
+        if n > 16:
+            with pytest.raises(fp4.Fp4Error):
+                c.run(ws=ws[:n - 16])
 
 
 def test_repeated_streamed_and_captured():
     """Replays with other lengths (shorter than the shared pages too), each against the eager call; two graphs on one
     workspace, one after the other."""
-    c = Case([900, 777, 640], [1, 1, 1], 8, 2, 128, 64, shared=8)
+    b, sh = 48, 64
+    c = Case([4500, 4196, 4100] * 16, [1] * b, 32, 8, 128, 64, shared=sh)
+    assert parts(c) == 2
     q, table, lens = c.q.to(DEV), c.table.to(DEV), i32(c.lens)
-    ws = max((fp4.kv4_attention_workspace(q, c.cache, table, shared=n) for n in (0, 8)), key=len)
-    calls = [lambda: fp4.kv4_attention(q, c.cache, table, lens, return_lse=True, ws=ws, shared=8),
+    ws = max((fp4.kv4_attention_workspace(q, c.cache, table, shared=n) for n in (0, sh)), key=len)
+    calls = [lambda: fp4.kv4_attention(q, c.cache, table, lens, return_lse=True, ws=ws, shared=sh),
              lambda: fp4.kv4_attention(q, c.cache, table, lens, return_lse=True, ws=ws, window=100, sinks=20)]
     s = torch.cuda.Stream()
     s.wait_stream(torch.cuda.current_stream())
@@ -306,8 +344,8 @@ def test_repeated_streamed_and_captured():
         with torch.cuda.graph(g):
             outs.append(f())
         graphs.append(g)
-    for new in ([900, 777, 640], [3, 0, 512], [513, 1, 900]):
-        lens.copy_(i32(new))
+    for new in ([4500, 4196, 4100], [3, 0, 4096], [4097, 1, 4500]):
+        lens.copy_(i32(new * 16))
         for g in graphs:
             g.replay()
         torch.cuda.synchronize()

@@ -119,19 +119,21 @@ def test_sinks_and_shared_reject():
         return L.fp4_kv4_attention_sinks(q, 1024, 128, 1, 8, None, FAKE, 1, 1, FAKE, 64, 64, FAKE, 64, 16, 2, 128, win, sinks, 0.1, FAKE,
                                          None, ws, n, None)
     assert s(sinks=-1) == ESHAPE and s(win=-1) == ESHAPE and s(n=need - 1) == EWS and s(q=None) == ENULL and s(ws=ODD) == EALIGN
-    size = lambda nq=1, b=1, mq=1, hq=8, hkv=2, d=128, page=16, width=64, sh=8: \
-        L.fp4_kv4_attention_shared_workspace_bytes(nq, b, mq, hq, hkv, d, page, width, sh)  # noqa: E731
+    big = dict(nq=64, b=64, mq=1, hq=32, hkv=8, d=128, page=64, width=80, sh=64)
+    size, parts = ((lambda fn: lambda **kw: fn(*({**big, **kw}.values())))(fn) for fn in (
+        L.fp4_kv4_attention_shared_workspace_bytes, L.fp4_kv4_attention_shared_parts))
     need = size()
-    assert need > 0
-    for kw in (dict(nq=0), dict(b=0), dict(mq=0), dict(hq=7), dict(d=96), dict(page=24), dict(sh=0), dict(sh=65), dict(nq=1 << 24),
+    assert need > 0 and parts() == 2
+    assert parts(nq=1, b=1) == 1 and parts(nq=4, b=4, width=6, sh=4) == 1     # nothing to save
+    for kw in (dict(nq=0), dict(b=0), dict(mq=0), dict(hq=12), dict(d=96), dict(page=24), dict(sh=0), dict(sh=81), dict(nq=1 << 24),
                dict(nq=(1 << 22) + 1)):
-        assert size(**kw) == 0, kw
+        assert size(**kw) == 0 and parts(**kw) == 0, kw
 
-    def f(q=FAKE, nq=1, hq=8, qs=None, b=1, mq=1, ts=64, width=64, sh=8, o=FAKE, ws=FAKE, n=need):
-        return L.fp4_kv4_attention_shared(q, 1024, 128, nq, hq, qs, FAKE, b, mq, FAKE, ts, width, FAKE, 64, 16, 2, 128, sh, 0.1, o, None,
-                                          ws, n, None)
+    def f(q=FAKE, nq=64, hq=32, qs=None, b=64, mq=1, ts=80, width=80, sh=64, o=FAKE, ws=FAKE, n=need):
+        return L.fp4_kv4_attention_shared(q, 4096, 128, nq, hq, qs, FAKE, b, mq, FAKE, ts, width, FAKE, 9000, 64, 8, 128, sh, 0.1, o,
+                                          None, ws, n, None)
     assert f(q=None) == ENULL and f(o=None) == ENULL and f(ws=None) == ENULL and f(n=need - 1) == EWS
-    for kw in (dict(sh=0), dict(sh=65), dict(hq=7), dict(ts=63), dict(nq=2), dict(nq=0, qs=FAKE), dict(mq=2)):
+    for kw in (dict(sh=0), dict(sh=81), dict(hq=12), dict(ts=79), dict(nq=2), dict(nq=0, qs=FAKE), dict(mq=2)):
         assert f(**kw) == ESHAPE, kw
     assert f(q=ODD) == EALIGN and f(o=HALF) == EALIGN and f(ws=HALF) == EALIGN
 
