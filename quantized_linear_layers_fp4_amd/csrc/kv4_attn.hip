@@ -1,6 +1,6 @@
 // Attention of packed queries over the 4-bit paged cache (layout: kv4.h).
 //
-//      s = scale * q . k   over the visible tokens: j <= p, and j > p - window if there is a window
+//      s = scale * q . k   over the visible tokens: j <= p, and if there is a window j > p - window or j < sinks
 //      o = sum softmax(s) v,   lse = log sum exp s
 //
 // Query i of a sequence with len tokens in the cache and qlen queries stands at p = len - qlen + i.
@@ -395,8 +395,8 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? 3 : 1) void k_kv4_decode(DecArgs
 #pragma unroll
             for (int r = 0; r < 4; ++r) x[4 * s + r] = d[r] * p.c;
         }
-        const bool before = t0 < sp.full_lo && !(MODE == SINKS && t0 + TT <= a.sinks);
-        if (okm != ~0ull || before || t0 + TT > min(sp.full_hi, stop)) {  // some token is masked
+        if (okm != ~0ull || (t0 < sp.full_lo && !(MODE == SINKS && t0 + TT <= a.sinks)) ||
+            t0 + TT > min(sp.full_hi, stop)) {  // some token is masked
             const bool okp = ((okm >> (4 * h)) & 1) != 0;  // of the lane's score tokens' page
             const int hi = okp ? min(vhi, stop) : 0;
 #pragma unroll
@@ -550,7 +550,7 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? 3 : 1) void k_kv4_decode(DecArgs
 // Eight waves a CU in either size.  2 x 1024 queries of 32 heads over 8192 tokens (d 128, 8 key/value heads), us:
 // 16 rows a wave 700; this with four waves 362, page indices looked up a tile earlier 341, the maximum
 // in one instruction for two scores 322; with eight waves, which halves a thread's unpacking, and bytes two
-// tiles ahead 305 (short runs; 276 once the clock is up, 0.93 PFLOP/s).  Of a busy CU's cycles matrix instructions
+// tiles ahead 305 (short runs; 276 once the clock is up), with scalar pages and addresses 268 (0.96 PFLOP/s).  Of a busy CU's cycles matrix instructions
 // take 44 %, vector instructions (the exponentials first) 61 % and LDS 34 %: a deeper interleaving within a wave
 // (64 rows, 512 registers) was slower.
 template <int D, int NT, int MODE>
