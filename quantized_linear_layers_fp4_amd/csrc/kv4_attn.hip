@@ -157,9 +157,30 @@ __device__ __forceinline__ int owner_of(const Kv4Attn &a, int query) {
     return lo - 1;
 }
 
-// OWN: PREFIX's first partial result of a row of the call's; the next ones are ppr * (d + 4) floats on.
-__device__ __forceinline__ const float *prefix_part(const DecArgs &p, int head, int64_t row) {
-    return p.ppart + ((row / p.ptr_ * p.a.geo.hkv + head) * p.psplits * p.ppr + row % p.ptr_) * (p.a.geo.d + 4);
+// PREFIX's partial result of a row of the call's, for OWN and the join: column c of split s is sums[s * split + (c / 8) *
+// eight + c % 8], and the maximum and sum ml[s * split].  The decode kernel leaves a row's d columns side by side (eight = 8); the
+// many-rows kernel eight columns of 32 rows, which is 1 KB of a wave's store instruction (row by row it wrote pieces of 32
+// bytes: 53 against 49 us for 256 rows a head over 32768 tokens).
+struct PrefixRow {
+    const float *sums, *ml;
+    int64_t split;
+    int eight;
+};
+__device__ __forceinline__ PrefixRow prefix_row(const DecArgs &p, int head, int64_t row) {
+    const int d = p.a.geo.d, r = (int)(row % p.ptr_);
+    const float *block = p.ppart + (row / p.ptr_ * p.a.geo.hkv + head) * p.psplits * p.ppr * (d + 4);
+    PrefixRow x;
+    x.split = (int64_t)p.ppr * (d + 4);
+    x.eight = p.ptr_ > 16 ? 256 : 8;
+    if (p.ptr_ > 16) {
+        block += (r >> 5) * 32 * (d + 4);
+        x.sums = block + (r & 31) * 8;
+        x.ml = block + 32 * d + (r & 31) * 2;
+    } else {
+        x.sums = block + r * (d + 4);
+        x.ml = x.sums + d;
+    }
+    return x;
 }
 
 // PREFIX: whether some sequence has queries that do not see all shared tokens (all threads of the workgroup call it).
@@ -446,15 +467,15 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? 3 : 1) void k_kv4_decode(DecArgs
     // OWN: the shared tokens' partial results, by turns of the waves: columns (4 h + r) J .. + J - 1 of the row, as
     // acc holds them
     auto take_prefix = [&] {
-        const float *w = prefix_part(p, head, (int64_t)sp.qbeg * p.g + row) + 4 * h * J;
+        const PrefixRow w = prefix_row(p, head, (int64_t)sp.qbeg * p.g + row);
         if (p.takes && live) {
 #pragma unroll 2
             for (int s = wave; s < p.psplits; s += NW) {
-                const float *ws = w + (int64_t)s * p.ppr * (D + 4);
-                const float2 ml = *reinterpret_cast<const float2 *>(ws + D - 4 * h * J);
+                const float *ws = w.sums + s * w.split + (h * J / 2) * w.eight;
+                const float2 ml = *reinterpret_cast<const float2 *>(w.ml + s * w.split);
                 float4 v[J];
 #pragma unroll
-                for (int i = 0; i < J; ++i) v[i] = *reinterpret_cast<const float4 *>(ws + 4 * i);
+                for (int i = 0; i < J; ++i) v[i] = *reinterpret_cast<const float4 *>(ws + (i >> 1) * w.eight + 4 * (i & 1));
                 const float nm = fmaxf(m, ml.x), mu = nm == -INFINITY ? 0.0f : nm;
                 const float f0 = __builtin_amdgcn_exp2f(m - mu), f1 = __builtin_amdgcn_exp2f(ml.x - mu);
                 m = nm;
@@ -818,10 +839,11 @@ __global__ __launch_bounds__(NT, 2) void k_kv4_chunk(DecArgs p) {
     if (!live) return;
     float ms = m == -INFINITY ? m : m * c;  // of the scaled scores
     if constexpr (MODE == OWN) {
-        const float *w = prefix_part(p, head, (int64_t)sp.qbeg * p.g + row);
+        const PrefixRow w = prefix_row(p, head, (int64_t)sp.qbeg * p.g + row);
         if (p.takes) {
-            for (int s = 0; s < p.psplits; ++s, w += (int64_t)p.ppr * (D + 4)) {
-                const float2 ml = *reinterpret_cast<const float2 *>(w + D);
+            for (int s = 0; s < p.psplits; ++s) {
+                const float *ws = w.sums + s * w.split + 4 * h;
+                const float2 ml = *reinterpret_cast<const float2 *>(w.ml + s * w.split);
                 const float nm = fmaxf(ms, ml.x), mu = nm == -INFINITY ? 0.0f : nm;
                 const float f0 = __builtin_amdgcn_exp2f(ms - mu), f1 = __builtin_amdgcn_exp2f(ml.x - mu);
                 ms = nm;
@@ -830,7 +852,7 @@ __global__ __launch_bounds__(NT, 2) void k_kv4_chunk(DecArgs p) {
                 for (int j = 0; j < DT; ++j)
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
-                        const float4 v = *reinterpret_cast<const float4 *>(w + 32 * j + 8 * q + 4 * h);
+                        const float4 v = *reinterpret_cast<const float4 *>(ws + (4 * j + q) * w.eight);
                         const float x[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                         for (int u = 0; u < 4; ++u) acc[j][4 * q + u] = acc[j][4 * q + u] * f0 + x[u] * f1;
@@ -852,16 +874,18 @@ __global__ __launch_bounds__(NT, 2) void k_kv4_chunk(DecArgs p) {
         if (a.lse && h == 0) a.lse[out] = l == 0.0f ? -INFINITY : (ms + __builtin_amdgcn_logf(l)) * LN2;
     } else {
         float *w = p.part +
-                   (((((int64_t)seq * p.rt + rt) * a.geo.hkv + head) * p.splits + split) * p.pr + wave * 32 + n) * (D + 4);
+                   (((((int64_t)seq * p.rt + rt) * a.geo.hkv + head) * p.splits + split) * p.pr + wave * 32) * (D + 4);
+        float *ml = w + (MODE == PREFIX ? 32 * D + n * 2 : n * (D + 4) + D);  // (PREFIX: as PrefixRow says)
+        w += MODE == PREFIX ? n * 8 : n * (D + 4);
 #pragma unroll
         for (int j = 0; j < DT; ++j)
 #pragma unroll
             for (int q = 0; q < 4; ++q)
-                *reinterpret_cast<float4 *>(w + 32 * j + 8 * q + 4 * h) =
+                *reinterpret_cast<float4 *>(w + (4 * j + q) * (MODE == PREFIX ? 256 : 8) + 4 * h) =
                     make_float4(acc[j][4 * q], acc[j][4 * q + 1], acc[j][4 * q + 2], acc[j][4 * q + 3]);
         if (h == 0) {
-            w[D] = ms;
-            w[D + 1] = l;
+            ml[0] = ms;
+            ml[1] = l;
         }
     }
 }
@@ -886,18 +910,16 @@ __global__ __launch_bounds__(256) void k_kv4_join(DecArgs p) {
     const int ns = sp.hi > sp.lo ? (sp.hi - sp.lo + p.chunk - 1) / p.chunk : 0;
     const int64_t SS = (int64_t)p.pr * (D + 4);
     const float *w = p.part + ((((int64_t)seq * p.rt + rt) * a.geo.hkv + head) * p.splits * p.pr + r) * (D + 4);
-    const float *pw = nullptr;  // the shared tokens' partial results of the row
-    const int64_t PS = (int64_t)p.ppr * (D + 4);
-    if constexpr (MODE == OWN) {
-        pw = prefix_part(p, head, (int64_t)sp.qbeg * p.g + row);
-    }
+    PrefixRow pw{};  // the shared tokens' partial results of the row
+    if constexpr (MODE == OWN) pw = prefix_row(p, head, (int64_t)sp.qbeg * p.g + row);
     float M = -INFINITY, Lsum = 0.0f, o[4] = {0, 0, 0, 0};
     const int parts = MODE == OWN ? ns + p.psplits : ns;
 #pragma unroll 4
     for (int s = grp; s < parts; s += G) {
-        const float *ws = MODE == OWN && s >= ns ? pw + (s - ns) * PS : w + s * SS;
-        const float4 v = *reinterpret_cast<const float4 *>(ws + lane * 4);
-        const float2 ml = *reinterpret_cast<const float2 *>(ws + D);
+        const bool pre = MODE == OWN && s >= ns;
+        const float *ws = pre ? pw.sums + (s - ns) * pw.split + (lane >> 1) * pw.eight + (lane & 1) * 4 : w + s * SS + lane * 4;
+        const float4 v = *reinterpret_cast<const float4 *>(ws);
+        const float2 ml = *reinterpret_cast<const float2 *>(pre ? pw.ml + (s - ns) * pw.split : w + s * SS + D);
         const float nm = fmaxf(M, ml.x), mu = nm == -INFINITY ? 0.0f : nm;
         const float f0 = __builtin_amdgcn_exp2f(M - mu), f1 = __builtin_amdgcn_exp2f(ml.x - mu);
         M = nm;
@@ -1045,6 +1067,7 @@ SharedPlan plan_shared(const Kv4Attn &a) {
     const int g = a.hq / a.geo.hkv, row = (a.geo.d + 4) * 4;
     s.pre = s.own = args_of(a);
     tiles_of(a.nq, g, a.geo.d, s.pre);
+    if (s.pre.tr > 16) s.pre.pr = (s.pre.pr + 31) & ~31;  // whole waves' rows
     tiles_of(a.max_q, g, a.geo.d, s.own);
     const int64_t pg = (int64_t)a.geo.hkv * s.pre.rt, og = (int64_t)a.b * a.geo.hkv * s.own.rt;
     const int64_t shared = (int64_t)a.shared << a.geo.page_log2, all = (int64_t)a.width << a.geo.page_log2, rest = all - shared + TT;
