@@ -97,20 +97,21 @@ __device__ __forceinline__ void values(const Raw<DT> &r, float (&v)[8]) {
     }
 }
 
-// The values that the lane's are paired with: of another lane, or its own neighbours.
+// The values that the lane's are paired with: of another lane, or its own neighbours; zeros where the lane's columns are not
+// rotated (`mask` 0 instead of ~0).  They stand there beside a sine of 0, and an infinity would make that NaN.
 template <int DT, bool IL>
-__device__ __forceinline__ void partners(const Raw<DT> &r, int from, float (&v)[8]) {
+__device__ __forceinline__ void partners(const Raw<DT> &r, int from, uint32_t mask, float (&v)[8]) {
+    Raw<DT> p;
+#pragma unroll
+    for (int q = 0; q < (DT == DT_BF16 ? 1 : 2); ++q)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) p.w[q][i] = (IL ? r.w[q][i] : (uint32_t)__shfl((int)r.w[q][i], from, 64)) & mask;
     if constexpr (IL) {
         float u[8];
-        values<DT>(r, u);
+        values<DT>(p, u);
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = u[i ^ 1];
     } else {
-        Raw<DT> p;
-#pragma unroll
-        for (int q = 0; q < (DT == DT_BF16 ? 1 : 2); ++q)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) p.w[q][i] = (uint32_t)__shfl((int)r.w[q][i], from, 64);
         values<DT>(p, v);
     }
 }
@@ -144,12 +145,12 @@ __device__ __forceinline__ void weights_at(const NormRope &a, const void *w, int
     }
 }
 
-// A lane's part of a token: its columns, their partners' place, the angles.  State 0: rows of zeros (a negative
-// position); 1: as computed.  A position past the table gives NaN angles.
+// A lane's part of a token: its columns, their partners' place, the angles.  A position past the table gives NaN angles.
 template <bool IL>
 struct Turn {
     int col;         // first of the lane's 8 columns
-    bool live, zero; // its columns are the row's; the token's rows are zeros
+    bool live, zero; // its columns are the row's; the token's rows are zeros (a negative position)
+    uint32_t mask;   // ~0 if its columns are rotated (all eight are, or none), else 0
     int from;        // lane of the partners
     float c[8], s[8];
 
@@ -157,6 +158,7 @@ struct Turn {
         col = lane * 8;
         live = col < a.d;
         zero = false;
+        mask = col < a.rot ? ~0u : 0u;
         const int me = threadIdx.x & 63, half = a.rot / 16;
         from = IL || lane >= 2 * half ? me : lane < half ? me + half : me - half;
 #pragma unroll
@@ -197,7 +199,8 @@ struct Turn {
     }
 };
 
-// A token's weights times its angles: y = r (x u + partner v).
+// A token's weights times its angles: y = r (x u + partner v).  Where the lane's columns are not rotated, partners are 0, u is
+// the weight and v -0, so that y is r x u, a zero's sign with it.
 template <bool IL, typename T>
 __device__ __forceinline__ void factors(const NormRope &a, const void *w, const Turn<IL> &t, T (&u)[8], T (&v)[8]) {
     float own[8], other[8];
@@ -210,9 +213,9 @@ __device__ __forceinline__ void factors(const NormRope &a, const void *w, const 
         weights_at(a, w, t.col >= a.rot ? 0 : t.col < half ? t.col + half : t.col - half, other);
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {  // (columns past the rotated ones: c = 1, s = 0; past the row's: x = 0)
+    for (int i = 0; i < 8; ++i) {  // (columns past the rotated ones: c = 1; past the row's: x = 0)
         u[i] = (T)own[i] * (T)t.c[i];
-        v[i] = (T)other[i] * (T)t.s[i];
+        v[i] = t.mask ? (T)other[i] * (T)t.s[i] : (T)-0.0f;
     }
 }
 
@@ -240,7 +243,7 @@ __device__ __forceinline__ void turn_row(const NormRope &a, const Raw<DT> &raw, 
                                          const double (&v)[8], float (&y)[8]) {
     float x[8], p[8];
     values<DT>(raw, x);
-    partners<DT, IL>(raw, t.from, p);
+    partners<DT, IL>(raw, t.from, t.mask, p);
     const double r = a.norm ? row_scale64<L>(a, x) : 1.0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -253,7 +256,7 @@ __device__ __forceinline__ void turn_row(const NormRope &a, const Raw<DT> &raw, 
                                          const float (&v)[8], float (&y)[8]) {
     float x[8], p[8];
     values<DT>(raw, x);
-    partners<DT, IL>(raw, t.from, p);
+    partners<DT, IL>(raw, t.from, t.mask, p);
     float r = 1.0f;
     const bool fits = !a.norm || row_scale32<L>(a, x, r);
 #pragma unroll
@@ -449,7 +452,7 @@ __global__ __launch_bounds__(256) void k_norm_rope_bwd(BwdArgs f) {
             float x[8], y[8], p[8], g[8];
             values<DT>(xw[j], x);
             values<DT>(yw[j], y);
-            partners<DT, IL>(yw[j], turn.from, p);
+            partners<DT, IL>(yw[j], turn.from, turn.mask, p);
 #pragma unroll
             for (int i = 0; i < 8; ++i) g[i] = __builtin_fmaf(-turn.s[i], p[i], y[i] * turn.c[i]);
             if (a.norm) {
