@@ -31,6 +31,14 @@ namespace {
 constexpr int FWD16 = 8, FWD32 = 4, FILL16 = 4, FILL32 = 2, BWD16 = 4, BWD32 = 2;
 constexpr int BWD_BLOCKS = 1024;  // workgroups of a backward at most: rows of partial weight gradients
 
+// A launch has fewer than 2^32 threads along x, and the largest calls more: workgroups lie in rows of 2^23 at most, numbered on.
+// The last row's surplus finds no token of its own.
+__device__ __forceinline__ uint32_t workgroup() { return blockIdx.y * gridDim.x + blockIdx.x; }
+dim3 grid_of(int64_t workgroups) {
+    const int64_t rows = (workgroups + (1 << 23) - 1) >> 23;
+    return dim3((unsigned)((workgroups + rows - 1) / rows), (unsigned)rows);
+}
+
 // x of another lane of the 16 that a DPP row is.
 template <int CTRL>
 __device__ __forceinline__ float lane_of(float x) {
@@ -286,8 +294,9 @@ template <int DT, int L, bool IL, int HP>
 __global__ __launch_bounds__(256) void k_norm_rope(FwdArgs f) {
     const NormRope &a = f.a;
     const int lane = threadIdx.x % L;
-    int run = blockIdx.x % (f.qc + f.kc);
-    const int64_t t = (int64_t)(blockIdx.x / (f.qc + f.kc)) * (256 / L) + threadIdx.x / L;
+    const uint32_t id = workgroup(), runs = f.qc + f.kc;
+    int run = (int)(id % runs);
+    const int64_t t = (int64_t)(id / runs) * (256 / L) + threadIdx.x / L;
     const int64_t tc = min(t, a.n - 1);  // lanes past the last token stay for the exchanges, with its data
     const bool isq = run < f.qc;
     const HeadRows in = isq ? a.q : a.k;
@@ -335,8 +344,9 @@ __global__ __launch_bounds__(256) void k_norm_rope_kv4(FillArgs f) {
     constexpr int L = D / 8;
     const NormRope &a = f.a;
     const int lane = threadIdx.x % L;
-    int run = blockIdx.x % (f.qc + f.kc);
-    const int64_t t = (int64_t)(blockIdx.x / (f.qc + f.kc)) * (256 / L) + threadIdx.x / L;
+    const uint32_t id = workgroup(), runs = f.qc + f.kc;
+    int run = (int)(id % runs);
+    const int64_t t = (int64_t)(id / runs) * (256 / L) + threadIdx.x / L;
     const int64_t tc = min(t, a.n - 1);
     const bool isq = run < f.qc;
     const HeadRows in = isq ? a.q : a.k;
@@ -583,7 +593,7 @@ hipError_t launch_norm_rope(const NormRope &a, void *qo, void *ko, hipStream_t s
     f.qc = (a.q.heads + hp - 1) / hp;
     f.kc = (a.k.heads + hp - 1) / hp;
     const int per = 256 / lanes_of(a.d);
-    const dim3 grid((unsigned)((a.n + per - 1) / per * (f.qc + f.kc)));
+    const dim3 grid = grid_of((a.n + per - 1) / per * (f.qc + f.kc));
     ROPE_DISPATCH(k_norm_rope, FWD16, FWD32, f);
     return hipGetLastError();
 }
@@ -602,7 +612,7 @@ hipError_t launch_norm_rope_kv4(const NormRope &a, const HeadRows &v, void *qo, 
     f.qc = (a.q.heads + hp - 1) / hp;
     f.kc = (a.k.heads + hp - 1) / hp;
     const int per = 256 / lanes_of(a.d);
-    const dim3 grid((unsigned)((a.n + per - 1) / per * (f.qc + f.kc)));
+    const dim3 grid = grid_of((a.n + per - 1) / per * (f.qc + f.kc));
 #define FILL_HP(DT, D, HP)                                                                                \
     do {                                                                                                  \
         if (a.interleaved) hipLaunchKernelGGL((k_norm_rope_kv4<DT, D, true, HP>), grid, dim3(256), 0, s, f); \
