@@ -1019,18 +1019,39 @@ int64_t turns_of(const DecArgs &p, int64_t groups, int64_t span, int64_t most, b
     return best;
 }
 
+// A decode call of 256 groups or more through a window with sinks, in a table at least twice as wide as that: most of its sequences
+// are past the window and alike long, so one split of four waves a group needs no join; past a span that grows with
+// the groups, four splits cost alike lengths 5 % at most and balance unlike ones, whose number a call does not know.
+// One split | four | as many as splits_of says | wide workgroups, us, sequences past the window; in brackets lengths of 32 to 131072
+// tokens, even in their logarithm; heads of 128:
+//    256 groups    2048: 17 | 22 | 22 | 20 (16 | 18 | 18 | 18)     8192: 61 | 62 | 63 | 67 (51 | 38 | 40 | 53)
+//    320           1024: 15 | 19 | 19 | 24 (14 | 17 | 17 | 19)     4096: 45 | 44 | 45 | 64 (38 | 29 | 30 | 36)
+//    512           8192: 108 | 113 | 117 | 127 (72 | 72 | 75 | 105)  16384: 201 | 210 | 224 | 233 (133 | 114 | 120 | 173)
+//   1024           8192: 205 | 220 | 232 | 246 (120 | 120 | 126 | 164)  32768: 787 | 798 | 887 | 865 (368 | 276 | 308 | 424)
+// heads of 64:
+//    256           1024: 10 | 13 | 13 | 9 (10 | 13 | 13 | 9)       4096: 24 | 21 | 22 | 18 (23 | 21 | 20 | 17)
+//    512           2048: 20 | 25 | 24 | 22 (18 | 23 | 23 | 21)     8192: 71 | 67 | 72 | 62 (59 | 49 | 50 | 55)
+// A batch of sequences shorter than the window is quickest with one split: 10 | 14 | 14 | 13 of 256 groups.
+int64_t sinks_splits(int64_t groups, int64_t span, int d, int64_t splits) {
+    const int64_t one = (groups > 256 && groups < 512 ? FAR * 5 / 2 : FAR * groups / 64) * d / 128;
+    return span <= one ? 1 : std::min<int64_t>(splits, 4);
+}
+
 // The rest of a call's plan: `groups` of rows, each over `span` tokens at most, of the `full` that the table's rows hold.
 // Returns about how many us it takes, launch and all (not of PLAIN's many-rows kernels): the decode kernel 6 and what
 // the bytes take, of the last-level cache where they are shared, 7.9 TB/s at heads of 128 and 5.8 at 64.
 float split(DecArgs &p, int64_t groups, int64_t span, int64_t full, int mode) {
     int64_t splits = splits_of(p, groups, span);
+    const int d = p.a.geo.d;
     float us = 0.0f;
     if (p.tr > 16) {
         if (mode == SINKS) splits = turns_of(p, groups, span, splits, false, us);  // (PLAIN's workspace)
         else if (mode != PLAIN) splits = turns_of(p, groups, span, 64, mode == PREFIX, us);
         us += 4.0f;
     } else {
-        if (mode == SINKS && groups >= 256 && 2 * span <= full) splits = 1;  // alike long, most of them: 45 -> 36 us, 64 x 2112 tokens
+        // (256 groups of heads of 64 are quicker in the wide workgroups)
+        const bool many = groups >= 256 && !(d == 64 && wide(groups, span));
+        if (mode == SINKS && many && 2 * span <= full) splits = sinks_splits(groups, span, d, splits);
         if (mode == OWN && groups >= 256 && span <= 2 * FAR) splits = 1;     // then no join, 12 us for 64 sequences of 8 heads
     }
     p.nw = p.tr == 16 && splits > 1 && wide(groups, span) ? WIDE : 4;
