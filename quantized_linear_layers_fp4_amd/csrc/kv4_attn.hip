@@ -1052,7 +1052,9 @@ float split(DecArgs &p, int64_t groups, int64_t span, int64_t full, int mode) {
         // (256 groups of heads of 64 are quicker in the wide workgroups)
         const bool many = groups >= 256 && !(d == 64 && wide(groups, span));
         if (mode == SINKS && many && 2 * span <= full) splits = sinks_splits(groups, span, d, splits);
-        if (mode == OWN && groups >= 256 && span <= 2 * FAR) splits = 1;     // then no join, 12 us for 64 sequences of 8 heads
+        // then no join.  One | many | wide, us: 64 sequences of 8 heads of 128 over 16384 shared tokens and up to 450 of their own
+        // 41 | 60 | 48, to 1900 52 | 71 | 65; 32 of them 31 | 45 | 32 and 38 | 51 | 38, at heads of 64 36 | 36 | 23 and 40 | 40 | 27
+        if (mode == OWN && many && span <= 2 * FAR) splits = 1;
     }
     p.nw = p.tr == 16 && splits > 1 && wide(groups, span) ? WIDE : 4;
     if (p.nw == WIDE) splits = 1;
