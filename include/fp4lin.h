@@ -436,7 +436,8 @@ fp4_status fp4_kv4_read(const uint8_t *cache, int64_t pages, int32_t page, int32
  * A query that sees no token gets zeros and lse = -infinity, and so does one of no sequence (before q_start[0] or
  * from q_start[b] on) and one past its sequence's first max_q.  Softmax statistics and sums are fp32; the
  * probabilities are rounded to bf16 (2^-8 of a term) for the product with the values, after their sum is taken.
- * Two calls on overlapping workspaces must be ordered.  Limits: max_q * (hq / hkv) < 2^24.
+ * Two calls on overlapping workspaces must be ordered.  Limits: max_q * (hq / hkv) < 2^24, width * page <= 2^30,
+ * b * hkv * ceil(max_q * (hq / hkv) / 16) < 2^22, nq * hq < 2^31.
  * Return FP4_OK or FP4_ERR_{NULL,SHAPE,DTYPE,WORKSPACE,ALIGN,DEVICE,HIP}. */
 size_t fp4_kv4_attention_workspace_bytes(int32_t b, int32_t max_q, int32_t hq, int32_t hkv, int32_t d, int32_t page,
                                          int32_t width);
@@ -460,7 +461,7 @@ fp4_status fp4_kv4_attention_sinks(const void *q, int64_t q_token_stride, int64_
  * sequences and each sequence's own tokens beside them (two parts), else once for each sequence (one part).  lens count the
  * shared tokens; a sequence may be shorter than they are.  Results are those of fp4_kv4_attention within the
  * roundings of its sums.
- * Further limit: nq * (hq / hkv) < 2^24.
+ * Further limits: nq * (hq / hkv) < 2^24, hkv * ceil(nq * (hq / hkv) / 16) < 2^22.
  *   workspace: at least fp4_kv4_attention_shared_workspace_bytes(...) bytes (0 for invalid arguments, or if none is needed).
  * fp4_kv4_attention_shared_parts (host-only): 1 or 2, as a call of these sizes is done; 0 for invalid arguments. */
 int32_t fp4_kv4_attention_shared_parts(int64_t nq, int32_t b, int32_t max_q, int32_t hq, int32_t hkv, int32_t d, int32_t page,
