@@ -515,7 +515,10 @@ fp4_status fp4_kv4_release(int32_t *table, int64_t table_stride, int32_t b, int3
  *      y = x / sqrt(mean(x^2) + eps) * w  over the d values of a row (eps = -1: y = x, and no weights), then
  *      (a, b) -> (a cos - b sin, b cos + a sin) for the pairs (i, i + rot / 2) of the first rot columns, or
  *      (2 i, 2 i + 1) if interleaved (rot = 0: none, and table and positions may be NULL)
- * computed in 64 bits and rounded to fp32, then to the type.  A row with a NaN or an infinity is NaN under the norm.
+ * Keys are computed in 64 bits and rounded to fp32, then to the type.  Queries are computed in fp32, within 16 * 2^-24 of
+ * the sum of their two terms' magnitudes, then rounded to the type (rows whose mean square + eps leaves 2^-80 .. 2^120 with
+ * r and the sums in 64 bits).  A row with a NaN or an infinity is NaN under the norm; without it such a value stays in its
+ * column, or in the two of its pair, as a weight's does.
  *   q, k      n x hq x d and n x hkv x d of dtype (fp32 or bf16), d contiguous, strides in elements, any element alignment;
  *             hkv = 0: no k.  d a multiple of 8 from 32 to 256, rot a multiple of 16 up to d
  *   q_weight, k_weight  d values of w_dtype, or NULL: ones
@@ -552,7 +555,8 @@ fp4_status fp4_kv4_norm_rope(uint8_t *cache, int64_t pages, int32_t page, const 
  *            overlapping the inputs
  *   q_weight_grad, k_weight_grad  fp32[d], summed in fp32 in an order that does not change, or NULL (not wanted)
  *   workspace: at least fp4_qk_norm_rope_backward_workspace_bytes(d) bytes if a weight's gradient is wanted.
- * Rows of a negative position add nothing and get zeros.
+ * Rows of a negative position add nothing and get zeros.  Computed in fp32: x's within 80 * 2^-24 * r (H + |x r| mean(H |x r|)),
+ * H being |w| times the magnitudes that g is the sum of, then the type's rounding.
  * Returns FP4_OK or FP4_ERR_{NULL,SHAPE,DTYPE,WORKSPACE,ALIGN,DEVICE,HIP}. */
 size_t fp4_qk_norm_rope_backward_workspace_bytes(int32_t d);
 fp4_status fp4_qk_norm_rope_backward(const void *dq, int64_t dq_token_stride, int64_t dq_head_stride, const void *dk,
