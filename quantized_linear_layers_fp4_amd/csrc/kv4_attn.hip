@@ -998,7 +998,7 @@ int64_t splits_of(const DecArgs &p, int64_t groups, int64_t span) {
 // at heads of 64, 1.6 and 2.4 with two at 128.  A turn of workgroups costs 5 us besides; partial results are written and
 // read at 4.8 TB/s; `always`: one split leaves them too, and otherwise more than one costs the join's launch.
 // Against the rule above, splits and us: 17 x 75 queries of 20 heads of 64 behind 4000 shared tokens 4 -> 5 and 101 -> 53 with
-// its join gone, 2 x 1000 of them through a window of 1500 2 -> 1 and 65 -> 55.
+// its join gone.  (2 x 1000 of them through a window of 1500 keep their two splits.)
 int64_t turns_of(const DecArgs &p, int64_t groups, int64_t span, int64_t most, bool always, float &us) {
     const int64_t tiles = (span + CT - 1) / CT;
     const bool wide_tile = p.tr == 256, small_head = p.a.geo.d == 64;

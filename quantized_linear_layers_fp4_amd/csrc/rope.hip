@@ -14,8 +14,8 @@
 // a sum: the fused write puts into the cache what the norm and kv4_write put there one after the other, bit for bit, and a
 // code of the cache next to a border is the right one.  Queries and gradients are made in fp32 (36.3 instead of
 // 39.8 us for the layer's forward below), but for rows whose mean square leaves 2^-80 .. 2^120.
-// A layer's forward (8192 tokens of 32 + 8 heads of 128, bf16: 168 MB) takes 36 us, 4.6 TB/s where a large copy reaches
-// 4.8; its gradients (252 MB) 53 and the weights' sums 3; 16384 tokens into the cache (353 MB) 81.
+// A layer's forward (8192 tokens of 32 + 8 heads of 128, bf16: 168 MB) takes 36.6 us, 4.6 TB/s where a large copy reaches
+// 4.8; its gradients (252 MB) 48 and the weights' sums 5; 16384 tokens into the cache (353 MB) 81 to 83.
 #include <algorithm>
 
 #include "block8.h"
